@@ -43,7 +43,7 @@ typedef enum {
   GPTQ_ENOTSPD = 4       /* the damped Hessian is not positive definite */
 } gptq_status;
 
-typedef enum { GPTQ_BF16 = 0, GPTQ_F32 = 1 } gptq_dtype;
+typedef enum { GPTQ_BF16 = 0, GPTQ_F32 = 1, GPTQ_I8 = 2 } gptq_dtype;
 
 /* hipStream_t, kept opaque so this header needs no HIP include. */
 typedef void* gptq_stream;
@@ -295,6 +295,98 @@ int gptq_quantize_layers(const void* const* W_list, const int64_t* d_out_list, i
 int gptq_w4a16_matmul(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
                       const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
                       int64_t d_in, int group_size, int sym, float* Y, gptq_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * The product above for a few tokens (generation: one row of X per sequence).
+ *
+ *   Y[i][n] = sum_k X[i][k] W_hat[n][k],   0 <= i < m <= GPTQ_MATVEC_MAX_M
+ *
+ * Arguments and layouts as gptq_w4a16_matmul, and
+ *   d_in        a multiple of 32 (GPTQ_EUNSUPPORTED otherwise).
+ *   m           0 .. GPTQ_MATVEC_MAX_M (0 is a no-op; more gives
+ *               GPTQ_EUNSUPPORTED: gptq_w4a16_matmul takes any m).
+ *   qweight     16-byte aligned.
+ * The weights are read once.  Per group, sum x q and sum x are formed with
+ * exact products and fp32 sums and joined as s (sum x q - z sum x); groups
+ * are added in fp32.  The order of every sum is fixed: the same inputs give
+ * the same bits, though not those of gptq_w4a16_matmul, which adds in another
+ * order.
+ * ------------------------------------------------------------------------- */
+#define GPTQ_MATVEC_MAX_M 64
+int gptq_w4a16_matvec(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
+                      const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
+                      int64_t d_in, int group_size, int sym, float* Y, gptq_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Residual addition, root-mean-square norm and an 8-bit output with a scale
+ * per row: what stands between two quantized layers of a block, writing the
+ * activations that gptq_w4a8_matmul reads (8 bits) or those that the W4A16
+ * products and gptq_hessian_accumulate read (bf16).
+ *
+ *   h    = x + r, formed in float32 and rounded once more to R's type
+ *          (R = NULL: h = x, not rounded); written to R_out
+ *   y_c  = h_c weight_c / sqrt(mean_c(h_c^2) + eps)
+ *   bf16 output: y rounded to bf16
+ *   8-bit output, with p_c = h_c weight_c and P = max_c |p_c|:
+ *     scale = max_c |y_c| / 127 (float32),
+ *     q_c   = rint(127 p_c / P), ties to even, -127 .. 127,
+ *     so that scale q_c stands for y_c; the quotient is decided as float64
+ *     division gives it, so the codes do not depend on the order in which the
+ *     mean square is summed.  A row with P = 0, or whose scale rounds to 0 in
+ *     float32, gets scale 1 and zero codes (the rule of a zero range in
+ *     gptq_quantize_layer).
+ * A row whose mean square plus eps is 0 gives zeros.
+ *
+ * X           [m x ldx] of x_dtype (bf16 or float32), row-major; columns
+ *             0..d-1 are used (so for R, R_out and out with their leading
+ *             dimensions).  A float32 X takes a product's Y as it is.
+ * R           [m x ldr] of r_dtype (bf16 or float32), or NULL: no residual
+ *             (r_dtype and ldr are then ignored).
+ * R_out       [m x ldro] of r_dtype out, or NULL: h is not stored.  R_out may
+ *             be R itself (with ldro = ldr): the residual is updated in
+ *             place.  Only with R.  No other overlap of outputs with inputs
+ *             or with each other is allowed.
+ * weight      [d] of w_dtype (bf16 or float32).
+ * eps         >= 0.
+ * out         [m x ldo] of out_dtype: GPTQ_I8 (int8_t) or GPTQ_BF16;
+ *             GPTQ_F32 gives GPTQ_EUNSUPPORTED.
+ * out_scales  [m] float32 out; with GPTQ_BF16 not written (may be NULL).
+ * m may be 0 (no-op); 1 <= d <= 65536, any value; no alignment beyond the
+ * elements' own is asked (rows that start on multiples of 16 bytes are read
+ * and written faster).  Columns past d of a row are left as they were.
+ * ------------------------------------------------------------------------- */
+int gptq_add_rmsnorm(const void* X, int x_dtype, int64_t ldx, const void* R, int r_dtype,
+                     int64_t ldr, void* R_out, int64_t ldro, const void* weight, int w_dtype,
+                     double eps, int64_t m, int64_t d, void* out, int out_dtype, int64_t ldo,
+                     float* out_scales, gptq_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Product of the packed 4-bit weights with 8-bit activations (W4A8).
+ *
+ *   Y[i][n] = x_scales[i] sum_k X[i][k] W_hat[n][k],
+ *   W_hat[n][k] = s[n][k/g] (q[n][k] - z[n][k/g])   (g = d_in when group_size = -1)
+ *
+ * X           [m x ldx] int8, row-major, d_in used columns (gptq_add_rmsnorm's
+ *             8-bit output); 16-byte aligned, ldx a multiple of 16.
+ * x_scales    [m] float32.
+ * qweight, scales_f16, zeros_f16, group_size, sym: as gptq_w4a16_matmul;
+ *             qweight 16-byte aligned.
+ * Y           [m x d_out] float32 out.
+ * d_in        a multiple of 32 (GPTQ_EUNSUPPORTED otherwise), <= 65536.
+ * m           0 (no-op) or more.
+ * ws          gptq_w4a8_workspace(m, d_out, d_in, group_size) bytes (0 for
+ *             most shapes); its contents on entry do not matter.
+ * A group's sum of x q and of x is exact (32-bit integers, at most 8192 terms
+ * before it is taken into float32, where it is exact too); with the integer
+ * zeros that gptq_pack writes sum x q - z sum x is exact as well, so only the
+ * scaling by s and x_scales and the addition of groups round, in float32.
+ * The order of those sums is fixed: the same inputs give the same bits.
+ * ------------------------------------------------------------------------- */
+int gptq_w4a8_matmul(const int8_t* X, const float* x_scales, int64_t m, int64_t ldx,
+                     const uint32_t* qweight, const uint16_t* scales_f16,
+                     const uint16_t* zeros_f16, int64_t d_out, int64_t d_in, int group_size,
+                     int sym, float* Y, void* ws, size_t ws_bytes, gptq_stream stream);
+size_t gptq_w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size);
 
 /* ---------------------------------------------------------------------------
  * Two-sided adaptive rounding.  "GPTQ-2D: 三次时间复杂度的双侧自适应舍入",

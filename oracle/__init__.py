@@ -22,6 +22,7 @@ from .storage import (bits_per_weight, model_gigabytes, round_half_up, pack_rows
 from .gptq2d_oracle import two_sided_quartic, two_sided_antidiagonal
 from .act_order import activation_order, gptq_ordered
 from .dequant_gemm import dequantize, dequant_matmul
+from .norm_quant import residual_sum, rms_norm, norm_codes, round_bf16
 
 __all__ = [
     "NotSPD", "hessian", "hessian_entry", "prepare", "reversed_route_U", "group_params",
@@ -29,5 +30,5 @@ __all__ = [
     "maxq_for", "bits_per_weight", "model_gigabytes", "round_half_up", "pack_rows",
     "unpack_rows", "words_per_row", "fp16_bits", "two_sided_quartic",
     "two_sided_antidiagonal", "activation_order", "gptq_ordered", "dequantize",
-    "dequant_matmul",
+    "dequant_matmul", "residual_sum", "rms_norm", "norm_codes", "round_bf16",
 ]

@@ -15,7 +15,8 @@ LIB_NAME = "libgptq_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["syrk.hip", "prepare.hip", "quant.hip", "gptq2d.hip", "act_order.hip",
-           "w4a16.hip", "gptq_abi.cpp"]
+           "w4a16.hip", "w4a16_vec.hip", "w4a8.hip", "add_rmsnorm.hip", "gptq_abi.cpp",
+           "serve_abi.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

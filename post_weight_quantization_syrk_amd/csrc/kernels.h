@@ -78,6 +78,24 @@ hipError_t w4a16_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* q
                         const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
                         int64_t d_in, int group_size, float* Y, hipStream_t stream);
 
+// ---- the same product for a few tokens (m <= 64) ---------------------------
+hipError_t w4a16_vec_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
+                            const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
+                            int64_t d_in, int group_size, float* Y, hipStream_t stream);
+
+// ---- residual addition, RMS norm, bf16 or 8-bit output ---------------------
+hipError_t add_rmsnorm_launch(const void* X, int x_dtype, int64_t ldx, const void* R, int r_dtype,
+                              int64_t ldr, void* R_out, int64_t ldro, const void* weight,
+                              int w_dtype, double eps, int64_t m, int64_t d, void* out,
+                              int out_dtype, int64_t ldo, float* out_scales, hipStream_t stream);
+
+// ---- product of 4-bit packed weights with 8-bit activations ----------------
+size_t w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size);
+hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_t ldx,
+                       const uint32_t* qweight, const uint16_t* scales_f16,
+                       const uint16_t* zeros_f16, int64_t d_out, int64_t d_in, int group_size,
+                       float* Y, void* ws, hipStream_t stream);
+
 // Polls a bounded wait between workgroups may take before it gives up
 // (environment GPTQ_SYNC_SPIN_LIMIT, default 2^20), read once per process.
 int64_t sync_spin_limit();

@@ -15,7 +15,8 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq_mi355x.so")
 
 GPTQ_OK, GPTQ_EINVAL, GPTQ_EUNSUPPORTED, GPTQ_EHIP, GPTQ_ENOTSPD = range(5)
-GPTQ_BF16, GPTQ_F32 = 0, 1
+GPTQ_BF16, GPTQ_F32, GPTQ_I8 = 0, 1, 2
+GPTQ_MATVEC_MAX_M = 64
 
 _lib = None
 
@@ -70,6 +71,11 @@ def lib() -> ctypes.CDLL:
         "gptq_pack": (I, [P, P, P, I64, I64, I, I, I, P, P, P, P]),
         "gptq2d_round": (I, [P, P, P, I64, P, P, SZ, P]),
         "gptq_w4a16_matmul": (I, [P, I64, I64, P, P, P, I64, I64, I, I, P, P]),
+        "gptq_w4a16_matvec": (I, [P, I64, I64, P, P, P, I64, I64, I, I, P, P]),
+        "gptq_w4a8_matmul": (I, [P, P, I64, I64, P, P, P, I64, I64, I, I, P, P, SZ, P]),
+        "gptq_w4a8_workspace": (SZ, [I64, I64, I64, I]),
+        "gptq_add_rmsnorm": (I, [P, I, I64, P, I, I64, P, I64, P, I, D, I64, I64, P, I, I64, P,
+                                 P]),
         "gptq_quantize_layers": (I, [P, P, I, I, I64, P, P, I, I, I, I, P, P, P, P, P, SZ, P]),
         "gptq_act_order": (I, [P, I, I64, I64, I64, P, P, P, SZ, P]),
         "gptq_act_order_workspace": (SZ, [I64, I64]),
@@ -427,3 +433,160 @@ def gptq_w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.
                                    _ptr(zeros_f16), d_out, d_in, group_size, int(bool(sym)),
                                    _ptr(Y), _stream(stream)), "gptq_w4a16_matmul")
     return Y
+
+
+# -------------------------------------------------- running a quantized layer
+_W16_TYPES = (torch.int16, torch.uint16, torch.float16)
+_W32_TYPES = (torch.int32, torch.uint32)
+
+
+def _call(where: str, args, device, stream):
+    """The library call, on the tensors' device and on one of its streams."""
+    if stream is None:
+        s = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
+    else:
+        s = stream
+    f = getattr(lib(), where)
+    if device.index == torch.cuda.current_device():
+        st = f(*args, s.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, s.cuda_stream)
+    if st != GPTQ_OK:
+        raise GPTQError(st, where)
+
+
+def _rows(where: str, name: str, t: torch.Tensor, shape, dtypes, device):
+    """Checks a row-major matrix and returns its leading dimension."""
+    if t.dim() != 2 or t.shape != shape or t.dtype not in dtypes:
+        raise ValueError(f"{where}: {name} must be {list(shape)} of {dtypes}, "
+                         f"got {list(t.shape)} {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{where}: {name} is on {t.device}, X on {device}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{where}: {name} must be row-major")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _flat(where: str, name: str, t: torch.Tensor, shape, dtypes, device):
+    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be contiguous {list(shape)} of {dtypes}, "
+                         f"got {list(t.shape)} {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{where}: {name} is on {t.device}, X on {device}")
+
+
+def _gpu_matrix(where: str, X: torch.Tensor, dtypes):
+    if X.dim() != 2 or X.dtype not in dtypes or not X.is_cuda:
+        raise ValueError(f"{where}: X must be a GPU matrix of {dtypes}, got {X.dim()}-D "
+                         f"{X.dtype} on {X.device}")
+    return X.device
+
+
+def _w4_checks(where, X, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream):
+    """The packed weights' shapes against X's; returns (d_out, ldx, Y).  A group
+    size that the library refuses is left to it: it reads nothing then."""
+    m, d_in = X.shape
+    dev = X.device
+    d_out = qweight.shape[0]
+    _flat(where, "qweight", qweight, (d_out, d_in // 8), _W32_TYPES, dev)
+    if group_size == -1 or (group_size > 0 and d_in % group_size == 0):
+        ng = n_groups_for(d_in, group_size)
+        _flat(where, "scales_f16", scales_f16, (d_out, ng), _W16_TYPES, dev)
+        if not sym:
+            if zeros_f16 is None:
+                raise ValueError(f"{where}: zeros_f16 is needed unless sym")
+            _flat(where, "zeros_f16", zeros_f16, (d_out, ng), _W16_TYPES, dev)
+    ldx = _rows(where, "X", X, (m, d_in), (X.dtype,), dev)
+    if Y is None:
+        Y = _empty(stream, (m, d_out), dtype=torch.float32, device=dev)
+    else:
+        _flat(where, "Y", Y, (m, d_out), (torch.float32,), dev)
+    return d_out, ldx, Y
+
+
+def gptq_w4a16_matvec(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.Tensor,
+                      zeros_f16: torch.Tensor | None, *, group_size: int, sym: bool,
+                      Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gptq_w4a16_matmul for the rows of a few tokens (m <= GPTQ_MATVEC_MAX_M), any d_in that is a
+    multiple of 32: Y [m, d_out] fp32 = X [m, d_in] bf16 times the dequantized weights transposed."""
+    where = "gptq_w4a16_matvec"
+    dev = _gpu_matrix(where, X, (torch.bfloat16,))
+    m, d_in = X.shape
+    d_out, ldx, Y = _w4_checks(where, X, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream)
+    _call(where, (X.data_ptr(), m, ldx, qweight.data_ptr(), scales_f16.data_ptr(),
+                  None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size, int(bool(sym)),
+                  Y.data_ptr()), dev, stream)
+    return Y
+
+
+def gptq_w4a8_workspace(m: int, d_out: int, d_in: int, group_size: int) -> int:
+    return int(lib().gptq_w4a8_workspace(m, d_out, d_in, group_size))
+
+
+def gptq_w4a8_matmul(X: torch.Tensor, x_scales: torch.Tensor, qweight: torch.Tensor,
+                     scales_f16: torch.Tensor, zeros_f16: torch.Tensor | None, *,
+                     group_size: int, sym: bool, Y: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y [m, d_out] fp32 = x_scales [m] times X [m, d_in] int8 (gptq_add_rmsnorm's 8-bit output)
+    times the dequantized 4-bit weights transposed."""
+    where = "gptq_w4a8_matmul"
+    dev = _gpu_matrix(where, X, (torch.int8,))
+    m, d_in = X.shape
+    d_out, ldx, Y = _w4_checks(where, X, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream)
+    _flat(where, "x_scales", x_scales, (m,), (torch.float32,), dev)
+    if ws is None:
+        ws = _workspace(gptq_w4a8_workspace(m, d_out, d_in, group_size), dev, stream)
+    elif ws.device != dev:
+        raise ValueError(f"{where}: ws is on {ws.device}, X on {dev}")
+    _call(where, (X.data_ptr(), x_scales.data_ptr(), m, ldx, qweight.data_ptr(),
+                  scales_f16.data_ptr(), None if sym else zeros_f16.data_ptr(), d_out, d_in,
+                  group_size, int(bool(sym)), Y.data_ptr(), None if ws is None else ws.data_ptr(),
+                  0 if ws is None else ws.numel() * ws.element_size()), dev, stream)
+    return Y
+
+
+def gptq_add_rmsnorm(X: torch.Tensor, weight: torch.Tensor, *,
+                     residual: torch.Tensor | None = None,
+                     residual_out: torch.Tensor | None = None, eps: float = 1e-6,
+                     out_dtype: torch.dtype = torch.int8, out: torch.Tensor | None = None,
+                     out_scales: torch.Tensor | None = None, stream=None):
+    """h = X + residual (X alone without one), then h weight / sqrt(mean h^2 + eps) per row, in
+    bf16 or as int8 codes with an fp32 scale per row.  Returns (out, out_scales or None,
+    residual_out or None); residual_out = residual updates the residual in place."""
+    where = "gptq_add_rmsnorm"
+    floats = (torch.bfloat16, torch.float32)
+    dev = _gpu_matrix(where, X, floats)
+    m, d = X.shape
+    if out_dtype not in (torch.int8, torch.bfloat16):
+        raise ValueError(f"{where}: out_dtype must be torch.int8 or torch.bfloat16")
+    i8 = out_dtype == torch.int8
+    ldx = _rows(where, "X", X, (m, d), floats, dev)
+    _flat(where, "weight", weight, (d,), floats, dev)
+    r_code, ldr, ldro = 0, 0, 0
+    if residual is not None:
+        ldr = _rows(where, "residual", residual, (m, d), floats, dev)
+        r_code = _dtype_code(residual)
+        if residual_out is None:
+            residual_out = _empty(stream, (m, d), dtype=residual.dtype, device=dev)
+        ldro = _rows(where, "residual_out", residual_out, (m, d), (residual.dtype,), dev)
+    elif residual_out is not None:
+        raise ValueError(f"{where}: residual_out without residual")
+    if out is None:
+        out = _empty(stream, (m, d), dtype=out_dtype, device=dev)
+    ldo = _rows(where, "out", out, (m, d), (out_dtype,), dev)
+    if not i8:
+        out_scales = None
+    elif out_scales is None:
+        out_scales = _empty(stream, m, dtype=torch.float32, device=dev)
+    else:
+        _flat(where, "out_scales", out_scales, (m,), (torch.float32,), dev)
+    _call(where, (X.data_ptr(), _dtype_code(X), ldx,
+                  None if residual is None else residual.data_ptr(), r_code, ldr,
+                  None if residual_out is None else residual_out.data_ptr(), ldro,
+                  weight.data_ptr(), _dtype_code(weight), float(eps), m, d, out.data_ptr(),
+                  GPTQ_I8 if i8 else GPTQ_BF16, ldo,
+                  out_scales.data_ptr() if i8 else None), dev, stream)
+    return out, out_scales, residual_out

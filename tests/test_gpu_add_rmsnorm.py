@@ -1,0 +1,237 @@
+"""GPU parity of the residual addition with the root-mean-square norm (gptq_add_rmsnorm)
+against the float64 oracle.
+
+Bars.  The residual sum is one float32 addition and one rounding to the residual's type:
+bit-exact.  The 8-bit codes are decided by the float64 quotient 127 p / max|p|, which involves
+no sum: exact.  The scale is formed in float64 (sums of d terms there err by d 2^-53 at most)
+and rounded once to float32: within 2^-24 (1 + 2^-10) relative.  The bf16 output is formed in
+float64, rounded to float32 and then to bf16: within (2^-8 + 2^-24 + 2^-34) |y|."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from post_weight_quantization_syrk_amd import gptq, synth
+from serve_util import DEV, U16, U32, replayed
+
+pytestmark = pytest.mark.gpu
+
+T = {"bf16": torch.bfloat16, "f32": torch.float32, "i8": torch.int8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a ROCm GPU")
+    gptq.lib()
+
+
+def values(rng, m, d, kind, scale=1.0):
+    x = rng.standard_normal((m, d), dtype=np.float32) * np.exp(
+        rng.standard_normal(d, dtype=np.float32)) * np.float32(scale)
+    return oracle.round_bf16(x) if kind == "bf16" else x
+
+
+def dev(a, kind, pad=0, skew=0):
+    """a [m, d] as a device matrix of `kind` with `pad` unused columns (NaN), its first element
+    `skew` elements into its buffer."""
+    m, d = a.shape
+    buf = torch.full((skew + m * (d + pad),), float("nan"), dtype=T[kind], device=DEV)
+    t = buf[skew:].as_strided((m, d), (d + pad, 1))
+    t.copy_(torch.from_numpy(np.ascontiguousarray(a)).to(DEV))
+    return t
+
+
+def out_buffer(m, d, kind, pad, skew):
+    buf = torch.full((skew + m * (d + pad) + 64,), 77, dtype=T[kind], device=DEV)
+    return buf, buf[skew:].as_strided((m, d), (d + pad, 1))
+
+
+def untouched(buf, view):
+    keep = torch.ones_like(buf, dtype=torch.bool)
+    keep.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(False)
+    return bool((buf[keep] == 77).all())
+
+
+def check(x, r, w, rk, eps, out_kind, out, scales, r_out):
+    h = oracle.residual_sum(x, r, rk)
+    if r is not None and r_out is not None:
+        np.testing.assert_array_equal(r_out.float().cpu().numpy(), h)
+    if out_kind == "i8":
+        q, s = oracle.norm_codes(h, w, eps)
+        np.testing.assert_array_equal(out.cpu().numpy(), q)
+        got = scales.cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - s) <= U32 * (1 + 2.0 ** -10) * s + 2.0 ** -149)
+    else:
+        y = oracle.rms_norm(h, w, eps)
+        got = out.float().cpu().numpy().astype(np.float64)
+        assert np.all(np.abs(got - y) <= (U16 + U32 + 2.0 ** -34) * np.abs(y) + 2.0 ** -133)
+
+
+CASES = [
+    # m, d, x, residual, weight, out, pad, skew
+    (1, 1, "f32", "f32", "f32", "i8", 0, 0),
+    (1, 1, "bf16", None, "bf16", "bf16", 0, 0),
+    (3, 2, "bf16", "bf16", "bf16", "i8", 3, 1),
+    (2, 7, "f32", "bf16", "f32", "bf16", 0, 0),
+    (5, 8, "bf16", "f32", "bf16", "i8", 0, 0),
+    (1, 63, "f32", None, "bf16", "i8", 0, 0),
+    (9, 64, "bf16", "bf16", "bf16", "i8", 0, 0),
+    (4, 100, "f32", "f32", "bf16", "bf16", 28, 0),
+    (33, 128, "bf16", "bf16", "f32", "i8", 8, 0),
+    (7, 255, "bf16", "bf16", "bf16", "bf16", 0, 0),
+    (6, 256, "f32", "bf16", "bf16", "i8", 0, 0),
+    (300, 256, "bf16", "bf16", "bf16", "i8", 0, 0),
+    (3, 512, "bf16", "bf16", "bf16", "i8", 0, 1),
+    (5, 520, "f32", "f32", "f32", "i8", 8, 0),
+    (2, 1000, "bf16", None, "bf16", "bf16", 0, 0),
+    (3, 1024, "bf16", "f32", "bf16", "bf16", 0, 0),
+    (11, 1528, "f32", "bf16", "bf16", "i8", 16, 0),
+    (2, 2047, "f32", "f32", "bf16", "i8", 0, 0),
+    (2, 2048, "f32", "f32", "bf16", "i8", 0, 0),
+    (1, 4096, "f32", "bf16", "bf16", "i8", 0, 0),
+    (17, 4096, "bf16", "bf16", "bf16", "bf16", 0, 0),
+    (3, 4104, "bf16", "bf16", "f32", "i8", 0, 0),
+    (4, 5003, "f32", "f32", "bf16", "i8", 0, 0),
+    (2, 8192, "bf16", "bf16", "bf16", "i8", 24, 0),
+    (2, 11008, "bf16", "f32", "bf16", "bf16", 0, 0),
+    (2, 11009, "bf16", "bf16", "bf16", "i8", 0, 0),
+    (2, 16384, "f32", "f32", "f32", "i8", 0, 0),
+    (2, 16392, "bf16", "bf16", "bf16", "i8", 0, 0),
+    (2, 32768, "bf16", "bf16", "bf16", "bf16", 0, 0),
+    (1, 32775, "f32", "bf16", "bf16", "i8", 0, 0),
+    (2, 65536, "f32", "f32", "bf16", "i8", 0, 0),
+    (1, 65535, "bf16", "bf16", "bf16", "bf16", 0, 0),
+]
+
+
+@pytest.mark.parametrize("m,d,xk,rk,wk,ok,pad,skew", CASES)
+def test_add_rmsnorm_matches_oracle(m, d, xk, rk, wk, ok, pad, skew):
+    print(f"[norm] m={m} d={d} x={xk} r={rk} w={wk} out={ok} pad={pad} skew={skew}", flush=True)
+    rng = np.random.default_rng([m, d, pad])
+    x = values(rng, m, d, xk, 0.3)
+    r = None if rk is None else values(rng, m, d, rk)
+    w = values(rng, 1, d, wk)[0]
+    X, W = dev(x, xk, pad, skew), dev(w[None], wk)[0]
+    R = None if rk is None else dev(r, rk, pad, skew)
+    obuf, out = out_buffer(m, d, ok, pad, skew)
+    sbuf = torch.full((m + 8,), 77.0, device=DEV)
+    rbuf, R_out = (None, None) if rk is None else out_buffer(m, d, rk, pad, skew)
+    o, s, h = gptq.gptq_add_rmsnorm(X, W, residual=R, residual_out=R_out, eps=1e-5,
+                                    out_dtype=T[ok], out=out, out_scales=sbuf[:m])
+    torch.cuda.synchronize()
+    check(x, r, w, rk, 1e-5, ok, o, s, h)
+    assert untouched(obuf, out) and (rk is None or untouched(rbuf, R_out))
+    assert bool((sbuf[m if ok == "i8" else 0:] == 77.0).all())
+    if rk is not None:  # in place, and without storing the sum: the same output
+        o2, s2, _ = gptq.gptq_add_rmsnorm(X, W, residual=R, residual_out=R, eps=1e-5,
+                                          out_dtype=T[ok])
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and (s is None or torch.equal(s, s2))
+        np.testing.assert_array_equal(R.float().cpu().numpy(), oracle.residual_sum(x, r, rk))
+
+
+def test_add_rmsnorm_residual_sum_not_stored():
+    rng = np.random.default_rng(2)
+    for d in (96, 97):
+        x, r, w = values(rng, 4, d, "f32"), values(rng, 4, d, "bf16"), values(rng, 1, d, "bf16")[0]
+        X, R, W = dev(x, "f32"), dev(r, "bf16"), dev(w[None], "bf16")[0]
+        out = torch.empty((4, d), dtype=torch.int8, device=DEV)
+        s = torch.empty(4, device=DEV)
+        L = gptq.lib()
+        st = L.gptq_add_rmsnorm(X.data_ptr(), gptq.GPTQ_F32, d, R.data_ptr(), gptq.GPTQ_BF16, d,
+                                None, 0, W.data_ptr(), gptq.GPTQ_BF16, 1e-5, 4, d, out.data_ptr(),
+                                gptq.GPTQ_I8, d, s.data_ptr(),
+                                torch.cuda.current_stream().cuda_stream)
+        assert st == gptq.GPTQ_OK
+        torch.cuda.synchronize()
+        check(x, r, w, "bf16", 1e-5, "i8", out, s, None)
+        np.testing.assert_array_equal(R.float().cpu().numpy(), r)
+
+
+@pytest.mark.parametrize("d", [96, 97, 1024, 3001])
+def test_add_rmsnorm_codes_at_exact_ties(d):
+    # p is a whole number of half steps of the row's grid: 127 p / P falls on k + 1/2 exactly
+    rng = np.random.default_rng(d)
+    k = rng.integers(-127, 128, size=(6, d)).astype(np.float32)
+    half = rng.integers(0, 2, size=(6, d)).astype(np.float32)
+    x = np.clip(2 * k + half, -254, 254)  # integers up to 254: exact in bf16 with 8 bits
+    x[:, 0] = 254.0
+    x = x * np.exp2(np.arange(6, dtype=np.float32) - 3)[:, None]
+    assert np.array_equal(oracle.round_bf16(x), x)
+    w = np.ones(d, dtype=np.float32)
+    X, W = dev(x, "bf16"), dev(w[None], "bf16")[0]
+    out, s, _ = gptq.gptq_add_rmsnorm(X, W, eps=1e-5)
+    check(x, None, w, None, 1e-5, "i8", out, s, None)
+    # and next to ties, in float32: one step of float32 to either side
+    xn = np.nextafter(x, rng.choice(np.array([-1e9, 1e9], dtype=np.float32), size=x.shape))
+    xn[:, 0] = x[:, 0]
+    out, s, _ = gptq.gptq_add_rmsnorm(dev(xn, "f32"), W, eps=1e-5)
+    check(xn, None, w, None, 1e-5, "i8", out, s, None)
+
+
+@pytest.mark.parametrize("d", [40, 41, 4096])
+def test_add_rmsnorm_rows_of_zeros_and_extreme_values(d):
+    rng = np.random.default_rng(d)
+    x = values(rng, 8, d, "f32")
+    x[0] = 0.0
+    x[1] *= np.float32(1e-30)   # squares underflow float32, not float64
+    x[2] *= np.float32(1e30)    # squares overflow float32, not float64
+    x[3] = 0.0
+    x[3, d // 2] = 1.0
+    x[4] = np.float32(1e-44)    # subnormal
+    x[5] *= np.float32(1e35)
+    x[6] = -x[6]
+    w = values(rng, 1, d, "bf16")[0]
+    X, W = dev(x, "f32"), dev(w[None], "bf16")[0]
+    for eps in (1e-5, 0.0):
+        out, s, _ = gptq.gptq_add_rmsnorm(X, W, eps=eps)
+        check(x, None, w, None, eps, "i8", out, s, None)
+        assert bool((out[0] == 0).all()) and float(s[0]) == 1.0
+        out, _, _ = gptq.gptq_add_rmsnorm(X, W, eps=eps, out_dtype=torch.bfloat16)
+        check(x, None, w, None, eps, "bf16", out, None, None)
+    # a weight of zeros: no code, scale 1
+    out, s, _ = gptq.gptq_add_rmsnorm(X, torch.zeros_like(W))
+    assert bool((out == 0).all()) and bool((s == 1.0).all())
+
+
+def test_add_rmsnorm_no_rows():
+    W = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+    out, s, _ = gptq.gptq_add_rmsnorm(torch.empty((0, 64), device=DEV), W)
+    assert out.shape == (0, 64) and s.shape == (0,)
+
+
+def test_add_rmsnorm_on_another_stream_and_replayed():
+    rng = np.random.default_rng(3)
+    x, r, w = values(rng, 50, 2048, "bf16"), values(rng, 50, 2048, "bf16"), values(rng, 1, 2048, "bf16")[0]
+    X, R, W = dev(x, "bf16"), dev(r, "bf16"), dev(w[None], "bf16")[0]
+    want, ws, wr = gptq.gptq_add_rmsnorm(X, W, residual=R)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = gptq.gptq_add_rmsnorm(X, W, residual=R, stream=side)
+    side.synchronize()
+    for a, b in zip(got, (want, ws, wr)):
+        assert torch.equal(a, b)
+    out, s, ro = torch.empty_like(want), torch.empty_like(ws), torch.empty_like(wr)
+    for y in replayed(lambda: gptq.gptq_add_rmsnorm(X, W, residual=R, residual_out=ro, out=out,
+                                                    out_scales=s), [out, s, ro]):
+        for a, b in zip(y, (want, ws, wr)):
+            assert torch.equal(a, b.cpu())
+
+
+@pytest.mark.parametrize("d", [520, 521])
+def test_add_rmsnorm_rows_past_two_gigabytes(d):
+    rng = np.random.default_rng(6)
+    ld, m = 1 << 29, 4
+    x, r, w = values(rng, m, d, "f32"), values(rng, m, d, "bf16"), values(rng, 1, d, "bf16")[0]
+    X = torch.empty((m - 1) * ld + d, dtype=torch.float32, device=DEV).as_strided((m, d), (ld, 1))
+    R = torch.empty((m - 1) * ld + d, dtype=torch.bfloat16, device=DEV).as_strided((m, d), (ld, 1))
+    out = torch.empty((m - 1) * 2 * ld + d, dtype=torch.int8, device=DEV).as_strided((m, d), (2 * ld, 1))
+    X.copy_(torch.from_numpy(x).to(DEV))
+    R.copy_(torch.from_numpy(r).to(DEV))
+    W = dev(w[None], "bf16")[0]
+    o, s, h = gptq.gptq_add_rmsnorm(X, W, residual=R, residual_out=R, eps=1e-5, out=out)
+    torch.cuda.synchronize()
+    check(x, r, w, "bf16", 1e-5, "i8", o, s, h)

@@ -1,0 +1,182 @@
+"""GPU parity of the product of 4-bit weights with 8-bit activations (gptq_w4a8_matmul)
+against the float64 oracle ("GPTQ：基于近似二阶信息的大模型权重量化", 阶段三; "GPTQ/AWQ量化中
+Group Size的精确含义与计算", 存储代价).
+
+Bar: the sums of x (q - z) over a group (or over a run of a long one) are exact integers, so
+only the products with s and x_scales and the addition of at most K / 32 such terms round:
+
+  |Y_gpu - Y_ref| <= (K / 32 + 4) u sum_k |x_k W_hat_nk| x_scale,   u = 2^-24."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from post_weight_quantization_syrk_amd import gptq
+from serve_util import DEV, U32, dev_weights, packed_weights, replayed
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a ROCm GPU")
+    gptq.lib()
+
+
+def make(m, d_in, d_out, g, sym, seed, ld=None):
+    _, qw, s16, z16 = packed_weights(d_in, d_out, g, seed)
+    rng = np.random.default_rng([seed, 1])
+    xi = np.full((m, ld or d_in), 113, dtype=np.int8)
+    xi[:, :d_in] = rng.integers(-128, 128, size=(m, d_in))
+    xs = np.exp(rng.uniform(-8.0, -1.0, size=m)).astype(np.float32)
+    X = torch.from_numpy(xi).to(DEV)[:, :d_in]
+    return X, torch.from_numpy(xs).to(DEV), xi[:, :d_in], xs, qw, s16, None if sym else z16
+
+
+def check(Y, xi, xs, qw, s16, z16, sym, g):
+    d_in = xi.shape[1]
+    x64 = xi.astype(np.float64) * xs.astype(np.float64)[:, None]
+    What = oracle.dequantize(qw, s16, z16, bits=4, group_size=g, sym=sym, d_in=d_in)
+    ref = x64 @ What.T
+    bound = (d_in / 32 + 4) * U32 * (np.abs(x64) @ np.abs(What).T)
+    err = np.abs(Y.cpu().numpy().astype(np.float64) - ref)
+    print(f"max err / bound {float((err / np.maximum(bound, 1e-300)).max()):.3e}", flush=True)
+    assert np.all(err <= bound)
+
+
+CASES = [
+    # m, d_in, d_out, g, sym, ldx
+    (1, 32, 1, 32, False, None),
+    (1, 32, 5, -1, False, None),
+    (1, 64, 16, 64, True, None),
+    (1, 96, 33, 32, False, None),
+    (1, 160, 17, -1, True, None),
+    (1, 256, 256, 128, False, None),
+    (2, 128, 31, 128, True, 144),
+    (3, 1056, 100, 32, True, 1072),
+    (4, 4096, 513, 128, False, None),
+    (7, 11008, 67, 64, False, None),
+    (8, 1312, 49, -1, True, None),
+    (16, 4096, 200, 128, False, 4112),
+    (17, 2208, 48, 32, False, None),
+    (31, 640, 127, 128, True, None),
+    (37, 11008, 131, 32, False, None),
+    (48, 4064, 40, -1, False, None),
+    (64, 8192, 96, 128, False, None),
+    (65, 192, 130, 64, False, None),
+    (64, 65536, 8, -1, False, None),
+    (1, 65536, 3, 32, False, None),
+    (100, 96, 70, 32, False, 112),
+    (127, 1024, 129, 128, False, None),
+    (128, 512, 128, 64, True, None),
+    (129, 416, 257, -1, False, 432),
+    (200, 512, 130, -1, False, None),
+    (257, 1056, 300, 32, True, None),
+    (300, 1152, 520, 128, False, 1168),
+    (515, 4096, 264, 64, True, None),
+    (1000, 224, 1030, 32, False, None),
+    (300, 65536, 136, -1, False, None),
+    (2049, 256, 2051, 128, False, None),
+]
+
+
+@pytest.mark.parametrize("m,d_in,d_out,g,sym,ld", CASES)
+def test_w4a8_matches_oracle(m, d_in, d_out, g, sym, ld):
+    print(f"[w4a8] m={m} d_in={d_in} d_out={d_out} g={g} sym={sym} ld={ld}", flush=True)
+    X, XS, xi, xs, qw, s16, z16 = make(m, d_in, d_out, g, sym, seed=m + d_in + d_out, ld=ld)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    Yg = torch.full((m * d_out + 64,), 77.0, dtype=torch.float32, device=DEV)
+    Y = Yg[:m * d_out].view(m, d_out)
+    gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=g, sym=sym, Y=Y)
+    torch.cuda.synchronize()
+    assert bool((Yg[m * d_out:] == 77.0).all())  # nothing behind the last row
+    check(Y, xi, xs, qw, s16, z16, sym, g)
+    again = gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=g, sym=sym)
+    assert torch.equal(Y, again)
+
+
+@pytest.mark.parametrize("m", [3, 150])
+@pytest.mark.parametrize("g,d_in", [(32, 352), (64, 320), (128, 384), (-1, 8224)])
+def test_w4a8_extreme_codes_are_exact(m, g, d_in):
+    # x = -128 or 127 throughout and codes 0 or 15 against zeros 15 or 0: the largest group sums,
+    # with scales that are powers of two every product is exact, and sums below 2^24 too
+    d_out = 33
+    ng = 1 if g == -1 else d_in // g
+    codes = np.zeros((d_out, d_in), dtype=np.uint8)
+    codes[1::2] = 15
+    zeros = np.where(np.arange(d_out)[:, None] % 2 == 1, 0.0, 15.0) * np.ones((d_out, ng))
+    qw, z16 = oracle.pack_rows(codes, 4), oracle.fp16_bits(zeros)
+    s16 = oracle.fp16_bits(np.full((d_out, ng), 0.25))
+    xi = np.full((m, d_in), -128, dtype=np.int8)
+    xi[1::2] = 127
+    Q, S, Z = dev_weights(qw, s16, z16)
+    Y = gptq.gptq_w4a8_matmul(torch.from_numpy(xi).to(DEV), torch.ones(m, device=DEV), Q, S, Z,
+                              group_size=g, sym=False)
+    ref = xi.astype(np.float64) @ oracle.dequantize(qw, s16, z16, bits=4, group_size=g, sym=False,
+                                                    d_in=d_in).T
+    assert np.abs(ref).max() * 4 < 2 ** 24
+    np.testing.assert_array_equal(Y.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("g,d_in", [(32, 256), (64, 320), (128, 256), (-1, 352)])
+def test_w4a8_identity_rows_give_w_hat(g, d_in):
+    d_out = 40
+    _, qw, s16, z16 = packed_weights(d_in, d_out, g, 5)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    eye = torch.eye(d_in, dtype=torch.int8, device=DEV)
+    What = oracle.dequantize(qw, s16, z16, bits=4, group_size=g, sym=False, d_in=d_in)
+    for rows in (d_in, 37):
+        Y = gptq.gptq_w4a8_matmul(eye[:rows], torch.ones(rows, device=DEV), Q, S, Z, group_size=g,
+                                  sym=False)
+        np.testing.assert_array_equal(Y.cpu().numpy(), What.T[:rows])
+
+
+def test_w4a8_no_tokens():
+    _, qw, s16, z16 = packed_weights(256, 24, 64, 9)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    Y = gptq.gptq_w4a8_matmul(torch.empty((0, 256), dtype=torch.int8, device=DEV),
+                              torch.empty(0, device=DEV), Q, S, Z, group_size=64, sym=False)
+    assert Y.shape == (0, 24)
+
+
+@pytest.mark.parametrize("m", [6, 90, 400])
+def test_w4a8_on_another_stream_and_replayed(m):
+    X, XS, xi, xs, qw, s16, z16 = make(m, 2048, 300, 64, False, seed=21)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    want = gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=64, sym=False)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=64, sym=False, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    Y = torch.empty_like(want)
+    for (y,) in replayed(
+            lambda: gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=64, sym=False, Y=Y), [Y]):
+        assert torch.equal(y, want.cpu())
+
+
+def test_w4a8_outputs_past_two_gigabytes():
+    # 70001 x 32769 fp32: offsets past 2^31 elements, sampled rows against the oracle
+    m, d_in, d_out, g = 70001, 32, 32769, 32
+    X, XS, xi, xs, qw, s16, z16 = make(m, d_in, d_out, g, False, seed=8)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    Y = gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=g, sym=False)
+    torch.cuda.synchronize()
+    for i in (0, 35000, 65535, 65536, 70000):
+        check(Y[i:i + 1], xi[i:i + 1], xs[i:i + 1], qw, s16, z16, False, g)
+
+
+@pytest.mark.parametrize("m", [3, 130])
+def test_w4a8_rows_of_x_past_two_gigabytes(m):
+    # a leading dimension of 2^30 / 2^25 bytes: the last rows start past 2^31
+    d_in, d_out, g = 160, 48, 32
+    ld = (1 << 30) if m == 3 else (1 << 25)
+    _, XS, xi, xs, qw, s16, z16 = make(m, d_in, d_out, g, False, seed=17)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    X = torch.empty((m - 1) * ld + d_in, dtype=torch.int8, device=DEV).as_strided((m, d_in), (ld, 1))
+    X.copy_(torch.from_numpy(xi.copy()).to(DEV))
+    check(gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=g, sym=False), xi, xs, qw, s16, z16,
+          False, g)
