@@ -30,7 +30,8 @@ FLAGS = [
 # Per-file additions.  The W4A16 product rescales its group accumulators with
 # plain VALU arithmetic; MFMA results kept in ordinary VGPRs spare the moves
 # to and from the accumulation registers around every rescale.
-FILE_FLAGS = {"w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+FILE_FLAGS = {"w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "w4a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str, verbose: bool) -> str:
