@@ -2,6 +2,7 @@
 //   Y[i][n] = sx[i] sum_k X[i][k] s[n][k/g] (q[n][k] - z[n][k/g])
 #include "common.h"
 #include "kernels.h"
+#include "w4_vec.h"
 
 #include <hip/hip_fp16.h>
 #include <algorithm>
@@ -14,6 +15,7 @@ typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(16))) int i32x16;
 
 constexpr int KCH = 128;           // k per chunk (bytes of a row of X, twice those of a weight row)
+constexpr int VEC_M = 64;          // up to here w4_vec.h's kernel
 constexpr int PANEL = 32 * KCH;    // bytes of a panel: 32 rows of one chunk
 
 // Where the product's tiles are in the workspace: X as panels of 32 rows by
@@ -309,6 +311,7 @@ void launch(const MulArgs& a, int G, hipStream_t stream) {
 }  // namespace
 
 size_t w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
+  if (m <= VEC_M) return 0;
   const Tile t = tile_for(m, d_out);
   return layout_of(m, d_out, d_in, group_size, 64 * t.mi, 64 * t.ni).bytes;
 }
@@ -317,6 +320,13 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
                        const uint32_t* qweight, const uint16_t* scales_f16,
                        const uint16_t* zeros_f16, int64_t d_out, int64_t d_in, int group_size,
                        float* Y, void* ws, hipStream_t stream) {
+  if (m <= VEC_M) {
+    w4vec::VecArgs v;
+    v.x = (const char*)X, v.sx = x_scales, v.q = qweight, v.s16 = scales_f16, v.z16 = zeros_f16;
+    v.y = Y, v.ldx = ldx, v.m = (int)m, v.n = (int)d_out, v.k = (int)d_in;
+    v.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
+    return w4vec::vec_launch<true>(v, group_size == -1 ? 0 : group_size, stream);
+  }
   const Tile t = tile_for(m, d_out);
   const Layout l = layout_of(m, d_out, d_in, group_size, 64 * t.mi, 64 * t.ni);
   const int64_t items = l.rows * l.nch * (KCH / 16) + (int64_t)l.ng * l.cols;
