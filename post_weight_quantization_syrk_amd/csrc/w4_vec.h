@@ -2,23 +2,23 @@
 // int8 activations, one kernel template for both.
 //   Y[i][n] = sx[i] sum_g s[n][g] (sum_{k in g} x q - z[n][g] sum_{k in g} x)
 //
-// A workgroup owns 16 R weight rows and all tokens; its waves take 256-byte
-// runs of k in turn and their sums meet in LDS at the end, in wave order.
-// Weights go from memory to registers, 16 bytes per lane: lane l holds 32
-// consecutive codes of row l % 16, and the four lanes of a row 64 bytes.
-// A matrix instruction wants, in lane quarter h, the h-th piece of one run of
-// k.  With groups of 128 (or one per row) the order of k inside a chunk is
-// free, so word j of every lane makes up instruction j; with groups of 32 or
-// 64 a 4 x 4 transposition of words between the quarters (four swaps for 32
-// codes) puts consecutive words side by side first.
-// The zero is not taken off the codes: x q and x are summed apart (the sum of
-// x by the same instruction against ones, shared by all rows), and joined per
-// group.
+// A workgroup owns 16 R weight rows and all tokens.  Its waves take blocks of
+// 512 k in turn, each with two buffers of its own in LDS, so that no wave
+// waits for another, and their sums meet at the end, in wave order.  A step is
+// 128 k: 64 bytes of each weight row and the tokens' pieces, loaded straight
+// into LDS with four neighbouring lanes on 64 consecutive bytes.  (Loaded into
+// registers as the matrix instructions want them, neighbouring lanes are in
+// different rows, and the vector cache takes one lane per cycle: measured 63
+// accesses per load, 26 us for 16 tokens through 11008 x 4096.)
+// For int8 X the zero is taken off the codes, four at a time.  For bf16 X that
+// would cost an operation per code: x q and x are summed apart (the sum of x by
+// the same instruction against ones, shared by all rows), and joined per group.
 #pragma once
 
 #include "common.h"
 
 #include <hip/hip_fp16.h>
+#include <type_traits>
 
 namespace gptq {
 namespace w4vec {
@@ -27,8 +27,6 @@ typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 
-constexpr int KCH = 128;
-constexpr int max_waves(int nt) { return nt == 1 ? 16 : 8; }
 
 struct VecArgs {
   const char* x;        // rows of X
@@ -39,7 +37,14 @@ struct VecArgs {
   float* y;
   int64_t ldx;          // bytes
   int m, n, k, ng;
+  int vec;              // scales (and zeros) that one aligned load may take: 1, 2, 4 or 8
 };
+
+// The most that divides a row of scales and its addresses.
+inline int scale_vec(const uint16_t* s16, const uint16_t* z16, int ng) {
+  const uintptr_t bits = (uintptr_t)s16 | (uintptr_t)z16 | (uintptr_t)(2 * ng);
+  return bits % 16 == 0 ? 8 : bits % 8 == 0 ? 4 : bits % 4 == 0 ? 2 : 1;
+}
 
 template <bool I8>
 struct Types;
@@ -85,83 +90,166 @@ __device__ __forceinline__ float half_bits(uint16_t b) {
   return __half2float(__ushort_as_half(b));
 }
 
+// A stored zero as the whole number it is.
+__device__ __forceinline__ int whole_zero(uint16_t b) {
+  return (int)fminf(fmaxf(rintf(half_bits(b)), -100.0f), 100.0f);
+}
+
+// The codes of a word minus their zero, as int8; bits 16..23 of sz hold 128 -
+// z.  A byte q + (128 - z) stays within 0..255 for |z| <= 100, so no carry
+// crosses bytes; flipping its top bit takes the 128 off again.
+__device__ __forceinline__ uint2 code_i8(uint32_t w, uint32_t sz) {
+  const uint32_t zc = __builtin_amdgcn_perm(sz, sz, 0x02020202u);
+  const uint2 b = code_bytes(w);
+  return make_uint2((b.x + zc) ^ 0x80808080u, (b.y + zc) ^ 0x80808080u);
+}
+
+constexpr int KCH = 128;   // k per step
+constexpr int KBLK = 512;  // k per block: whole scale runs for every group size
+
+// Direct global -> LDS load of 16 bytes per lane: lane l's bytes land at
+// lds + 16 l.  In asm, as the compiler would wait for every load in flight
+// before any LDS read; the loop waits by count itself.
+__device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
+  const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds);
+  __asm__ volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+                   :
+                   : "v"(p), "s"(lbase)
+                   : "memory", "m0");
+}
+
+template <bool I8, int NT, int R, int G>
+struct Shape {
+  static constexpr int XB = I8 ? 1 : 2;
+  static constexpr int WBYTES = 1024 * R;             // a step's words
+  static constexpr int XBYTES = 16 * NT * KCH * XB;   // a step's tokens
+  static constexpr int STAGE = WBYTES + XBYTES;
+  static constexpr int GPB = G == 0 ? 0 : KBLK / G;   // groups per block
+  static constexpr int SCBYTES = GPB * 16 * R * 4;    // scale and zero of each
+  static constexpr int WAVE = 2 * STAGE + SCBYTES;    // LDS of a wave
+  static constexpr int WAVES = 8 * WAVE <= 160 * 1024 ? 8 : 4;
+  static_assert(WAVES * WAVE <= 160 * 1024, "LDS");
+  static_assert(WAVE >= R * NT * 4 * 256, "the wave's sums reuse its buffers");
+};
+
 // I8: int8 X; NT: tiles of 16 tokens; R: tiles of 16 weight rows; G: group
-// size, 0 for one group per row; CPS: chunks of 128 k per step of a wave.
-template <bool I8, int NT, int R, int G, int CPS>
-__global__ __launch_bounds__(64 * max_waves(NT)) void w4_vec_kernel(VecArgs a) {
+// size, 0 for one group per row.
+template <bool I8, int NT, int R, int G>
+__global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kernel(VecArgs a) {
   typedef typename Types<I8>::acc_t acc_t;
+  typedef Shape<I8, NT, R, G> S;
   constexpr bool TR = G == 32 || G == 64;
-  constexpr int GPC = G == 0 ? 1 : KCH / G;          // groups per chunk
-  constexpr int XB = I8 ? 1 : 2;                     // bytes of an X element
-  extern __shared__ float red[];                     // [waves][R * NT * 4][64]
+  constexpr int GPC = G == 0 ? 1 : KCH / G;  // groups per step
+  constexpr int XB = S::XB;
+  constexpr int XD = NT * XB * 2;            // direct loads of a step's tokens
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
   const int l16 = lane & 15, h = lane >> 4;
   const int n0 = blockIdx.x * 16 * R;
   const int row_bytes = a.k / 2;
-  const int nst = (a.k + CPS * KCH - 1) / (CPS * KCH);
+  char* const mine = smem + wave * S::WAVE;
+  const uint32_t mine_off = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)mine;
+  uint32_t* const sc = (uint32_t*)(mine + 2 * S::STAGE);
 
+  // steps of this wave: blocks wave, wave + waves, ...; only the row's last
+  // block may hold fewer than four
+  const int nch = (a.k + KCH - 1) / KCH, nblk = (nch + 3) / 4;
+  const int nb = wave < nblk ? (nblk - 1 - wave) / waves + 1 : 0;
+  const bool has_last = nb > 0 && wave + waves * (nb - 1) == nblk - 1;
+  const int nst = 4 * nb - (has_last ? 4 * nblk - nch : 0);
+  auto chunk = [&](int i) __attribute__((always_inline)) { return 4 * (wave + waves * (i >> 2)) + (i & 3); };
+
+  // Direct loads.  Weights: 16 rows of 64 bytes, unit u of row r at u ^ (r / 4
+  // mod 4).  Tokens: rows of 128 XB bytes, unit u of token t at u ^ (t mod 16)
+  // (bf16) or u ^ (t / 2 mod 8).  Either way 16 lanes that read one unit of 16
+  // rows fall on different banks.
   const char* qrow[R];
-  int64_t srow[R];
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int64_t n = min(n0 + 16 * r + l16, a.n - 1);
-    qrow[r] = (const char*)a.q + n * row_bytes;
-    srow[r] = n * a.ng;
+  for (int r = 0; r < R; ++r)
+    qrow[r] = (const char*)a.q + (int64_t)min(n0 + 16 * r + (lane >> 2), a.n - 1) * row_bytes;
+  const int qu = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
+  const char* xrow[XD];
+  int xu[XD];
+#pragma unroll
+  for (int i = 0; i < XD; ++i) {
+    const int t = I8 ? 8 * i + (lane >> 3) : 4 * i + (lane >> 4);
+    xrow[i] = a.x + (int64_t)min(t, a.m - 1) * a.ldx;
+    xu[i] = 16 * (I8 ? (lane & 7) ^ ((t >> 1) & 7) : (lane & 15) ^ (t & 15));
   }
-  const char* xrow[NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) xrow[t] = a.x + (int64_t)min(16 * t + l16, a.m - 1) * a.ldx;
-
-  struct Step {
-    uint4 w[CPS][R];
-    uint32_t x[CPS][NT][I8 ? 8 : 16];  // 32 k of one token: four 8-k pieces
-    uint16_t s[CPS][R][GPC], z[CPS][R][GPC];
+  const int nx = I8 ? (a.m + 7) / 8 : (a.m + 3) / 4;  // loads of tokens that are there
+  auto wait_older = [&]() __attribute__((always_inline)) {
+    // all but the newest step's R + nx loads (or fewer: that waits longer)
+    if (nx == XD)
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(R + XD) : "memory");
+    else if (nx >= (XD + 1) / 2)
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(R + (XD + 1) / 2) : "memory");
+    else
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(R + 1) : "memory");
   };
-  auto load = [&](int st, Step& v) __attribute__((always_inline)) {
+  auto issue = [&](int i) __attribute__((always_inline)) {
+    const int c = chunk(i);
+    const uint32_t dst = mine_off + (i & 1) * S::STAGE;
 #pragma unroll
-    for (int cc = 0; cc < CPS; ++cc) {
-      const int c = st * CPS + cc;
+    for (int r = 0; r < R; ++r)
+      dma16_at(qrow[r] + min(c * (KCH / 2) + qu, row_bytes - 16), dst + 1024 * r);
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        v.w[cc][r] = *(const uint4*)(qrow[r] + min(c * (KCH / 2) + 16 * h, row_bytes - 16));
+    for (int j = 0; j < XD; ++j) {
+      // (whole loads past the last token are left out: their rows hold whatever
+      // is there, in sums that are not stored)
+      if (j < nx)
+        dma16_at(xrow[j] + min(c * KCH * XB + xu[j], a.k * XB - 16), dst + S::WBYTES + 1024 * j);
+    }
+  };
+  auto zero_bits = [](uint16_t z) __attribute__((always_inline)) {
+    return (uint32_t)(I8 ? 128 - whole_zero(z) : z);
+  };
+  // The scales and zeros of a block, side by side in LDS, V at a time per lane
+  // (a.vec: what their rows' alignment allows); neighbouring lanes take
+  // neighbouring pieces of a row.
+  auto scales_by = [&](int b, auto vec) __attribute__((always_inline)) {
+    constexpr int V = decltype(vec)::value, P = S::GPB / V;  // pieces per row
+    constexpr int LD = (16 * R * P + 63) / 64;
+    struct alignas(2 * V) Piece {
+      uint16_t v[V];
+    };
+    Piece s[LD], z[LD];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if constexpr (TR) {
+    for (int i = 0; i < LD; ++i) {
+      const int e = (64 * i + lane) & (16 * R * P - 1);
+      const int64_t o = (int64_t)min(n0 + e / P, a.n - 1) * a.ng + min(b * S::GPB + (e % P) * V, a.ng - V);
+      s[i] = *(const Piece*)(a.s16 + o);
+      if (a.z16) z[i] = *(const Piece*)(a.z16 + o);
+    }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = min(c * KCH + 32 * j + 8 * h, a.k - 8);
-            if constexpr (I8) {
-              const uint2 p = *(const uint2*)(xrow[t] + k);
-              v.x[cc][t][2 * j] = p.x, v.x[cc][t][2 * j + 1] = p.y;
-            } else {
-              const uint4 p = *(const uint4*)(xrow[t] + 2 * k);
-              v.x[cc][t][4 * j] = p.x, v.x[cc][t][4 * j + 1] = p.y;
-              v.x[cc][t][4 * j + 2] = p.z, v.x[cc][t][4 * j + 3] = p.w;
-            }
-          }
-        } else {
-          const char* p = xrow[t] + XB * min(c * KCH + 32 * h, a.k - 32);
+    for (int i = 0; i < LD; ++i) {
+      const int e = (64 * i + lane) & (16 * R * P - 1);
 #pragma unroll
-          for (int j = 0; j < 2 * XB; ++j) {
-            const uint4 u = *(const uint4*)(p + 16 * j);
-            v.x[cc][t][4 * j] = u.x, v.x[cc][t][4 * j + 1] = u.y;
-            v.x[cc][t][4 * j + 2] = u.z, v.x[cc][t][4 * j + 3] = u.w;
-          }
-        }
-      }
-      if constexpr (G != 0) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int g = 0; g < GPC; ++g) {
-            const int64_t i = srow[r] + min(c * GPC + g, a.ng - 1);
-            v.s[cc][r][g] = a.s16[i];
-            v.z[cc][r][g] = a.z16 ? a.z16[i] : (uint16_t)0x4800;  // 8
-          }
-      }
+      for (int v = 0; v < V; ++v)
+        sc[((e % P) * V + v) * 16 * R + e / P] =
+            s[i].v[v] | zero_bits(a.z16 ? z[i].v[v] : (uint16_t)0x4800) << 16;  // 8
+    }
+  };
+  auto scales = [&](int b) __attribute__((always_inline)) {
+    if constexpr (G != 0) {
+      if (S::GPB >= 8 && a.vec >= 8)
+        scales_by(b, std::integral_constant<int, S::GPB >= 8 ? 8 : 1>());
+      else if (a.vec >= 4)
+        scales_by(b, std::integral_constant<int, 4>());
+      else if (a.vec >= 2)
+        scales_by(b, std::integral_constant<int, 2>());
+      else
+        scales_by(b, std::integral_constant<int, 1>());
     }
   };
 
+  uint32_t row_sz[R];  // G == 0: the row's scale and zero, as in sc
+  if constexpr (G == 0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t n = min(n0 + 16 * r + l16, a.n - 1);
+      row_sz[r] = a.s16[n] | zero_bits(a.z16 ? a.z16[n] : (uint16_t)0x4800) << 16;
+    }
+  }
   float tot[R][NT][4];
   acc_t acc0[R][NT], one0[NT];  // G == 0: over the whole row
 #pragma unroll
@@ -174,169 +262,169 @@ __global__ __launch_bounds__(64 * max_waves(NT)) void w4_vec_kernel(VecArgs a) {
       for (int i = 0; i < 4; ++i) tot[r][t][i] = 0.0f;
     }
   }
-  // tot += s (acc - z one)
-  auto join = [&](float t, float s, uint16_t zb, auto acc, auto one) __attribute__((always_inline)) {
-    if constexpr (I8) {
-      const int z = (int)fminf(fmaxf(rintf(half_bits(zb)), -100.0f), 100.0f);
-      return fmaf(s, (float)(acc - __mul24(z, one)), t);
-    } else {
-      return fmaf(s, fmaf(-half_bits(zb), one, acc), t);
-    }
+  // tot += s acc, or s (acc - z one) where the zero is still in acc
+  auto join = [&](float t, uint32_t sz, auto acc, auto one) __attribute__((always_inline)) {
+    const float s = half_bits((uint16_t)sz);
+    if constexpr (I8)
+      return fmaf(s, (float)acc, t);
+    else
+      return fmaf(s, fmaf(-half_bits((uint16_t)(sz >> 16)), one, acc), t);
   };
 
-  auto compute = [&](int st, Step& v) __attribute__((always_inline)) {
+  auto compute = [&](int i) __attribute__((always_inline)) {
+    const int c = chunk(i);
+    const char* st = mine + (i & 1) * S::STAGE;
+    const char* xs = st + S::WBYTES;
+    const bool tail = (c + 1) * KCH > a.k;  // pieces past the row's end count as zeros
+    uint32_t w[R][4];
 #pragma unroll
-    for (int cc = 0; cc < CPS; ++cc) {
-      const int c = st * CPS + cc;
-      // pieces past the row's end count as zeros
+    for (int r = 0; r < R; ++r) {
+      const uint4 v = *(const uint4*)(st + 1024 * r + 64 * l16 + 16 * (h ^ ((l16 >> 2) & 3)));
+      w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+      if constexpr (TR) transpose4(w[r]);
+    }
+    acc_t one[NT], acc[R][NT];
+    auto sz_of = [&](int r, int g) __attribute__((always_inline)) {
+      if constexpr (G == 0)
+        return row_sz[r];
+      else
+        return sc[((i & 3) * GPC + g) * 16 * R + 16 * r + l16];
+    };
+    auto start = [&]() __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool in = c * KCH + 32 * (TR ? j : h) < a.k;
+      for (int t = 0; t < NT; ++t) {
+        one[t] = acc_t{0, 0, 0, 0};
+        if constexpr (G == 0) one[t] = one0[t];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int e = 0; e < (I8 ? 2 : 4); ++e)
-            v.x[cc][t][(I8 ? 2 : 4) * j + e] = in ? v.x[cc][t][(I8 ? 2 : 4) * j + e] : 0u;
+        for (int r = 0; r < R; ++r) {
+          acc[r][t] = acc_t{0, 0, 0, 0};
+          if constexpr (G == 0) acc[r][t] = acc0[r][t];
+        }
       }
-      uint32_t w[R][4];
+    };
+    auto finish = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        w[r][0] = v.w[cc][r].x, w[r][1] = v.w[cc][r].y, w[r][2] = v.w[cc][r].z,
-        w[r][3] = v.w[cc][r].w;
-        if constexpr (TR) transpose4(w[r]);
-      }
-      if constexpr (!I8) {
-        bf16x8 b[R][4];
-        const __bf16 o = (__bf16)1.0f;
-        const bf16x8 ones = {o, o, o, o, o, o, o, o};
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) b[r][j] = code_bf16(w[r][j]);
+        const uint32_t p = sz_of(r, g);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          bf16x8 x[4];
+          if constexpr (G == 0) {
+            acc0[r][t] = acc[r][t];
+            one0[t] = one[t];
+          } else {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) __builtin_memcpy(&x[j], &v.x[cc][t][4 * j], 16);
-#pragma unroll
-          for (int g = 0; g < GPC; ++g) {
-            acc_t one = {0, 0, 0, 0}, acc[R];
-            if constexpr (G == 0) one = one0[t];
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              acc[r] = acc_t{0, 0, 0, 0};
-              if constexpr (G == 0) acc[r] = acc0[r][t];
-            }
-#pragma unroll
-            for (int j = 4 * g / GPC; j < 4 * (g + 1) / GPC; ++j) {
-              one = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j], ones, one, 0, 0, 0);
-#pragma unroll
-              for (int r = 0; r < R; ++r)
-                acc[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[j], b[r][j], acc[r], 0, 0, 0);
-            }
-            if constexpr (G == 0) one0[t] = one;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              if constexpr (G == 0) {
-                acc0[r][t] = acc[r];
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  tot[r][t][i] = join(tot[r][t][i], half_bits(v.s[cc][r][g]), v.z[cc][r][g],
-                                      acc[r][i], one[i]);
-              }
-            }
+            for (int e = 0; e < 4; ++e)
+              tot[r][t][e] = join(tot[r][t][e], p, acc[r][t][e], one[t][e]);
           }
         }
-      } else {
-        uint2 b[R][4];
+      }
+    };
+    if constexpr (!I8) {
+      const __bf16 o = (__bf16)1.0f;
+      const bf16x8 ones = {o, o, o, o, o, o, o, o};
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+      for (int j = 0; j < 4; ++j) {
+        if (j % (4 / GPC) == 0) start();
+        bf16x8 b[R];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) b[r][j] = code_bytes(w[r][j]);
+        for (int r = 0; r < R; ++r) b[r] = code_bf16(w[r][j]);
+        const int u = TR ? 4 * j + h : 4 * h + j;  // 8 k of a token
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          const uint32_t* x = v.x[cc][t];
+          uint4 v = *(const uint4*)(xs + (16 * t + l16) * 256 + 16 * (u ^ l16));
+          if (tail && c * KCH + 8 * u >= a.k) v = make_uint4(0u, 0u, 0u, 0u);
+          bf16x8 x;
+          __builtin_memcpy(&x, &v, 16);
+          one[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, ones, one[t], 0, 0, 0);
 #pragma unroll
-          for (int g = 0; g < GPC; ++g) {
-            acc_t one = {0, 0, 0, 0}, acc[R];
-            if constexpr (G == 0) one = one0[t];
+          for (int r = 0; r < R; ++r)
+            acc[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x, b[r], acc[r][t], 0, 0, 0);
+        }
+        if ((j + 1) % (4 / GPC) == 0) finish(j * GPC / 4);
+      }
+    } else {
+      auto two = [](uint2 v) { return (long)(((uint64_t)v.y << 32) | v.x); };
+      auto piece = [&](int t, int k) __attribute__((always_inline)) {  // 8 k of a token
+        const int u = k >> 4;
+        uint2 v = *(const uint2*)(xs + (16 * t + l16) * 128 + 16 * (u ^ ((l16 >> 1) & 7)) + (k & 8));
+        if (tail && c * KCH + k >= a.k) v = make_uint2(0u, 0u);
+        return v;
+      };
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-              acc[r] = acc_t{0, 0, 0, 0};
-              if constexpr (G == 0) acc[r] = acc0[r][t];
-            }
-            if constexpr (G == 32) {
-              auto two = [](uint32_t lo, uint32_t hi) { return (long)(((uint64_t)hi << 32) | lo); };
-              const long xv = two(x[2 * g], x[2 * g + 1]);
-              one = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, 0x0101010101010101l, one, 0, 0, 0);
+      for (int j = 0; j < 2; ++j) {
+        if constexpr (G == 32) {
+#pragma unroll
+          for (int jj = 2 * j; jj < 2 * j + 2; ++jj) {
+            start();
+            long b[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) b[r] = two(code_i8(w[r][jj], sz_of(r, jj)));
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+              const long x = two(piece(t, 32 * jj + 8 * h));
 #pragma unroll
               for (int r = 0; r < R; ++r)
-                acc[r] = __builtin_amdgcn_mfma_i32_16x16x32_i8(xv, two(b[r][g].x, b[r][g].y),
-                                                               acc[r], 0, 0, 0);
-            } else {
-              const int o = 0x01010101;
-#pragma unroll
-              for (int j = 2 * g / GPC; j < 2 * (g + 1) / GPC; ++j) {
-                const i32x4 xv = {(int)x[4 * j], (int)x[4 * j + 1], (int)x[4 * j + 2],
-                                  (int)x[4 * j + 3]};
-                one = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv, i32x4{o, o, o, o}, one, 0, 0, 0);
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                  const i32x4 bv = {(int)b[r][2 * j].x, (int)b[r][2 * j].y,
-                                    (int)b[r][2 * j + 1].x, (int)b[r][2 * j + 1].y};
-                  acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(xv, bv, acc[r], 0, 0, 0);
-                }
-              }
+                acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x32_i8(x, b[r], acc[r][t], 0, 0, 0);
             }
-            if constexpr (G == 0) one0[t] = one;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              if constexpr (G == 0) {
-                acc0[r][t] = acc[r];
-              } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  tot[r][t][i] = join(tot[r][t][i], half_bits(v.s[cc][r][g]), v.z[cc][r][g],
-                                      acc[r][i], one[i]);
-              }
-            }
+            finish(jj);
           }
+        } else {
+          if (j % (2 / GPC) == 0) start();
+          i32x4 b[R];
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const uint32_t sz = sz_of(r, j * GPC / 2);
+            const uint2 p = code_i8(w[r][2 * j], sz), q = code_i8(w[r][2 * j + 1], sz);
+            b[r] = i32x4{(int)p.x, (int)p.y, (int)q.x, (int)q.y};
+          }
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const uint2 p = piece(t, TR ? 64 * j + 8 * h : 32 * h + 16 * j);
+            const uint2 q = piece(t, TR ? 64 * j + 32 + 8 * h : 32 * h + 16 * j + 8);
+            const i32x4 x = {(int)p.x, (int)p.y, (int)q.x, (int)q.y};
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+              acc[r][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, b[r], acc[r][t], 0, 0, 0);
+          }
+          if ((j + 1) % (2 / GPC) == 0) finish(j * GPC / 2);
         }
       }
     }
   };
 
-  Step cur, nxt;
-  if (wave < nst) load(wave, cur);
-  for (int st = wave; st < nst; st += waves) {
-    if (st + waves < nst) load(st + waves, nxt);
-    compute(st, cur);
-    cur = nxt;
+  if (nst > 0) issue(0);
+  for (int i = 0; i < nst; ++i) {
+    // every read of the other buffer has returned before it is written again
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if ((i & 3) == 0) scales(chunk(i) >> 2);
+    if (i + 1 < nst) {
+      issue(i + 1);
+      wait_older();
+    } else {
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    compute(i);
   }
   if constexpr (G == 0) {
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float s = half_bits(a.s16[srow[r]]);
-      const uint16_t z = a.z16 ? a.z16[srow[r]] : (uint16_t)0x4800;
+    for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tot[r][t][i] = join(0.0f, s, z, acc0[r][t][i], one0[t][i]);
-    }
+        for (int e = 0; e < 4; ++e) tot[r][t][e] = join(0.0f, row_sz[r], acc0[r][t][e], one0[t][e]);
   }
   constexpr int PER = R * NT * 4;
+  float* const out = (float*)mine;  // this wave's buffers are done with
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[(wave * PER + (r * NT + t) * 4 + i) * 64 + lane] = tot[r][t][i];
+      for (int e = 0; e < 4; ++e) out[((r * NT + t) * 4 + e) * 64 + lane] = tot[r][t][e];
   __syncthreads();
   for (int e = wave; e < PER; e += waves) {
     float v = 0.0f;
-    for (int w = 0; w < waves; ++w) v += red[(w * PER + e) * 64 + lane];
+    for (int w = 0; w < waves; ++w) v += ((const float*)(smem + w * S::WAVE))[e * 64 + lane];
     const int i = e & 3, t = (e >> 2) % NT, r = (e >> 2) / NT;
     const int token = 16 * t + 4 * h + i, n = n0 + 16 * r + l16;
     if (token < a.m && n < a.n) {
@@ -346,23 +434,14 @@ __global__ __launch_bounds__(64 * max_waves(NT)) void w4_vec_kernel(VecArgs a) {
   }
 }
 
-// Waves per workgroup: enough of them over the whole launch to keep the memory
-// busy, no more than there are steps.
-inline int vec_waves(int64_t groups, int steps, int most) {
-  int w = 4;
-  while (w < most && groups * w < 4096) w *= 2;
-  while (w > 1 && w > steps) w /= 2;
-  return w;
-}
-
 template <bool I8, int NT, int R, int G>
 hipError_t vec_launch_one(const VecArgs& a, hipStream_t stream) {
-  constexpr int CPS = NT == 1 && (I8 || G == 0 || G == 128) ? 2 : 1;
-  const int64_t groups = ceil_div(a.n, 16 * R);
-  const int waves = vec_waves(groups, (int)ceil_div(a.k, CPS * KCH), max_waves(NT));
-  const size_t lds = (size_t)waves * R * NT * 4 * 64 * sizeof(float);
-  hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G, CPS>), dim3((unsigned)groups), dim3(64 * waves),
-                     lds, stream, a);
+  typedef Shape<I8, NT, R, G> S;
+  int waves = 1;  // no more than there are blocks
+  while (waves < S::WAVES && waves * KBLK < a.k) waves *= 2;
+  const size_t lds = (size_t)waves * S::WAVE;
+  hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G>), dim3((unsigned)ceil_div(a.n, 16 * R)),
+                     dim3(64 * waves), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -376,11 +455,26 @@ hipError_t vec_launch_g(const VecArgs& a, int G, hipStream_t stream) {
   }
 }
 
+// Weight rows per workgroup.  More of them read X fewer times, fewer of them
+// use more CUs: 64 while that leaves some 160 workgroups (16 tokens through
+// 11008 x 4096: 11.6 us, against 14.4 and 16.6 us with 32 and 16), else 16
+// while they find room at once on 256 CUs (4096 x 4096: 5.8 us, against 6.7
+// and 8.9 us with 32 and 64), else 32 (37 tokens through 4099 x 11008 in 8
+// bits: 26 us, against 36 us with 16, whose 257th workgroup waits).
+template <bool I8, int NT>
+hipError_t vec_launch_t(const VecArgs& a, int G, hipStream_t stream) {
+  constexpr int RMAX = !I8 && NT > 2 ? 2 : 4;  // what fits LDS with four waves
+  if (a.n >= 160 * 64) return vec_launch_g<I8, NT, RMAX>(a, G, stream);
+  if (a.n <= 256 * 16) return vec_launch_g<I8, NT, 1>(a, G, stream);
+  return vec_launch_g<I8, NT, 2>(a, G, stream);
+}
+
 template <bool I8>
 hipError_t vec_launch(const VecArgs& a, int G, hipStream_t stream) {
-  if (a.m <= 16) return vec_launch_g<I8, 1, 1>(a, G, stream);
-  if (a.m <= 32) return vec_launch_g<I8, 2, 1>(a, G, stream);
-  return vec_launch_g<I8, 4, 1>(a, G, stream);
+  if (a.m <= 16) return vec_launch_t<I8, 1>(a, G, stream);
+  if (a.m <= 32) return vec_launch_t<I8, 2>(a, G, stream);
+  if (a.m <= 48) return vec_launch_t<I8, 3>(a, G, stream);
+  return vec_launch_t<I8, 4>(a, G, stream);
 }
 
 }  // namespace w4vec

@@ -1,6 +1,6 @@
 // The W4A16 product for a few tokens (m <= 64), X bf16.
 #include "kernels.h"
-#include "w4_vec.h"
+#include "w4_dot.h"
 
 namespace gptq {
 
@@ -11,7 +11,10 @@ hipError_t w4a16_vec_launch(const void* X, int64_t m, int64_t ldx, const uint32_
   a.x = (const char*)X, a.sx = nullptr, a.q = qweight, a.s16 = scales_f16, a.z16 = zeros_f16;
   a.y = Y, a.ldx = 2 * ldx, a.m = (int)m, a.n = (int)d_out, a.k = (int)d_in;
   a.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
-  return w4vec::vec_launch<false>(a, group_size == -1 ? 0 : group_size, stream);
+  a.vec = w4vec::scale_vec(scales_f16, zeros_f16, a.ng);
+  const int G = group_size == -1 ? 0 : group_size;
+  return w4vec::dot_takes(m, d_in) ? w4vec::dot_launch<false>(a, G, stream)
+                                        : w4vec::vec_launch<false>(a, G, stream);
 }
 
 }  // namespace gptq

@@ -2,7 +2,7 @@
 //   Y[i][n] = sx[i] sum_k X[i][k] s[n][k/g] (q[n][k] - z[n][k/g])
 #include "common.h"
 #include "kernels.h"
-#include "w4_vec.h"
+#include "w4_dot.h"
 
 #include <hip/hip_fp16.h>
 #include <algorithm>
@@ -325,7 +325,10 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
     v.x = (const char*)X, v.sx = x_scales, v.q = qweight, v.s16 = scales_f16, v.z16 = zeros_f16;
     v.y = Y, v.ldx = ldx, v.m = (int)m, v.n = (int)d_out, v.k = (int)d_in;
     v.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
-    return w4vec::vec_launch<true>(v, group_size == -1 ? 0 : group_size, stream);
+    v.vec = w4vec::scale_vec(scales_f16, zeros_f16, v.ng);
+    const int G = group_size == -1 ? 0 : group_size;
+    return w4vec::dot_takes(m, d_in) ? w4vec::dot_launch<true>(v, G, stream)
+                                          : w4vec::vec_launch<true>(v, G, stream);
   }
   const Tile t = tile_for(m, d_out);
   const Layout l = layout_of(m, d_out, d_in, group_size, 64 * t.mi, 64 * t.ni);
