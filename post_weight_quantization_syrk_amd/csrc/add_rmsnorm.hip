@@ -5,6 +5,12 @@
 //           scale = P / sqrt(mean h^2 + eps) / 127
 // The norm's own factor cancels in the codes, so they depend on no sum's
 // order; p is exact in float64 and the quotient is formed there.
+//
+// Bound by memory: x and r are read once, h and the output written once.  A
+// workgroup holds a row in registers between the one reduction (of sum h^2 and
+// max |p|, together) and the output.  The reductions are in float64: its
+// operations run at the rate of scalar float32 ones here and stay hidden
+// behind the loads, and squares neither overflow nor vanish.
 #include "common.h"
 #include "kernels.h"
 
@@ -15,88 +21,330 @@ namespace gptq {
 namespace {
 
 struct NormArgs {
-  const void* X;
-  const void* R;
-  void* R_out;
-  const void* weight;
-  void* out;
-  float* out_scales;
-  int64_t ldx, ldr, ldro, ldo;
+  const char* x;
+  const char* r;
+  char* r_out;
+  const char* w;
+  char* out;
+  float* scales;
+  int64_t ldx, ldr, ldro, ldo;  // elements
   double eps;
   int d;
-  int x_f32, r_f32, w_f32, out_i8;
+  int out_i8;
 };
 
-__device__ __forceinline__ uint16_t float_to_bf16_bits(float f) {
+constexpr int REG_D = 16384;  // longest row held in registers
+
+enum Kind { NONE, BF16, F32 };
+
+__device__ __forceinline__ uint32_t bf16_bits(float f) {
   const __bf16 b = (__bf16)f;  // nearest, ties to even
   uint16_t u;
   __builtin_memcpy(&u, &b, 2);
   return u;
 }
 
-__device__ __forceinline__ float load_as_float(const void* p, int64_t i, int f32) {
-  return f32 ? ((const float*)p)[i] : bf16_bits_to_float(((const uint16_t*)p)[i]);
+// v combined with a copy of itself whose lanes are moved by a DPP control.
+template <int CTRL, class F>
+__device__ __forceinline__ double dpp_fold(double v, F f) {
+  const int lo = __builtin_amdgcn_mov_dpp(__double2loint(v), CTRL, 0xF, 0xF, false);
+  const int hi = __builtin_amdgcn_mov_dpp(__double2hiint(v), CTRL, 0xF, 0xF, false);
+  return f(v, __hiloint2double(hi, lo));
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
+// f over the wave, in every lane.
+template <class F>
+__device__ __forceinline__ double wave_fold(double v, F f) {
+  v = dpp_fold<0x128>(v, f);  // row_ror:8, 4, 2, 1: over 16 lanes
+  v = dpp_fold<0x124>(v, f);
+  v = dpp_fold<0x122>(v, f);
+  v = dpp_fold<0x121>(v, f);
+  const auto lo16 = __builtin_amdgcn_permlane16_swap(__double2loint(v), __double2loint(v), false, false);
+  const auto hi16 = __builtin_amdgcn_permlane16_swap(__double2hiint(v), __double2hiint(v), false, false);
+  v = f(__hiloint2double(hi16[0], lo16[0]), __hiloint2double(hi16[1], lo16[1]));
+  const auto lo32 = __builtin_amdgcn_permlane32_swap(__double2loint(v), __double2loint(v), false, false);
+  const auto hi32 = __builtin_amdgcn_permlane32_swap(__double2hiint(v), __double2hiint(v), false, false);
+  return f(__hiloint2double(hi32[0], lo32[0]), __hiloint2double(hi32[1], lo32[1]));
+}
+
+// Sum of `sum` and maximum of `top` over the workgroup, in every thread; the
+// waves' parts are joined in wave order.
+__device__ __forceinline__ void fold_row(double& sum, double& top, double (*red)[16]) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = (int)blockDim.x >> 6;
+  sum = wave_fold(sum, [](double p, double q) { return p + q; });
+  top = wave_fold(top, [](double p, double q) { return fmax(p, q); });
+  if (waves > 1) {
+    if (lane == 0) red[0][wave] = sum, red[1][wave] = top;
+    __syncthreads();
+    sum = 0.0;
+    for (int i = 0; i < waves; ++i) {
+      sum += red[0][i];
+      top = fmax(top, red[1][i]);
+    }
+  }
+}
+
+// Eight elements of a row as they are in memory.  VEC: consecutive ones from
+// element 8 (v T + tid), as 16-byte loads; otherwise one in T, from element 8 v
+// T + tid, each on its own.
+template <Kind K>
+struct Raw {
+  uint32_t u[K == F32 ? 8 : 4];
+};
+
+template <Kind K, bool VEC>
+__device__ __forceinline__ void load8(const char* row, int v, int d, Raw<K>& o) {
+  const int T = blockDim.x, tid = threadIdx.x;
+  if constexpr (VEC) {
+    const int c = 8 * (v * T + tid);
+    const uint4* p = (const uint4*)(row + (int64_t)(c < d ? c : 0) * (K == F32 ? 4 : 2));
+    const uint4 a = p[0];
+    o.u[0] = a.x, o.u[1] = a.y, o.u[2] = a.z, o.u[3] = a.w;
+    if constexpr (K == F32) {
+      const uint4 b = p[1];
+      o.u[4] = b.x, o.u[5] = b.y, o.u[6] = b.z, o.u[7] = b.w;
+    }
+  } else {
 #pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+    for (int e = 0; e < 8; ++e) {
+      const int c = (8 * v + e) * T + tid, cc = c < d ? c : 0;
+      if constexpr (K == F32) {
+        o.u[e] = ((const uint32_t*)row)[cc];
+      } else {
+        const uint32_t b = ((const uint16_t*)row)[cc];
+        o.u[e / 2] = e & 1 ? o.u[e / 2] | b << 16 : b;
+      }
+    }
+  }
 }
 
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v = fmax(v, __shfl_xor(v, o));
-  return v;
+template <Kind K>
+__device__ __forceinline__ float element(const Raw<K>& o, int e) {
+  if constexpr (K == F32)
+    return __uint_as_float(o.u[e]);
+  else
+    return __uint_as_float(e & 1 ? o.u[e / 2] & 0xffff0000u : o.u[e / 2] << 16);
 }
 
-// One workgroup of 256 threads per row; h is formed twice.
-__global__ __launch_bounds__(256) void add_rmsnorm_kernel(NormArgs a) {
-  __shared__ double red[2][4];
+template <bool VEC>
+__device__ __forceinline__ int column(int v, int e) {
+  const int T = blockDim.x, tid = threadIdx.x;
+  return VEC ? 8 * (v * T + tid) + e : (8 * v + e) * T + tid;
+}
+
+// X, R, W: their types (R NONE: no residual); VPT: elements per thread / 8.
+template <Kind X, Kind R, Kind W, int VPT, bool VEC>
+__global__ __launch_bounds__((VPT == 4 ? 512 : 1024)) void add_rmsnorm_kernel(NormArgs a) {
+  __shared__ double red[2][16];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
-  auto h_at = [&](int c) {
-    float h = load_as_float(a.X, row * a.ldx + c, a.x_f32);
-    if (a.R) {
-      h += load_as_float(a.R, row * a.ldr + c, a.r_f32);
-      if (!a.r_f32) h = bf16_bits_to_float(float_to_bf16_bits(h));
+  const char* xp = a.x + row * a.ldx * (X == F32 ? 4 : 2);
+  float h[VPT][8];
+  Raw<W> w[VPT];
+  {
+    Raw<X> x[VPT];
+    Raw<R == NONE ? BF16 : R> r[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) load8<X, VEC>(xp, v, a.d, x[v]);
+    if constexpr (R != NONE) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) load8<R, VEC>(a.r + row * a.ldr * (R == F32 ? 4 : 2), v, a.d, r[v]);
+    }
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) load8<W, VEC>(a.w, v, a.d, w[v]);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float s = element(x[v], e);
+        if constexpr (R != NONE) s += element(r[v], e);
+        if constexpr (R == BF16) s = __uint_as_float(bf16_bits(s) << 16);
+        h[v][e] = column<VEC>(v, e) < a.d ? s : 0.0f;
+      }
+  }
+  if constexpr (R != NONE) {
+    if (a.r_out) {  // R_out may be R: these elements of it have been read
+      char* o = a.r_out + row * a.ldro * (R == F32 ? 4 : 2);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        if constexpr (VEC) {
+          const int c = column<VEC>(v, 0);
+          if (c < a.d) {
+            if constexpr (R == F32) {
+              ((float4*)(o + 4 * (int64_t)c))[0] = make_float4(h[v][0], h[v][1], h[v][2], h[v][3]);
+              ((float4*)(o + 4 * (int64_t)c))[1] = make_float4(h[v][4], h[v][5], h[v][6], h[v][7]);
+            } else {
+              uint32_t u[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                u[e] = __builtin_amdgcn_perm(__float_as_uint(h[v][2 * e + 1]),
+                                             __float_as_uint(h[v][2 * e]), 0x07060302u);
+              *(uint4*)(o + 2 * (int64_t)c) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int c = column<VEC>(v, e);
+            if (c < a.d) {
+              if constexpr (R == F32)
+                ((float*)o)[c] = h[v][e];
+              else
+                ((uint16_t*)o)[c] = (uint16_t)(__float_as_uint(h[v][e]) >> 16);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  double sum = 0.0, top = 0.0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double hd = (double)h[v][e];
+      sum = fma(hd, hd, sum);
+      top = fmax(top, fabs(hd * (double)element(w[v], e)));
+    }
+  fold_row(sum, top, red);
+  const double ms = sum / a.d + a.eps;
+  const double rstd = ms > 0.0 ? 1.0 / sqrt(ms) : 0.0;
+
+  if (!a.out_i8) {
+    uint16_t* o = (uint16_t*)a.out + row * a.ldo;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      uint32_t b[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        b[e] = bf16_bits((float)((double)h[v][e] * (double)element(w[v], e) * rstd));
+      if constexpr (VEC) {
+        const int c = column<VEC>(v, 0);
+        if (c < a.d)
+          *(uint4*)(o + c) = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16,
+                                        b[6] | b[7] << 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = column<VEC>(v, e);
+          if (c < a.d) o[c] = (uint16_t)b[e];
+        }
+      }
+    }
+    return;
+  }
+  const float scale = (float)(top * rstd / 127.0);
+  const bool empty = scale == 0.0f;
+  if (tid == 0) a.scales[row] = empty ? 1.0f : scale;
+  // A code from float32: h w, 127 / P and their product are off by half a step
+  // each, so t by less than 127 * 3 * 2^-24 < 2^-15, and unless t is that close
+  // to a border its nearest integer is the code.  Otherwise, and where float32
+  // could overflow or go subnormal, the float64 quotient decides.
+  const float c127 = (float)(127.0 / top);
+  const bool plain = top > 1e-25 && top < 1e30;
+  int8_t* o = (int8_t*)a.out + row * a.ldo;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    int q[8];
+    bool near = !plain;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float t = h[v][e] * element(w[v], e) * c127, k = rintf(t);
+      near |= fabsf(fabsf(t - k) - 0.5f) <= 3.0517578125e-05f;
+      q[e] = (int)k;
+    }
+    if (near) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        q[e] = empty ? 0 : (int)rint(127.0 * ((double)h[v][e] * (double)element(w[v], e)) / top);
+    }
+    if constexpr (VEC) {
+      const int c = column<VEC>(v, 0);
+      uint32_t b[2] = {0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e / 4] |= ((uint32_t)q[e] & 0xffu) << (8 * (e & 3));
+      if (c < a.d) *(uint2*)(o + c) = make_uint2(b[0], b[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = column<VEC>(v, e);
+        if (c < a.d) o[c] = (int8_t)q[e];
+      }
+    }
+  }
+}
+
+// Rows longer than REG_D: h is formed twice, from x and r again.
+__global__ __launch_bounds__(1024) void add_rmsnorm_long_kernel(NormArgs a, int x_f32, int r_f32,
+                                                                int w_f32) {
+  __shared__ double red[2][16];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  auto load = [](const char* p, int64_t i, int f32) __attribute__((always_inline)) {
+    return f32 ? ((const float*)p)[i] : bf16_bits_to_float(((const uint16_t*)p)[i]);
+  };
+  auto h_at = [&](int c) __attribute__((always_inline)) {
+    float h = load(a.x, row * a.ldx + c, x_f32);
+    if (a.r) {
+      h += load(a.r, row * a.ldr + c, r_f32);
+      if (!r_f32) h = __uint_as_float(bf16_bits(h) << 16);
     }
     return h;
   };
   double sum = 0.0, top = 0.0;
-  for (int c = tid; c < a.d; c += 256) {
-    const float h = h_at(c);
-    sum += (double)h * (double)h;
-    top = fmax(top, fabs((double)h * (double)load_as_float(a.weight, c, a.w_f32)));
+  for (int c = tid; c < a.d; c += 1024) {
+    const double hd = (double)h_at(c);
+    sum = fma(hd, hd, sum);
+    top = fmax(top, fabs(hd * (double)load(a.w, c, w_f32)));
   }
-  sum = wave_sum(sum);
-  top = wave_max(top);
-  if ((tid & 63) == 0) {
-    red[0][tid >> 6] = sum;
-    red[1][tid >> 6] = top;
-  }
-  __syncthreads();
-  sum = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
-  top = fmax(fmax(red[1][0], red[1][1]), fmax(red[1][2], red[1][3]));
+  fold_row(sum, top, red);
   const double ms = sum / a.d + a.eps;
   const double rstd = ms > 0.0 ? 1.0 / sqrt(ms) : 0.0;
   const float scale = (float)(top * rstd / 127.0);
   const bool empty = scale == 0.0f;
-  if (a.out_i8 && tid == 0) a.out_scales[row] = empty ? 1.0f : scale;
-  for (int c = tid; c < a.d; c += 256) {
+  if (a.out_i8 && tid == 0) a.scales[row] = empty ? 1.0f : scale;
+  for (int c = tid; c < a.d; c += 1024) {
     const float h = h_at(c);
-    const double p = (double)h * (double)load_as_float(a.weight, c, a.w_f32);
-    if (a.R_out) {  // after h is read: R_out may be R
-      if (a.r_f32)
-        ((float*)a.R_out)[row * a.ldro + c] = h;
+    const double p = (double)h * (double)load(a.w, c, w_f32);
+    if (a.r_out) {  // R_out may be R: this element of it has been read
+      if (r_f32)
+        ((float*)a.r_out)[row * a.ldro + c] = h;
       else
-        ((uint16_t*)a.R_out)[row * a.ldro + c] = float_to_bf16_bits(h);
+        ((uint16_t*)a.r_out)[row * a.ldro + c] = (uint16_t)(__float_as_uint(h) >> 16);
     }
     if (a.out_i8)
       ((int8_t*)a.out)[row * a.ldo + c] = empty ? 0 : (int8_t)(int)rint(127.0 * p / top);
     else
-      ((uint16_t*)a.out)[row * a.ldo + c] = float_to_bf16_bits((float)(p * rstd));
+      ((uint16_t*)a.out)[row * a.ldo + c] = (uint16_t)bf16_bits((float)(p * rstd));
   }
+}
+
+template <Kind X, Kind R, Kind W, int VPT>
+void launch(const NormArgs& a, int64_t m, int threads, bool vec, hipStream_t stream) {
+  if (vec)
+    hipLaunchKernelGGL((add_rmsnorm_kernel<X, R, W, VPT, true>), dim3((unsigned)m), dim3(threads),
+                       0, stream, a);
+  else
+    hipLaunchKernelGGL((add_rmsnorm_kernel<X, R, W, VPT, false>), dim3((unsigned)m), dim3(threads),
+                       0, stream, a);
+}
+
+template <Kind X, Kind R, Kind W>
+void launch_sized(const NormArgs& a, int64_t m, bool vec, hipStream_t stream) {
+  const bool many = m >= 1024;
+  const int vpt = many ? (a.d <= 2048 ? 1 : a.d <= 4096 ? 2 : 4) : (a.d <= 8192 ? 1 : 2);
+  const int threads = 64 * (int)ceil_div(a.d, 64 * 8 * vpt);
+  switch (vpt) {
+    case 1: launch<X, R, W, 1>(a, m, threads, vec, stream); break;
+    case 2: launch<X, R, W, 2>(a, m, threads, vec, stream); break;
+    default: launch<X, R, W, 4>(a, m, threads, vec, stream);
+  }
+}
+
+template <Kind X, Kind R>
+void launch_w(const NormArgs& a, int64_t m, bool w_f32, bool vec, hipStream_t stream) {
+  w_f32 ? launch_sized<X, R, F32>(a, m, vec, stream) : launch_sized<X, R, BF16>(a, m, vec, stream);
 }
 
 }  // namespace
@@ -106,11 +354,27 @@ hipError_t add_rmsnorm_launch(const void* X, int x_dtype, int64_t ldx, const voi
                               int w_dtype, double eps, int64_t m, int64_t d, void* out,
                               int out_dtype, int64_t ldo, float* out_scales, hipStream_t stream) {
   NormArgs a;
-  a.X = X, a.R = R, a.R_out = R_out, a.weight = weight, a.out = out, a.out_scales = out_scales;
-  a.ldx = ldx, a.ldr = ldr, a.ldro = ldro, a.ldo = ldo, a.eps = eps, a.d = (int)d;
-  a.x_f32 = x_dtype == GPTQ_F32, a.r_f32 = r_dtype == GPTQ_F32, a.w_f32 = w_dtype == GPTQ_F32;
-  a.out_i8 = out_dtype == GPTQ_I8;
-  hipLaunchKernelGGL(add_rmsnorm_kernel, dim3((unsigned)m), dim3(256), 0, stream, a);
+  a.x = (const char*)X, a.r = (const char*)R, a.r_out = (char*)R_out, a.w = (const char*)weight;
+  a.out = (char*)out, a.scales = out_scales, a.ldx = ldx, a.ldr = ldr, a.ldro = ldro, a.ldo = ldo;
+  a.eps = eps, a.d = (int)d, a.out_i8 = out_dtype == GPTQ_I8;
+  const bool xf = x_dtype == GPTQ_F32, rf = r_dtype == GPTQ_F32, wf = w_dtype == GPTQ_F32;
+  // 16-byte pieces: every row starts on one, and the row is whole eights
+  auto rows16 = [&](const void* p, int64_t ld, int size) {
+    return (uintptr_t)p % 16 == 0 && (m == 1 || ld * size % 16 == 0);
+  };
+  const bool vec = d % 8 == 0 && rows16(X, ldx, xf ? 4 : 2) && (uintptr_t)weight % 16 == 0 &&
+                   (!R || rows16(R, ldr, rf ? 4 : 2)) && (!R_out || rows16(R_out, ldro, rf ? 4 : 2)) &&
+                   (a.out_i8 ? (uintptr_t)out % 8 == 0 && (m == 1 || ldo % 8 == 0)
+                             : rows16(out, ldo, 2));
+  if (d > REG_D)
+    hipLaunchKernelGGL(add_rmsnorm_long_kernel, dim3((unsigned)m), dim3(1024), 0, stream, a, xf, rf,
+                       wf);
+  else if (!R)
+    xf ? launch_w<F32, NONE>(a, m, wf, vec, stream) : launch_w<BF16, NONE>(a, m, wf, vec, stream);
+  else if (rf)
+    xf ? launch_w<F32, F32>(a, m, wf, vec, stream) : launch_w<BF16, F32>(a, m, wf, vec, stream);
+  else
+    xf ? launch_w<F32, BF16>(a, m, wf, vec, stream) : launch_w<BF16, BF16>(a, m, wf, vec, stream);
   return hipGetLastError();
 }
 
