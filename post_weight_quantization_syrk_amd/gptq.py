@@ -8,6 +8,7 @@ caller does not pass in are allocated here with torch.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -436,75 +437,78 @@ def gptq_w4a16_matmul(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.
 
 
 # -------------------------------------------------- running a quantized layer
+# These calls take microseconds on the GPU, so the checks below are written to
+# cost little: one condition on the way through, and the words only on the way
+# out.  Devices are compared as indices (-1 for the host).
 _W16_TYPES = (torch.int16, torch.uint16, torch.float16)
 _W32_TYPES = (torch.int32, torch.uint32)
+_FLOATS = (torch.bfloat16, torch.float32)
 
 
-def _call(where: str, args, device, stream):
+def _call(where: str, index: int, stream, *args):
     """The library call, on the tensors' device and on one of its streams."""
     if stream is None:
-        s = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on {device}")
+        raw = torch._C._cuda_getCurrentRawStream(index)  # current_stream() without its object
+    elif stream.device.index != index:
+        raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on GPU {index}")
     else:
-        s = stream
+        raw = stream.cuda_stream
     f = getattr(lib(), where)
-    if device.index == torch.cuda.current_device():
-        st = f(*args, s.cuda_stream)
+    if index == torch._C._cuda_getDevice():
+        st = f(*args, raw)
     else:
-        with torch.cuda.device(device):
-            st = f(*args, s.cuda_stream)
+        with torch.cuda.device(index):
+            st = f(*args, raw)
     if st != GPTQ_OK:
         raise GPTQError(st, where)
 
 
-def _rows(where: str, name: str, t: torch.Tensor, shape, dtypes, device):
-    """Checks a row-major matrix and returns its leading dimension."""
-    if t.dim() != 2 or t.shape != shape or t.dtype not in dtypes:
-        raise ValueError(f"{where}: {name} must be {list(shape)} of {dtypes}, "
-                         f"got {list(t.shape)} {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{where}: {name} is on {t.device}, X on {device}")
-    if shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{where}: {name} must be row-major")
-    return t.stride(0) if shape[0] > 1 else shape[1]
-
-
-def _flat(where: str, name: str, t: torch.Tensor, shape, dtypes, device):
-    if t.shape != shape or t.dtype not in dtypes or not t.is_contiguous():
-        raise ValueError(f"{where}: {name} must be contiguous {list(shape)} of {dtypes}, "
-                         f"got {list(t.shape)} {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{where}: {name} is on {t.device}, X on {device}")
-
-
-def _gpu_matrix(where: str, X: torch.Tensor, dtypes):
+def _index(where: str, X: torch.Tensor, dtypes) -> int:
+    """The GPU that the matrix X is on."""
     if X.dim() != 2 or X.dtype not in dtypes or not X.is_cuda:
         raise ValueError(f"{where}: X must be a GPU matrix of {dtypes}, got {X.dim()}-D "
                          f"{X.dtype} on {X.device}")
-    return X.device
+    return X.get_device()
 
 
-def _w4_checks(where, X, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream):
-    """The packed weights' shapes against X's; returns (d_out, ldx, Y).  A group
+def _rows(where: str, name: str, t: torch.Tensor, shape, dtypes, index: int) -> int:
+    """Checks a row-major matrix and returns its leading dimension."""
+    if not (t.shape == shape and t.dtype in dtypes and t.get_device() == index
+            and (t.stride(1) == 1 or shape[1] == 1)):
+        raise ValueError(f"{where}: {name} must be row-major {list(shape)} of {dtypes} on GPU "
+                         f"{index}, got {list(t.shape)} {t.dtype} of strides {t.stride()} on "
+                         f"{t.device}")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def _flat(where: str, name: str, t: torch.Tensor, shape, dtypes, index: int):
+    if not (t.shape == shape and t.dtype in dtypes and t.get_device() == index
+            and t.is_contiguous()):
+        raise ValueError(f"{where}: {name} must be contiguous {list(shape)} of {dtypes} on GPU "
+                         f"{index}, got {list(t.shape)} {t.dtype} of strides {t.stride()} on "
+                         f"{t.device}")
+
+
+def _w4_checks(where, X, index, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream):
+    """The packed weights' shapes against X's; returns (m, d_in, d_out, ldx, Y).  A group
     size that the library refuses is left to it: it reads nothing then."""
     m, d_in = X.shape
-    dev = X.device
     d_out = qweight.shape[0]
-    _flat(where, "qweight", qweight, (d_out, d_in // 8), _W32_TYPES, dev)
+    _flat(where, "qweight", qweight, (d_out, d_in // 8), _W32_TYPES, index)
     if group_size == -1 or (group_size > 0 and d_in % group_size == 0):
-        ng = n_groups_for(d_in, group_size)
-        _flat(where, "scales_f16", scales_f16, (d_out, ng), _W16_TYPES, dev)
+        meta = (d_out, 1 if group_size == -1 else d_in // group_size)
+        _flat(where, "scales_f16", scales_f16, meta, _W16_TYPES, index)
         if not sym:
             if zeros_f16 is None:
                 raise ValueError(f"{where}: zeros_f16 is needed unless sym")
-            _flat(where, "zeros_f16", zeros_f16, (d_out, ng), _W16_TYPES, dev)
-    ldx = _rows(where, "X", X, (m, d_in), (X.dtype,), dev)
+            _flat(where, "zeros_f16", zeros_f16, meta, _W16_TYPES, index)
+    if d_in > 1 and X.stride(1) != 1:
+        raise ValueError(f"{where}: X must be row-major")
     if Y is None:
-        Y = _empty(stream, (m, d_out), dtype=torch.float32, device=dev)
+        Y = _empty(stream, (m, d_out), dtype=torch.float32, device=X.device)
     else:
-        _flat(where, "Y", Y, (m, d_out), (torch.float32,), dev)
-    return d_out, ldx, Y
+        _flat(where, "Y", Y, (m, d_out), (torch.float32,), index)
+    return m, d_in, d_out, X.stride(0) if m > 1 else d_in, Y
 
 
 def gptq_w4a16_matvec(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.Tensor,
@@ -513,15 +517,16 @@ def gptq_w4a16_matvec(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.
     """gptq_w4a16_matmul for the rows of a few tokens (m <= GPTQ_MATVEC_MAX_M), any d_in that is a
     multiple of 32: Y [m, d_out] fp32 = X [m, d_in] bf16 times the dequantized weights transposed."""
     where = "gptq_w4a16_matvec"
-    dev = _gpu_matrix(where, X, (torch.bfloat16,))
-    m, d_in = X.shape
-    d_out, ldx, Y = _w4_checks(where, X, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream)
-    _call(where, (X.data_ptr(), m, ldx, qweight.data_ptr(), scales_f16.data_ptr(),
-                  None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size, int(bool(sym)),
-                  Y.data_ptr()), dev, stream)
+    index = _index(where, X, (torch.bfloat16,))
+    m, d_in, d_out, ldx, Y = _w4_checks(where, X, index, qweight, scales_f16, zeros_f16,
+                                        group_size, sym, Y, stream)
+    _call(where, index, stream, X.data_ptr(), m, ldx, qweight.data_ptr(), scales_f16.data_ptr(),
+          None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size, 1 if sym else 0,
+          Y.data_ptr())
     return Y
 
 
+@functools.lru_cache(maxsize=1024)
 def gptq_w4a8_workspace(m: int, d_out: int, d_in: int, group_size: int) -> int:
     return int(lib().gptq_w4a8_workspace(m, d_out, d_in, group_size))
 
@@ -533,18 +538,18 @@ def gptq_w4a8_matmul(X: torch.Tensor, x_scales: torch.Tensor, qweight: torch.Ten
     """Y [m, d_out] fp32 = x_scales [m] times X [m, d_in] int8 (gptq_add_rmsnorm's 8-bit output)
     times the dequantized 4-bit weights transposed."""
     where = "gptq_w4a8_matmul"
-    dev = _gpu_matrix(where, X, (torch.int8,))
-    m, d_in = X.shape
-    d_out, ldx, Y = _w4_checks(where, X, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream)
-    _flat(where, "x_scales", x_scales, (m,), (torch.float32,), dev)
+    index = _index(where, X, (torch.int8,))
+    m, d_in, d_out, ldx, Y = _w4_checks(where, X, index, qweight, scales_f16, zeros_f16,
+                                        group_size, sym, Y, stream)
+    _flat(where, "x_scales", x_scales, (m,), (torch.float32,), index)
     if ws is None:
-        ws = _workspace(gptq_w4a8_workspace(m, d_out, d_in, group_size), dev, stream)
-    elif ws.device != dev:
-        raise ValueError(f"{where}: ws is on {ws.device}, X on {dev}")
-    _call(where, (X.data_ptr(), x_scales.data_ptr(), m, ldx, qweight.data_ptr(),
-                  scales_f16.data_ptr(), None if sym else zeros_f16.data_ptr(), d_out, d_in,
-                  group_size, int(bool(sym)), Y.data_ptr(), None if ws is None else ws.data_ptr(),
-                  0 if ws is None else ws.numel() * ws.element_size()), dev, stream)
+        ws = _workspace(gptq_w4a8_workspace(m, d_out, d_in, group_size), X.device, stream)
+    elif ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"{where}: ws must be contiguous on GPU {index}")
+    _call(where, index, stream, X.data_ptr(), x_scales.data_ptr(), m, ldx, qweight.data_ptr(),
+          scales_f16.data_ptr(), None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size,
+          1 if sym else 0, Y.data_ptr(), None if ws is None else ws.data_ptr(),
+          0 if ws is None else ws.numel() * ws.element_size())
     return Y
 
 
@@ -557,36 +562,35 @@ def gptq_add_rmsnorm(X: torch.Tensor, weight: torch.Tensor, *,
     bf16 or as int8 codes with an fp32 scale per row.  Returns (out, out_scales or None,
     residual_out or None); residual_out = residual updates the residual in place."""
     where = "gptq_add_rmsnorm"
-    floats = (torch.bfloat16, torch.float32)
-    dev = _gpu_matrix(where, X, floats)
-    m, d = X.shape
-    if out_dtype not in (torch.int8, torch.bfloat16):
+    index = _index(where, X, _FLOATS)
+    shape = X.shape
+    m, d = shape
+    if out_dtype is not torch.int8 and out_dtype is not torch.bfloat16:
         raise ValueError(f"{where}: out_dtype must be torch.int8 or torch.bfloat16")
-    i8 = out_dtype == torch.int8
-    ldx = _rows(where, "X", X, (m, d), floats, dev)
-    _flat(where, "weight", weight, (d,), floats, dev)
-    r_code, ldr, ldro = 0, 0, 0
+    i8 = out_dtype is torch.int8
+    if d > 1 and X.stride(1) != 1:
+        raise ValueError(f"{where}: X must be row-major")
+    _flat(where, "weight", weight, (d,), _FLOATS, index)
+    r_code = ldr = ldro = r_ptr = ro_ptr = 0
     if residual is not None:
-        ldr = _rows(where, "residual", residual, (m, d), floats, dev)
+        ldr = _rows(where, "residual", residual, shape, _FLOATS, index)
         r_code = _dtype_code(residual)
         if residual_out is None:
-            residual_out = _empty(stream, (m, d), dtype=residual.dtype, device=dev)
-        ldro = _rows(where, "residual_out", residual_out, (m, d), (residual.dtype,), dev)
+            residual_out = _empty(stream, (m, d), dtype=residual.dtype, device=X.device)
+        ldro = _rows(where, "residual_out", residual_out, shape, (residual.dtype,), index)
+        r_ptr, ro_ptr = residual.data_ptr(), residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError(f"{where}: residual_out without residual")
     if out is None:
-        out = _empty(stream, (m, d), dtype=out_dtype, device=dev)
-    ldo = _rows(where, "out", out, (m, d), (out_dtype,), dev)
+        out = _empty(stream, (m, d), dtype=out_dtype, device=X.device)
+    ldo = _rows(where, "out", out, shape, (out_dtype,), index)
     if not i8:
         out_scales = None
     elif out_scales is None:
-        out_scales = _empty(stream, m, dtype=torch.float32, device=dev)
+        out_scales = _empty(stream, m, dtype=torch.float32, device=X.device)
     else:
-        _flat(where, "out_scales", out_scales, (m,), (torch.float32,), dev)
-    _call(where, (X.data_ptr(), _dtype_code(X), ldx,
-                  None if residual is None else residual.data_ptr(), r_code, ldr,
-                  None if residual_out is None else residual_out.data_ptr(), ldro,
-                  weight.data_ptr(), _dtype_code(weight), float(eps), m, d, out.data_ptr(),
-                  GPTQ_I8 if i8 else GPTQ_BF16, ldo,
-                  out_scales.data_ptr() if i8 else None), dev, stream)
+        _flat(where, "out_scales", out_scales, (m,), (torch.float32,), index)
+    _call(where, index, stream, X.data_ptr(), _dtype_code(X), X.stride(0) if m > 1 else d, r_ptr,
+          r_code, ldr, ro_ptr, ldro, weight.data_ptr(), _dtype_code(weight), float(eps), m, d,
+          out.data_ptr(), GPTQ_I8 if i8 else GPTQ_BF16, ldo, out_scales.data_ptr() if i8 else None)
     return out, out_scales, residual_out
