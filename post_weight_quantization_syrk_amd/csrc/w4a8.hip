@@ -4,7 +4,6 @@
 #include "kernels.h"
 #include "w4_dot.h"
 
-#include <hip/hip_fp16.h>
 #include <algorithm>
 
 namespace gptq {
@@ -17,31 +16,29 @@ typedef __attribute__((ext_vector_type(16))) int i32x16;
 constexpr int KCH = 128;           // k per chunk (bytes of a row of X, twice those of a weight row)
 constexpr int VEC_M = 64;          // up to here w4_vec.h's kernel
 constexpr int PANEL = 32 * KCH;    // bytes of a panel: 32 rows of one chunk
+constexpr int TN = 128;            // weight rows of a tile
+constexpr int NST = 2;             // chunks in LDS
 
 // Where the product's tiles are in the workspace: X as panels of 32 rows by
-// 128 columns, and per group and weight row the scale and the zero.
+// 128 columns, and per group and weight row a word with the scale's binary16
+// bits below and 128 - zero above.
 struct Layout {
   int nch;        // chunks, ceil(d_in / 128)
   int64_t rows;   // rows of X, padded to whole tiles
   int64_t cols;   // weight rows, padded to whole tiles
   int ng;         // groups
-  size_t st_off;  // byte offset of the scales
+  size_t sz_off;  // byte offset of the scales and zeros
   size_t bytes;
 };
 
-struct GroupParam {
-  float s;
-  uint32_t z;  // 128 - zero in every byte
-};
-
-Layout layout_of(int64_t m, int64_t d_out, int64_t d_in, int group_size, int tm, int tn) {
+Layout layout_of(int64_t m, int64_t d_out, int64_t d_in, int group_size, int tm) {
   Layout l;
   l.nch = (int)ceil_div(d_in, KCH);
   l.rows = ceil_div(m, tm) * tm;
-  l.cols = ceil_div(d_out, tn) * tn;
+  l.cols = ceil_div(d_out, TN) * TN;
   l.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
-  l.st_off = (size_t)l.rows * l.nch * KCH;
-  l.bytes = l.st_off + (size_t)l.ng * l.cols * sizeof(GroupParam);
+  l.sz_off = (size_t)l.rows * l.nch * KCH;
+  l.bytes = l.sz_off + (size_t)l.ng * l.cols * 4;
   return l;
 }
 
@@ -52,9 +49,10 @@ Layout layout_of(int64_t m, int64_t d_out, int64_t d_in, int group_size, int tm,
 // Rows past m and columns past d_in are zeros: they add nothing to any sum.
 __global__ __launch_bounds__(256) void w4a8_layout_kernel(
     const int8_t* __restrict__ X, int64_t ldx, int64_t M, int N, int K, Layout l,
-    const uint16_t* __restrict__ S16, const uint16_t* __restrict__ Z16, char* __restrict__ ws) {
+    const uint16_t* __restrict__ S16, const uint16_t* __restrict__ Z16, int vec,
+    char* __restrict__ ws) {
   const int64_t units = l.rows * l.nch * (KCH / 16);
-  const int64_t params = (int64_t)l.ng * l.cols;
+  const int64_t params = ceil_div(l.ng, vec) * l.cols;
   for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < units + params;
        t += (int64_t)gridDim.x * 256) {
     if (t < units) {
@@ -71,16 +69,36 @@ __global__ __launch_bounds__(256) void w4a8_layout_kernel(
       const int r = (int)(row & 31), c = u >> 3, uu = (u & 7) ^ ((r >> 1) & 7);
       *(uint4*)(ws + ((row >> 5) * l.nch + c) * PANEL + r * KCH + 16 * uu) = o;
     } else {
+      // a weight row's parameters of `vec` groups (what its alignment allows
+      // in one load); neighbouring threads take neighbouring rows, so that the
+      // groups' planes are written whole
       const int64_t p = t - units;
-      const int g = (int)(p / l.cols);
-      const int64_t n = p - (int64_t)g * l.cols;
-      GroupParam gp = {0.0f, 0u};
+      const int g = (int)(p / l.cols) * vec;
+      const int64_t n = p % l.cols;
+      uint16_t s[8], z[8];
       if (n < N) {
-        gp.s = __half2float(__ushort_as_half(S16[n * l.ng + g]));
-        const float z = Z16 ? __half2float(__ushort_as_half(Z16[n * l.ng + g])) : 8.0f;
-        gp.z = (uint32_t)(128 - (int)fminf(fmaxf(rintf(z), -100.0f), 100.0f)) * 0x01010101u;
+        const int64_t at = n * l.ng + g;
+        if (vec == 8) {
+          *(uint4*)s = *(const uint4*)(S16 + at);
+          if (Z16) *(uint4*)z = *(const uint4*)(Z16 + at);
+        } else if (vec == 4) {
+          *(uint2*)s = *(const uint2*)(S16 + at);
+          if (Z16) *(uint2*)z = *(const uint2*)(Z16 + at);
+        } else if (vec == 2) {
+          *(uint32_t*)s = *(const uint32_t*)(S16 + at);
+          if (Z16) *(uint32_t*)z = *(const uint32_t*)(Z16 + at);
+        } else {
+          s[0] = S16[at];
+          if (Z16) z[0] = Z16[at];
+        }
       }
-      ((GroupParam*)(ws + l.st_off))[p] = gp;
+      uint32_t* out = (uint32_t*)(ws + l.sz_off) + (int64_t)g * l.cols + n;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= vec) break;
+        out[i * l.cols] =
+            n < N ? s[i] | (uint32_t)(128 - (Z16 ? w4vec::whole_zero(z[i]) : 8)) << 16 : 0u;
+      }
     }
   }
 }
@@ -112,243 +130,293 @@ struct MulArgs {
   const char* ws;
   const float* sx;
   const uint32_t* q;
-  float* y;
+  float* y;       // Y, or the splits' partial products
   Layout l;
   int64_t M;
   int N;
   int row_bytes;  // of a packed weight row
   int tiles_m, tiles_n;
+  int splits, per_split;  // of the chunks
 };
 
-// Four waves as 2 x 2, each 32 MI rows by 32 NI weight rows.  G: group size,
-// 0 for one group per row.
-template <int MI, int NI, int G>
+// Four waves side by side, each 32 MI rows of X by 32 weight rows: a wave
+// takes the codes of its own weight rows apart, and none twice.  G: group
+// size, 0 for one group per row.
+template <int MI, int G>
 __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
-  constexpr int TM = 64 * MI, TN = 64 * NI;
-  constexpr int ABYTES = TM * KCH, BBYTES = TN * (KCH / 2), STAGE = ABYTES + BBYTES;
-  constexpr int GPC = G == 0 ? 1 : KCH / G;  // groups per chunk
-  __shared__ __attribute__((aligned(1024))) char lds[2 * STAGE];
+  constexpr int TM = 32 * MI;
+  constexpr int GPC = G == 0 ? 0 : KCH / G;  // groups per chunk
+  constexpr int ABYTES = TM * KCH, BBYTES = TN * (KCH / 2), SZBYTES = GPC * TN * 4;
+  constexpr int STAGE = ABYTES + BBYTES + SZBYTES;
+  constexpr int LOADS = MI + 2 + GPC;        // direct loads of a wave per chunk
+  __shared__ __attribute__((aligned(1024))) char lds[NST * STAGE];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int h = lane >> 5, l32 = lane & 31, wm = wave & 1, wn = wave >> 1;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int h = lane >> 5, l32 = lane & 31;
   // consecutive workgroups go to the eight XCDs in turn: each XCD takes a run
-  // of tiles, 8 x 8 of them at a time, so that its L2 holds what they share
-  const int total = a.tiles_m * a.tiles_n, per = (total + 7) / 8;
-  const int t = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-  if (t >= min(total, ((int)(blockIdx.x & 7) + 1) * per)) return;
+  // of tiles, eight tiles of weight rows wide, so that its L2 holds what they
+  // share
+  const int tiles = a.tiles_m * a.tiles_n, total = tiles * a.splits, per = (total + 7) / 8;
+  const int t0 = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if (t0 >= min(total, ((int)(blockIdx.x & 7) + 1) * per)) return;
+  const int split = t0 / tiles, t = t0 - split * tiles;
   const int sup = t / (8 * a.tiles_m), rest = t - sup * 8 * a.tiles_m;
-  const int wn_tiles = min(8, a.tiles_n - 8 * sup);
-  const int tm = rest / wn_tiles, tn = 8 * sup + rest - tm * wn_tiles;
+  const int wide = min(8, a.tiles_n - 8 * sup);
+  const int tm = rest / wide, tn = 8 * sup + rest - tm * wide;
   const int64_t m0 = (int64_t)tm * TM;
   const int n0 = tn * TN;
-  const int nch = a.l.nch;
+  const int nch = a.l.nch, c0 = split * a.per_split, c1 = min(nch, c0 + a.per_split);
 
-  // direct loads: X panels are copied as they are; a weight row's 64 bytes of
-  // a chunk go to units that put 16 rows on different banks
+  // direct loads: X panels and group words are copied as they are; a weight
+  // row's 64 bytes of a chunk go to units that put 16 rows on different banks
   const char* xbase = a.ws + (m0 >> 5) * nch * PANEL;
   const char* qbase = (const char*)a.q + (int64_t)n0 * a.row_bytes;
-  uint32_t qrow[NI], qu;
+  const uint32_t* sz = (const uint32_t*)(a.ws + a.l.sz_off) + n0 + 32 * wave;
+  uint32_t qrow[2];
 #pragma unroll
-  for (int j = 0; j < NI; ++j)
-    qrow[j] = (uint32_t)min(16 * (NI * wave + j) + (lane >> 2), a.N - 1 - n0) * a.row_bytes;
-  qu = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
+  for (int j = 0; j < 2; ++j)
+    qrow[j] = (uint32_t)min(16 * (2 * wave + j) + (lane >> 2), a.N - 1 - n0) * a.row_bytes;
+  const uint32_t qu = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
   auto issue = [&](int c, int buf) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + buf * STAGE;
 #pragma unroll
-    for (int j = 0; j < 2 * MI; ++j) {  // 1 KB pieces of the tile's 2 MI panels
-      const int piece = 2 * MI * wave + j;
-      dma16(xbase + ((int64_t)(piece >> 2) * nch + c) * PANEL, (piece & 3) * 1024 + lane * 16,
+    for (int j = 0; j < MI; ++j) {  // 1 KB pieces of the tile's MI panels
+      const int piece = MI * wave + j;
+      dma16(xbase + ((int64_t)(piece >> 2) * nch + c) * PANEL + (piece & 3) * 1024, lane * 16,
             dst + piece * 1024);
     }
     const uint32_t k = min((uint32_t)c * (KCH / 2) + qu, (uint32_t)a.row_bytes - 16);
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
-      dma16(qbase, qrow[j] + k, dst + ABYTES + (NI * wave + j) * 1024);
-  };
-  const GroupParam* st = (const GroupParam*)(a.ws + a.l.st_off) + n0 + 32 * NI * wn + l32;
-  GroupParam gp[NI][GPC], gn[NI][GPC];
-  auto params = [&](int c) __attribute__((always_inline)) {
+    for (int j = 0; j < 2; ++j)
+      dma16(qbase, qrow[j] + k, dst + ABYTES + (2 * wave + j) * 1024);
+    if constexpr (G != 0) {
+      if (lane < 8) {  // this wave's 32 words of each group
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int g = 0; g < GPC; ++g)
-        gn[j][g] = st[(int64_t)(G == 0 ? 0 : min(c * GPC + g, a.l.ng - 1)) * a.l.cols + 32 * j];
-  };
-
-  f32x16 tot[G == 0 ? 1 : MI][G == 0 ? 1 : NI];
-  i32x16 sum[G == 0 ? MI : 1][G == 0 ? NI : 1];
-  if constexpr (G == 0) {
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[mi][ni][i] = 0;
-  } else {
-#pragma unroll
-    for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) tot[mi][ni][i] = 0.0f;
-  }
-  issue(0, 0);
-  params(0);
-  for (int c = 0; c < nch; ++c) {
-    const int buf = c & 1;
-    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();  // chunk c has landed, and chunk c - 1's buffer is read
-#pragma unroll
-    for (int j = 0; j < NI; ++j)
-#pragma unroll
-      for (int g = 0; g < GPC; ++g) gp[j][g] = gn[j][g];
-    if (c + 1 < nch) {
-      issue(c + 1, buf ^ 1);
-      params(c + 1);
+        for (int g = 0; g < GPC; ++g)
+          dma16(sz + (int64_t)min(c * GPC + g, a.l.ng - 1) * a.l.cols, lane * 16,
+                dst + ABYTES + BBYTES + (g * TN + 32 * wave) * 4);
+      }
     }
-    const char* la = lds + buf * STAGE + wm * MI * PANEL;
-    const char* lb = lds + buf * STAGE + ABYTES + 32 * NI * wn * (KCH / 2);
-    // MFMA q of a chunk takes, in lane half h, unit xu(q) of X: with groups of
-    // 32 the two halves share 32 consecutive k, otherwise 64
-    i32x4 bf[NI][4];
+  };
+  const uint32_t row_sz = G == 0 ? sz[l32] : 0u;
+
+  f32x16 tot[G == 0 ? 1 : MI];
+  i32x16 sum[G == 0 ? MI : 1];
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      const int row = 32 * ni + l32;
+  for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if constexpr (G == 0)
+        sum[mi][i] = 0;
+      else
+        tot[mi][i] = 0.0f;
+    }
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s)
+    if (c0 + s < c1) issue(c0 + s, s);
+  int buf = 0;
+  for (int c = c0; c < c1; ++c) {
+    // chunk c has landed (the newer chunks' loads may be on their way), and
+    // chunk c - 1's buffer is read
+    if (c + NST - 2 < c1)
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * LOADS) : "memory");
+    else
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (c + NST - 1 < c1) issue(c + NST - 1, buf == 0 ? NST - 1 : buf - 1);
+    const char* la = lds + buf * STAGE;
+    const char* lb = lds + buf * STAGE + ABYTES + (32 * wave + l32) * (KCH / 2);
+    const uint32_t* lz = (const uint32_t*)(lds + buf * STAGE + ABYTES + BBYTES) + 32 * wave + l32;
+    buf = buf == NST - 1 ? 0 : buf + 1;
+    const int sw = (l32 >> 2) & 3;
+    float scale[GPC ? GPC : 1];
+    uint32_t zc[GPC ? GPC : 1];
+#pragma unroll
+    for (int g = 0; g < (GPC ? GPC : 1); ++g) {
+      const uint32_t v = G == 0 ? row_sz : lz[g * TN];
+      scale[g] = w4vec::half_bits((uint16_t)v);
+      zc[g] = __builtin_amdgcn_perm(v, v, 0x02020202u);
+      asm("" : "+v"(scale[g]));  // or every product converts it again
+    }
+    // MFMA q of a chunk takes, in lane half h, unit u of X: with groups of 32
+    // the two halves share 32 consecutive k, otherwise 64
+    i32x4 bf[4];
+    {
       uint32_t w[8];
       if constexpr (G == 32) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const uint2 v = *(const uint2*)(lb + row * 64 + 16 * (q ^ ((row >> 2) & 3)) + 8 * h);
+          const uint2 v = *(const uint2*)(lb + 16 * (q ^ sw) + 8 * h);
           w[2 * q] = v.x, w[2 * q + 1] = v.y;
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint4 v = *(const uint4*)(lb + row * 64 + 16 * ((2 * j + h) ^ ((row >> 2) & 3)));
+          const uint4 v = *(const uint4*)(lb + 16 * ((2 * j + h) ^ sw));
           w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
         }
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint32_t zc = gp[ni][q * GPC / 4].z;
         int o[4];
-        minus_zero(w[2 * q], zc, o[0], o[1]);
-        minus_zero(w[2 * q + 1], zc, o[2], o[3]);
-        bf[ni][q] = i32x4{o[0], o[1], o[2], o[3]};
+        minus_zero(w[2 * q], zc[q * GPC / 4], o[0], o[1]);
+        minus_zero(w[2 * q + 1], zc[q * GPC / 4], o[2], o[3]);
+        bf[q] = i32x4{o[0], o[1], o[2], o[3]};
       }
     }
+    auto xfrag = [&](int mi, int q) __attribute__((always_inline)) {
+      const int u = G == 32 ? 2 * q + h : 4 * (q >> 1) + 2 * h + (q & 1);
+      return *(const i32x4*)(la + mi * PANEL + l32 * KCH + 16 * (u ^ ((l32 >> 1) & 7)));
+    };
+    if constexpr (G == 0) {
 #pragma unroll
-    for (int mi = 0; mi < MI; ++mi) {
-      i32x4 af[4];
+      for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int u = G == 32 ? 2 * q + h : 4 * (q >> 1) + 2 * h + (q & 1);
-        af[q] = *(const i32x4*)(la + mi * PANEL + l32 * KCH + 16 * (u ^ ((l32 >> 1) & 7)));
-      }
+        for (int q = 0; q < 4; ++q)
+          sum[mi] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xfrag(mi, q), bf[q], sum[mi], 0, 0, 0);
+    } else {
+      // step s multiplies for one block of 32 rows and one group while the
+      // step before it is scaled into its total
+      constexpr int STEPS = MI * GPC, QPS = 4 / GPC;
+      i32x4 af[2][QPS];
+      i32x16 acc[2];
 #pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        if constexpr (G == 0) {
+      for (int q = 0; q < QPS; ++q) af[0][q] = xfrag(0, q);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            sum[mi][ni] =
-                __builtin_amdgcn_mfma_i32_32x32x32_i8(af[q], bf[ni][q], sum[mi][ni], 0, 0, 0);
-        } else {
+      for (int s = 0; s <= STEPS; ++s) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (s + 1 < STEPS) {
 #pragma unroll
-          for (int g = 0; g < GPC; ++g) {
-            i32x16 acc = {};
+          for (int q = 0; q < QPS; ++q)
+            af[(s + 1) & 1][q] = xfrag((s + 1) / GPC, (s + 1) % GPC * QPS + q);
+        }
+        if (s < STEPS) {
+          acc[s & 1] = i32x16{};
 #pragma unroll
-            for (int q = 4 * g / GPC; q < 4 * (g + 1) / GPC; ++q)
-              acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[q], bf[ni][q], acc, 0, 0, 0);
+          for (int q = 0; q < QPS; ++q)
+            acc[s & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[s & 1][q], bf[s % GPC * QPS + q],
+                                                               acc[s & 1], 0, 0, 0);
+        }
+        if (s > 0) {
+          const int mi = (s - 1) / GPC, g = (s - 1) % GPC;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              tot[mi][ni][i] = fmaf(gp[ni][g].s, (float)acc[i], tot[mi][ni][i]);
-          }
+          for (int i = 0; i < 16; ++i)
+            tot[mi][i] = fmaf(scale[g], (float)acc[(s - 1) & 1][i], tot[mi][i]);
+        }
+#pragma unroll
+        for (int q = 0; q < QPS; ++q) {
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);        // an LDS read
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);        // a product
+          __builtin_amdgcn_sched_group_barrier(0x002, 32 / QPS, 0); // its share of the scaling
         }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
+  const int col = n0 + 32 * wave + l32;
+  float* const y = a.y + (int64_t)split * a.M * a.N;
+  if (col >= a.N) return;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const int64_t row = m0 + 32 * (MI * wm + mi) + 8 * (i >> 2) + 4 * h + (i & 3);
+      const int64_t row = m0 + 32 * mi + 8 * (i >> 2) + 4 * h + (i & 3);
       if (row >= a.M) continue;
-      const float sx = a.sx[row];
-#pragma unroll
-      for (int ni = 0; ni < NI; ++ni) {
-        const int col = n0 + 32 * (NI * wn + ni) + l32;
-        float v;
-        if constexpr (G == 0)
-          v = gp[ni][0].s * (float)sum[mi][ni][i];
-        else
-          v = tot[mi][ni][i];
-        if (col < a.N) a.y[row * a.N + col] = sx * v;
-      }
+      float v;
+      if constexpr (G == 0)
+        v = w4vec::half_bits((uint16_t)row_sz) * (float)sum[mi][i];
+      else
+        v = tot[mi][i];
+      y[row * a.N + col] = a.splits > 1 ? v : a.sx[row] * v;
     }
 }
 
-struct Tile {
-  int mi, ni;
-};
-
-Tile tile_for(int64_t m, int64_t d_out) {
-  if (ceil_div(m, 256) * ceil_div(d_out, 128) >= 512) return {4, 2};
-  if (ceil_div(m, 128) * ceil_div(d_out, 128) >= 256) return {2, 2};
-  return {1, 1};
+// Y = sx times the splits' products, added in split order.
+__global__ __launch_bounds__(256) void w4a8_join_kernel(const float* __restrict__ part,
+                                                        const float* __restrict__ sx, int64_t M,
+                                                        int N, int splits, float* __restrict__ Y) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= M * N) return;
+  float v = part[e];
+  for (int s = 1; s < splits; ++s) v += part[s * M * N + e];
+  Y[e] = sx[e / N] * v;
 }
 
-template <int MI, int NI>
+struct Plan {
+  int mi, splits, per_split;
+  Layout l;
+  size_t part_off, bytes;
+};
+
+Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
+  Plan p;
+  const int nch = (int)ceil_div(d_in, KCH);
+  auto tiles = [&](int mi) { return ceil_div(m, 32 * mi) * ceil_div(d_out, TN); };
+  p.mi = tiles(4) >= 384 ? 4 : tiles(2) >= 384 ? 2 : 1;
+  int64_t splits = 1;
+  while (splits < 16 && tiles(p.mi) * splits < 384 && nch >= 8 * splits) splits *= 2;
+  p.per_split = (int)ceil_div(nch, splits);
+  p.splits = (int)ceil_div(nch, p.per_split);
+  p.l = layout_of(m, d_out, d_in, group_size, 32 * p.mi);
+  p.part_off = (p.l.bytes + 255) / 256 * 256;
+  p.bytes = p.splits > 1 ? p.part_off + (size_t)p.splits * m * d_out * 4 : p.l.bytes;
+  return p;
+}
+
+template <int MI>
 void launch(const MulArgs& a, int G, hipStream_t stream) {
-  const dim3 grid((unsigned)(8 * ceil_div((int64_t)a.tiles_m * a.tiles_n, 8)));
+  const dim3 grid((unsigned)(8 * ceil_div((int64_t)a.tiles_m * a.tiles_n * a.splits, 8)));
   switch (G) {
-    case 32: hipLaunchKernelGGL((w4a8_kernel<MI, NI, 32>), grid, dim3(256), 0, stream, a); break;
-    case 64: hipLaunchKernelGGL((w4a8_kernel<MI, NI, 64>), grid, dim3(256), 0, stream, a); break;
-    case 128: hipLaunchKernelGGL((w4a8_kernel<MI, NI, 128>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((w4a8_kernel<MI, NI, 0>), grid, dim3(256), 0, stream, a);
+    case 32: hipLaunchKernelGGL((w4a8_kernel<MI, 32>), grid, dim3(256), 0, stream, a); break;
+    case 64: hipLaunchKernelGGL((w4a8_kernel<MI, 64>), grid, dim3(256), 0, stream, a); break;
+    case 128: hipLaunchKernelGGL((w4a8_kernel<MI, 128>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((w4a8_kernel<MI, 0>), grid, dim3(256), 0, stream, a);
   }
 }
 
 }  // namespace
 
 size_t w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
-  if (m <= VEC_M) return 0;
-  const Tile t = tile_for(m, d_out);
-  return layout_of(m, d_out, d_in, group_size, 64 * t.mi, 64 * t.ni).bytes;
+  return m <= VEC_M ? 0 : plan_for(m, d_out, d_in, group_size).bytes;
 }
 
 hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_t ldx,
                        const uint32_t* qweight, const uint16_t* scales_f16,
                        const uint16_t* zeros_f16, int64_t d_out, int64_t d_in, int group_size,
                        float* Y, void* ws, hipStream_t stream) {
+  const int G = group_size == -1 ? 0 : group_size;
   if (m <= VEC_M) {
     w4vec::VecArgs v;
     v.x = (const char*)X, v.sx = x_scales, v.q = qweight, v.s16 = scales_f16, v.z16 = zeros_f16;
     v.y = Y, v.ldx = ldx, v.m = (int)m, v.n = (int)d_out, v.k = (int)d_in;
     v.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
     v.vec = w4vec::scale_vec(scales_f16, zeros_f16, v.ng);
-    const int G = group_size == -1 ? 0 : group_size;
     return w4vec::dot_takes(m, d_in) ? w4vec::dot_launch<true>(v, G, stream)
-                                          : w4vec::vec_launch<true>(v, G, stream);
+                                     : w4vec::vec_launch<true>(v, G, stream);
   }
-  const Tile t = tile_for(m, d_out);
-  const Layout l = layout_of(m, d_out, d_in, group_size, 64 * t.mi, 64 * t.ni);
-  const int64_t items = l.rows * l.nch * (KCH / 16) + (int64_t)l.ng * l.cols;
+  const Plan p = plan_for(m, d_out, d_in, group_size);
+  const int vec = w4vec::scale_vec(scales_f16, zeros_f16, p.l.ng);
+  const int64_t items = p.l.rows * p.l.nch * (KCH / 16) + (int64_t)ceil_div(p.l.ng, vec) * p.l.cols;
   hipLaunchKernelGGL(w4a8_layout_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(items, 256), 8192)),
-                     dim3(256), 0, stream, X, ldx, m, (int)d_out, (int)d_in, l, scales_f16,
-                     zeros_f16, (char*)ws);
+                     dim3(256), 0, stream, X, ldx, m, (int)d_out, (int)d_in, p.l, scales_f16,
+                     zeros_f16, vec, (char*)ws);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   MulArgs a;
-  a.ws = (const char*)ws, a.sx = x_scales, a.q = qweight, a.y = Y, a.l = l, a.M = m;
+  a.ws = (const char*)ws, a.sx = x_scales, a.q = qweight, a.l = p.l, a.M = m;
+  a.y = p.splits > 1 ? (float*)((char*)ws + p.part_off) : Y;
   a.N = (int)d_out, a.row_bytes = (int)(d_in / 2);
-  a.tiles_m = (int)(l.rows / (64 * t.mi)), a.tiles_n = (int)(l.cols / (64 * t.ni));
-  const int G = group_size == -1 ? 0 : group_size;
-  if (t.mi == 4)
-    launch<4, 2>(a, G, stream);
-  else if (t.mi == 2)
-    launch<2, 2>(a, G, stream);
-  else
-    launch<1, 1>(a, G, stream);
+  a.tiles_m = (int)(p.l.rows / (32 * p.mi)), a.tiles_n = (int)(p.l.cols / TN);
+  a.splits = p.splits, a.per_split = p.per_split;
+  switch (p.mi) {
+    case 4: launch<4>(a, G, stream); break;
+    case 2: launch<2>(a, G, stream); break;
+    default: launch<1>(a, G, stream);
+  }
+  e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  hipLaunchKernelGGL(w4a8_join_kernel, dim3((unsigned)ceil_div(m * d_out, 256)), dim3(256), 0,
+                     stream, a.y, x_scales, m, (int)d_out, p.splits, Y);
   return hipGetLastError();
 }
 
