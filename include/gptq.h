@@ -306,6 +306,8 @@ int gptq_w4a16_matmul(const void* X, int64_t m, int64_t ldx, const uint32_t* qwe
  *   m           0 .. GPTQ_MATVEC_MAX_M (0 is a no-op; more gives
  *               GPTQ_EUNSUPPORTED: gptq_w4a16_matmul takes any m).
  *   qweight     16-byte aligned.
+ *   ws          gptq_w4a16_matvec_workspace(m, d_out, d_in, group_size) bytes
+ *               (0 for most shapes); its contents on entry do not matter.
  * The weights are read once.  Per group, sum x q and sum x are formed with
  * exact products and fp32 sums and joined as s (sum x q - z sum x); groups
  * are added in fp32.  The order of every sum is fixed: the same inputs give
@@ -315,7 +317,9 @@ int gptq_w4a16_matmul(const void* X, int64_t m, int64_t ldx, const uint32_t* qwe
 #define GPTQ_MATVEC_MAX_M 64
 int gptq_w4a16_matvec(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
                       const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
-                      int64_t d_in, int group_size, int sym, float* Y, gptq_stream stream);
+                      int64_t d_in, int group_size, int sym, float* Y, void* ws, size_t ws_bytes,
+                      gptq_stream stream);
+size_t gptq_w4a16_matvec_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size);
 
 /* ---------------------------------------------------------------------------
  * Residual addition, root-mean-square norm and an 8-bit output with a scale

@@ -79,9 +79,10 @@ hipError_t w4a16_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* q
                         int64_t d_in, int group_size, float* Y, hipStream_t stream);
 
 // ---- the same product for a few tokens (m <= 64) ---------------------------
+size_t w4a16_vec_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size);
 hipError_t w4a16_vec_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
                             const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
-                            int64_t d_in, int group_size, float* Y, hipStream_t stream);
+                            int64_t d_in, int group_size, float* Y, void* ws, hipStream_t stream);
 
 // ---- residual addition, RMS norm, bf16 or 8-bit output ---------------------
 hipError_t add_rmsnorm_launch(const void* X, int x_dtype, int64_t ldx, const void* R, int r_dtype,

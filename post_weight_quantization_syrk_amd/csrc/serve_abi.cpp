@@ -12,6 +12,10 @@ int hip_status(hipError_t e) { return e == hipSuccess ? GPTQ_OK : GPTQ_EHIP; }
 
 bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 
+bool workspace(const void* ws, size_t have, size_t need) {
+  return have >= need && (need == 0 || (ws && aligned(ws, 256)));
+}
+
 bool float_type(int t) { return t == GPTQ_BF16 || t == GPTQ_F32; }
 
 size_t type_size(int t) { return t == GPTQ_F32 ? 4 : t == GPTQ_BF16 ? 2 : 1; }
@@ -64,18 +68,27 @@ int gptq_add_rmsnorm(const void* X, int x_dtype, int64_t ldx, const void* R, int
                                              (hipStream_t)stream));
 }
 
+size_t gptq_w4a16_matvec_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
+  if (m <= 0 || m > GPTQ_MATVEC_MAX_M || check_w4(m, d_out, d_in, group_size, 0) != GPTQ_OK)
+    return 0;
+  return gptq::w4a16_vec_workspace(m, d_out, d_in, group_size);
+}
+
 int gptq_w4a16_matvec(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
                       const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
-                      int64_t d_in, int group_size, int sym, float* Y, gptq_stream stream) {
+                      int64_t d_in, int group_size, int sym, float* Y, void* ws, size_t ws_bytes,
+                      gptq_stream stream) {
   const int st = check_w4(m, d_out, d_in, group_size, sym);
   if (st != GPTQ_OK) return st;
   if (m > GPTQ_MATVEC_MAX_M) return GPTQ_EUNSUPPORTED;
   if (m == 0) return GPTQ_OK;
   if (ldx < d_in || ldx % 8 != 0 || !X || !aligned(X, 16)) return GPTQ_EINVAL;
   if (!w4_pointers(qweight, scales_f16, zeros_f16, sym, Y)) return GPTQ_EINVAL;
+  if (!workspace(ws, ws_bytes, gptq::w4a16_vec_workspace(m, d_out, d_in, group_size)))
+    return GPTQ_EINVAL;
   return hip_status(gptq::w4a16_vec_launch(X, m, ldx, qweight, scales_f16,
                                            sym ? nullptr : zeros_f16, d_out, d_in, group_size, Y,
-                                           (hipStream_t)stream));
+                                           ws, (hipStream_t)stream));
 }
 
 size_t gptq_w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
@@ -93,8 +106,8 @@ int gptq_w4a8_matmul(const int8_t* X, const float* x_scales, int64_t m, int64_t 
   if (ldx < d_in || ldx % 16 != 0 || !X || !aligned(X, 16)) return GPTQ_EINVAL;
   if (!x_scales || !aligned(x_scales, 4)) return GPTQ_EINVAL;
   if (!w4_pointers(qweight, scales_f16, zeros_f16, sym, Y)) return GPTQ_EINVAL;
-  const size_t need = gptq::w4a8_workspace(m, d_out, d_in, group_size);
-  if (ws_bytes < need || (need && (!ws || !aligned(ws, 256)))) return GPTQ_EINVAL;
+  if (!workspace(ws, ws_bytes, gptq::w4a8_workspace(m, d_out, d_in, group_size)))
+    return GPTQ_EINVAL;
   return hip_status(gptq::w4a8_launch(X, x_scales, m, ldx, qweight, scales_f16,
                                       sym ? nullptr : zeros_f16, d_out, d_in, group_size, Y, ws,
                                       (hipStream_t)stream));

@@ -1,6 +1,6 @@
-// The products of packed 4-bit weights with one to four tokens: bf16 or int8
-// activations, one kernel template for both.
-//   Y[i][n] = sx[i] sum_g s[n][g] (sum_{k in g} x q - z[n][g] sum_{k in g} x)
+// The products of packed 4-bit weights with one token: bf16 or int8 activations,
+// one kernel template for both.
+//   Y[n] = sx sum_g s[n][g] (sum_{k in g} x q - z[n][g] sum_{k in g} x)
 //
 // A wave keeps a run of 2048 k of X in registers, 32 consecutive k per lane,
 // and takes that run of one weight row after the other: 1 KB of a row per
@@ -50,11 +50,11 @@ __device__ __forceinline__ float wave_sum4(const float v[4]) {
   return row_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
-// MT: tokens; ks: waves that share a row (runs per row); rpw: rows per wave, a
+// ks: waves that share a row (runs per row); rpw: rows per wave, a
 // multiple of 4.
-template <bool I8, int MT>
-__global__ __launch_bounds__(MT == 1 ? 1024 : 512) void w4_dot_kernel(VecArgs a, int G, int ks, int rpw) {
-  extern __shared__ float red[];  // [rows of the workgroup][ks][MT]
+template <bool I8>
+__global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, int rpw) {
+  extern __shared__ float red[];  // [rows of the workgroup][ks]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int seg = wave % ks, rg = wave / ks, rows = (int)(blockDim.x >> 6) / ks * rpw;
   const int64_t n0 = (int64_t)blockIdx.x * rows + rg * rpw;
@@ -81,65 +81,51 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void w4_dot_kernel(VecArgs a,
   load(0, cur);
 
   // x in the order in which a word's codes come apart: 0 2 4 6 1 3 5 7
-  uint32_t x[MT][I8 ? 8 : 16];
-  float xsum[MT];
-  int xsumi[MT];
+  uint32_t x[I8 ? 8 : 16];
+  float xsum = 0.0f;
+  int xsumi = 0;
+  const uint4* p = (const uint4*)(a.x + kc * (I8 ? 1 : 2));
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const uint4* p = (const uint4*)(a.x + (int64_t)min(t, a.m - 1) * a.ldx + kc * (I8 ? 1 : 2));
-    xsum[t] = 0.0f;
-    xsumi[t] = 0;
+  for (int j = 0; j < (I8 ? 2 : 4); ++j) {
+    uint4 v = p[j];
+    if (!in) v = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (I8) {
+      x[4 * j] = __builtin_amdgcn_perm(v.y, v.x, 0x06040200u);
+      x[4 * j + 1] = __builtin_amdgcn_perm(v.y, v.x, 0x07050301u);
+      x[4 * j + 2] = __builtin_amdgcn_perm(v.w, v.z, 0x06040200u);
+      x[4 * j + 3] = __builtin_amdgcn_perm(v.w, v.z, 0x07050301u);
 #pragma unroll
-    for (int j = 0; j < (I8 ? 2 : 4); ++j) {
-      uint4 v = p[j];
-      if (!in) v = make_uint4(0u, 0u, 0u, 0u);
-      if constexpr (I8) {
-        x[t][4 * j] = __builtin_amdgcn_perm(v.y, v.x, 0x06040200u);
-        x[t][4 * j + 1] = __builtin_amdgcn_perm(v.y, v.x, 0x07050301u);
-        x[t][4 * j + 2] = __builtin_amdgcn_perm(v.w, v.z, 0x06040200u);
-        x[t][4 * j + 3] = __builtin_amdgcn_perm(v.w, v.z, 0x07050301u);
+      for (int e = 0; e < 4; ++e)
+        xsumi = __builtin_amdgcn_sdot4((int)x[4 * j + e], 0x01010101, xsumi, false);
+    } else {
+      x[4 * j] = __builtin_amdgcn_perm(v.y, v.x, 0x05040100u);
+      x[4 * j + 1] = __builtin_amdgcn_perm(v.w, v.z, 0x05040100u);
+      x[4 * j + 2] = __builtin_amdgcn_perm(v.y, v.x, 0x07060302u);
+      x[4 * j + 3] = __builtin_amdgcn_perm(v.w, v.z, 0x07060302u);
+      const bf16x2 ones = as_bf16x2(0x3f803f80u);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          xsumi[t] = __builtin_amdgcn_sdot4((int)x[t][4 * j + e], 0x01010101, xsumi[t], false);
-      } else {
-        x[t][4 * j] = __builtin_amdgcn_perm(v.y, v.x, 0x05040100u);
-        x[t][4 * j + 1] = __builtin_amdgcn_perm(v.w, v.z, 0x05040100u);
-        x[t][4 * j + 2] = __builtin_amdgcn_perm(v.y, v.x, 0x07060302u);
-        x[t][4 * j + 3] = __builtin_amdgcn_perm(v.w, v.z, 0x07060302u);
-        const bf16x2 ones = as_bf16x2(0x3f803f80u);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) xsum[t] = dot2(as_bf16x2(x[t][4 * j + e]), ones, xsum[t]);
-      }
+      for (int e = 0; e < 4; ++e) xsum = dot2(as_bf16x2(x[4 * j + e]), ones, xsum);
     }
   }
 
   for (int r = 0; r < rpw; r += 4) {
     if (r + 4 < rpw) load(r + 4, nxt);
-    float v[MT][4];
+    float v[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const uint32_t w[4] = {cur.w[u].x, cur.w[u].y, cur.w[u].z, cur.w[u].w};
       const float s = half_bits(cur.s[u]);
       if constexpr (I8) {
-        int acc[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) acc[t] = 0;
+        int acc = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int ev = (int)(w[j] & 0x0f0f0f0fu), od = (int)((w[j] >> 4) & 0x0f0f0f0fu);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            acc[t] = __builtin_amdgcn_sdot4((int)x[t][2 * j], ev, acc[t], false);
-            acc[t] = __builtin_amdgcn_sdot4((int)x[t][2 * j + 1], od, acc[t], false);
-          }
+          acc = __builtin_amdgcn_sdot4((int)x[2 * j], (int)(w[j] & 0x0f0f0f0fu), acc, false);
+          acc = __builtin_amdgcn_sdot4((int)x[2 * j + 1], (int)((w[j] >> 4) & 0x0f0f0f0fu), acc,
+                                       false);
         }
-        const int z = whole_zero(cur.z[u]);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) v[t][u] = s * (float)(acc[t] - __mul24(z, xsumi[t]));
+        v[u] = s * (float)(acc - __mul24(whole_zero(cur.z[u]), xsumi));
       } else {
-        float acc[MT];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) acc[t] = 0.0f;
+        float acc = 0.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t ev = w[j] & 0x0f0f0f0fu, od = (w[j] >> 4) & 0x0f0f0f0fu;
@@ -147,63 +133,42 @@ __global__ __launch_bounds__(MT == 1 ? 1024 : 512) void w4_dot_kernel(VecArgs a,
           const bf16x2 b1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ev, 512.0f, true);
           const bf16x2 b2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(od, 512.0f, false);
           const bf16x2 b3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(od, 512.0f, true);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            acc[t] = dot2(as_bf16x2(x[t][4 * j]), b0, acc[t]);
-            acc[t] = dot2(as_bf16x2(x[t][4 * j + 1]), b1, acc[t]);
-            acc[t] = dot2(as_bf16x2(x[t][4 * j + 2]), b2, acc[t]);
-            acc[t] = dot2(as_bf16x2(x[t][4 * j + 3]), b3, acc[t]);
-          }
+          acc = dot2(as_bf16x2(x[4 * j]), b0, acc);
+          acc = dot2(as_bf16x2(x[4 * j + 1]), b1, acc);
+          acc = dot2(as_bf16x2(x[4 * j + 2]), b2, acc);
+          acc = dot2(as_bf16x2(x[4 * j + 3]), b3, acc);
         }
-        const float z = half_bits(cur.z[u]);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) v[t][u] = s * fmaf(-z, xsum[t], acc[t]);
+        v[u] = s * fmaf(-half_bits(cur.z[u]), xsum, acc);
       }
     }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const float sum = wave_sum4(v[t]);
-      const int lr = lane >> 4, u = ((lr & 1) << 1) | (lr >> 1);
-      if ((lane & 15) == 0) red[((rg * rpw + r + u) * ks + seg) * MT + t] = sum;
-    }
+    const float sum = wave_sum4(v);
+    const int lr = lane >> 4, u = ((lr & 1) << 1) | (lr >> 1);
+    if ((lane & 15) == 0) red[(rg * rpw + r + u) * ks + seg] = sum;
     cur = nxt;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < rows * MT; e += blockDim.x) {
-    const int row = e % rows, t = e / rows;
+  for (int row = threadIdx.x; row < rows; row += blockDim.x) {
     const int64_t n = (int64_t)blockIdx.x * rows + row;
     float v = 0.0f;
-    for (int s = 0; s < ks; ++s) v += red[(row * ks + s) * MT + t];
-    if (t < a.m && n < a.n) {
-      if constexpr (I8) v *= a.sx[t];
-      a.y[(int64_t)t * a.n + n] = v;
-    }
+    for (int s = 0; s < ks; ++s) v += red[row * ks + s];
+    if constexpr (I8) v *= a.sx[0];
+    if (n < a.n) a.y[n] = v;
   }
 }
 
-// A workgroup's waves hold a whole row of X: 16 of them for one token, 8 for more.
-inline bool dot_takes(int64_t m, int64_t k) {
-  return (m == 1 && k <= 16 * RUN) || (m <= 4 && k <= 8 * RUN);
-}
+// One token, and a row of X that 16 waves hold.
+inline bool dot_takes(int64_t m, int64_t k) { return m == 1 && k <= 16 * RUN; }
 
-// Rows per wave: few enough that the launch has some 4096 waves.
-template <bool I8, int MT>
-hipError_t dot_launch_t(const VecArgs& a, int G, hipStream_t stream) {
+// Rows per wave: few enough that the launch has some 8192 waves' rows at once.
+template <bool I8>
+hipError_t dot_launch(const VecArgs& a, int G, hipStream_t stream) {
   const int ks = (int)ceil_div(a.k, RUN), rgs = ks >= 8 ? 1 : 8 / ks;
   int rpw = 4;
   while (rpw < 32 && (int64_t)a.n * ks / rpw > 8192) rpw *= 2;
   const int rows = rgs * rpw;
-  hipLaunchKernelGGL((w4_dot_kernel<I8, MT>), dim3((unsigned)ceil_div(a.n, rows)),
-                     dim3(64 * ks * rgs), (size_t)rows * ks * MT * sizeof(float), stream, a,
-                     G == 0 ? a.k : G, ks, rpw);
+  hipLaunchKernelGGL((w4_dot_kernel<I8>), dim3((unsigned)ceil_div(a.n, rows)), dim3(64 * ks * rgs),
+                     (size_t)rows * ks * sizeof(float), stream, a, G == 0 ? a.k : G, ks, rpw);
   return hipGetLastError();
-}
-
-template <bool I8>
-hipError_t dot_launch(const VecArgs& a, int G, hipStream_t stream) {
-  if (a.m == 1) return dot_launch_t<I8, 1>(a, G, stream);
-  if (a.m == 2) return dot_launch_t<I8, 2>(a, G, stream);
-  return dot_launch_t<I8, 4>(a, G, stream);
 }
 
 }  // namespace w4vec

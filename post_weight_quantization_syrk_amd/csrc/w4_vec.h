@@ -18,6 +18,7 @@
 #include "common.h"
 
 #include <hip/hip_fp16.h>
+#include <algorithm>
 #include <type_traits>
 
 namespace gptq {
@@ -38,6 +39,7 @@ struct VecArgs {
   int64_t ldx;          // bytes
   int m, n, k, ng;
   int vec;              // scales (and zeros) that one aligned load may take: 1, 2, 4 or 8
+  int splits, per_split;  // of the row's blocks of 512 k over workgroups
 };
 
 // The most that divides a row of scales and its addresses.
@@ -56,15 +58,6 @@ template <>
 struct Types<true> {
   typedef i32x4 acc_t;
 };
-
-// word j of lane quarter h <-> word h of lane quarter j
-__device__ __forceinline__ void transpose4(uint32_t w[4]) {
-  u32x2 a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-  u32x2 b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-  u32x2 lo = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  u32x2 hi = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  w[0] = lo[0], w[1] = lo[1], w[2] = hi[0], w[3] = hi[1];
-}
 
 // The codes of a word as bytes in their order.
 __device__ __forceinline__ uint2 code_bytes(uint32_t w) {
@@ -118,6 +111,14 @@ __device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
                    : "memory", "m0");
 }
 
+constexpr int LDS_BYTES = 160 * 1024;
+
+// LDS of a wave: two steps' words and tokens, and a word with the scale and
+// zero of each row and group of a block.
+constexpr int wave_bytes(bool i8, int nt, int r, int G) {
+  return 2 * (1024 * r + 16 * nt * KCH * (i8 ? 1 : 2)) + (G == 0 ? 0 : KBLK / G * 16 * r * 4);
+}
+
 template <bool I8, int NT, int R, int G>
 struct Shape {
   static constexpr int XB = I8 ? 1 : 2;
@@ -125,10 +126,9 @@ struct Shape {
   static constexpr int XBYTES = 16 * NT * KCH * XB;   // a step's tokens
   static constexpr int STAGE = WBYTES + XBYTES;
   static constexpr int GPB = G == 0 ? 0 : KBLK / G;   // groups per block
-  static constexpr int SCBYTES = GPB * 16 * R * 4;    // scale and zero of each
-  static constexpr int WAVE = 2 * STAGE + SCBYTES;    // LDS of a wave
-  static constexpr int WAVES = 8 * WAVE <= 160 * 1024 ? 8 : 4;
-  static_assert(WAVES * WAVE <= 160 * 1024, "LDS");
+  static constexpr int WAVE = wave_bytes(I8, NT, R, G);
+  static constexpr int WAVES = 8 * WAVE <= LDS_BYTES ? 8 : 4;
+  static_assert(WAVES * WAVE <= LDS_BYTES, "LDS");
   static_assert(WAVE >= R * NT * 4 * 256, "the wave's sums reuse its buffers");
 };
 
@@ -153,11 +153,14 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
 
   // steps of this wave: blocks wave, wave + waves, ...; only the row's last
   // block may hold fewer than four
-  const int nch = (a.k + KCH - 1) / KCH, nblk = (nch + 3) / 4;
+  const int nch = (a.k + KCH - 1) / KCH, b0 = blockIdx.y * a.per_split;
+  const int nblk = min((nch + 3) / 4 - b0, a.per_split);
   const int nb = wave < nblk ? (nblk - 1 - wave) / waves + 1 : 0;
-  const bool has_last = nb > 0 && wave + waves * (nb - 1) == nblk - 1;
-  const int nst = 4 * nb - (has_last ? 4 * nblk - nch : 0);
-  auto chunk = [&](int i) __attribute__((always_inline)) { return 4 * (wave + waves * (i >> 2)) + (i & 3); };
+  const bool has_last = nb > 0 && 4 * (b0 + wave + waves * (nb - 1)) + 4 > nch;
+  const int nst = 4 * nb - (has_last ? 4 - nch % 4 : 0);
+  auto chunk = [&](int i) __attribute__((always_inline)) {
+    return 4 * (b0 + wave + waves * (i >> 2)) + (i & 3);
+  };
 
   // Direct loads.  Weights: 16 rows of 64 bytes, unit u of row r at u ^ (r / 4
   // mod 4).  Tokens: rows of 128 XB bytes, unit u of token t at u ^ (t mod 16)
@@ -279,9 +282,15 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
     uint32_t w[R][4];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const uint4 v = *(const uint4*)(st + 1024 * r + 64 * l16 + 16 * (h ^ ((l16 >> 2) & 3)));
-      w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
-      if constexpr (TR) transpose4(w[r]);
+      const char* p = st + 1024 * r + 64 * l16;
+      if constexpr (TR) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[r][j] = *(const uint32_t*)(p + 16 * (j ^ ((l16 >> 2) & 3)) + 4 * h);
+      } else {
+        const uint4 v = *(const uint4*)(p + 16 * (h ^ ((l16 >> 2) & 3)));
+        w[r][0] = v.x, w[r][1] = v.y, w[r][2] = v.z, w[r][3] = v.w;
+      }
     }
     acc_t one[NT], acc[R][NT];
     auto sz_of = [&](int r, int g) __attribute__((always_inline)) {
@@ -428,19 +437,39 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
     const int i = e & 3, t = (e >> 2) % NT, r = (e >> 2) / NT;
     const int token = 16 * t + 4 * h + i, n = n0 + 16 * r + l16;
     if (token < a.m && n < a.n) {
-      if constexpr (I8) v *= a.sx[token];
-      a.y[(int64_t)token * a.n + n] = v;
+      if (I8 && a.splits == 1) v *= a.sx[token];
+      a.y[((int64_t)blockIdx.y * a.m + token) * a.n + n] = v;
     }
   }
+}
+
+// Y = the splits' products added in split order, times sx where there is one.
+// (static: each source that includes this has its own)
+static __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ part,
+                                                          const float* __restrict__ sx, int64_t m,
+                                                          int n, int splits,
+                                                          float* __restrict__ y) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= m * n) return;
+  float v = part[e];
+  for (int s = 1; s < splits; ++s) v += part[s * m * n + e];
+  y[e] = sx ? sx[e / n] * v : v;
+}
+
+inline hipError_t join_launch(const float* part, const float* sx, int64_t m, int n, int splits,
+                              float* y, hipStream_t stream) {
+  hipLaunchKernelGGL(join_kernel, dim3((unsigned)ceil_div(m * n, 256)), dim3(256), 0, stream, part,
+                     sx, m, n, splits, y);
+  return hipGetLastError();
 }
 
 template <bool I8, int NT, int R, int G>
 hipError_t vec_launch_one(const VecArgs& a, hipStream_t stream) {
   typedef Shape<I8, NT, R, G> S;
   int waves = 1;  // no more than there are blocks
-  while (waves < S::WAVES && waves * KBLK < a.k) waves *= 2;
+  while (waves < S::WAVES && waves < a.per_split) waves *= 2;
   const size_t lds = (size_t)waves * S::WAVE;
-  hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G>), dim3((unsigned)ceil_div(a.n, 16 * R)),
+  hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G>), dim3((unsigned)ceil_div(a.n, 16 * R), a.splits),
                      dim3(64 * waves), lds, stream, a);
   return hipGetLastError();
 }
@@ -455,26 +484,58 @@ hipError_t vec_launch_g(const VecArgs& a, int G, hipStream_t stream) {
   }
 }
 
-// Weight rows per workgroup.  More of them read X fewer times, fewer of them
-// use more CUs: 64 while that leaves some 160 workgroups (16 tokens through
-// 11008 x 4096: 11.6 us, against 14.4 and 16.6 us with 32 and 16), else 16
-// while they find room at once on 256 CUs (4096 x 4096: 5.8 us, against 6.7
-// and 8.9 us with 32 and 64), else 32 (37 tokens through 4099 x 11008 in 8
-// bits: 26 us, against 36 us with 16, whose 257th workgroup waits).
+struct VecPlan {
+  int r;  // tiles of 16 weight rows per workgroup
+  int splits, per_split;
+  size_t ws_bytes;
+};
+
+// Weight rows per workgroup: more of them read X fewer times, fewer of them use
+// more CUs.  64 while that leaves some 160 workgroups (16 tokens through 11008
+// x 4096: 11.4 us, against 14.3 and 16.6 us with 32 and 16), else 16 while they
+// find room at once on 256 CUs (4096 x 4096: 5.8 us, against 6.7 and 8.9 us),
+// else 32 (37 tokens through 4099 x 11008 in 8 bits: 26 us, against 36 us with
+// 16, whose 257th workgroup waits).
+// The row's k go to several workgroups where that leaves CUs idle and a wave
+// has more than one block of k: a second launch adds their sums (some 2.5 us;
+// 64 tokens through 1024 x 8192: 12.1 us with four, 24.5 us with one).  With
+// more than 32 bf16 tokens, which take most of LDS, 32 rows in two splits beat
+// 16 in one (4096 x 11008: 31 and 46 us; 4096 x 4096: 14.7 and 14.8 us).
+inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
+  VecPlan p;
+  const int nt = (int)ceil_div(m, 16);
+  const bool big_x = !i8 && nt > 2;
+  p.r = n >= 160 * 64 ? (big_x ? 2 : 4) : n <= 256 * 16 && !(big_x && n > 2048) ? 1 : 2;
+  const int nblk = (int)ceil_div(k, KBLK);
+  const int waves = 8 * wave_bytes(i8, nt, p.r, G) <= LDS_BYTES ? 8 : 4;
+  const int64_t idle = 256 / ceil_div(n, 16 * p.r);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(idle, ceil_div(nblk, waves)));
+  p.per_split = (int)ceil_div(nblk, p.splits);
+  p.splits = (int)ceil_div(nblk, p.per_split);
+  p.ws_bytes = p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
+  return p;
+}
+
 template <bool I8, int NT>
-hipError_t vec_launch_t(const VecArgs& a, int G, hipStream_t stream) {
-  constexpr int RMAX = !I8 && NT > 2 ? 2 : 4;  // what fits LDS with four waves
-  if (a.n >= 160 * 64) return vec_launch_g<I8, NT, RMAX>(a, G, stream);
-  if (a.n <= 256 * 16) return vec_launch_g<I8, NT, 1>(a, G, stream);
-  return vec_launch_g<I8, NT, 2>(a, G, stream);
+hipError_t vec_launch_t(const VecArgs& a, int r, int G, hipStream_t stream) {
+  constexpr int RMAX = !I8 && NT > 2 ? 2 : 4;
+  if (r == 4) return vec_launch_g<I8, NT, RMAX>(a, G, stream);
+  if (r == 2) return vec_launch_g<I8, NT, 2>(a, G, stream);
+  return vec_launch_g<I8, NT, 1>(a, G, stream);
 }
 
 template <bool I8>
-hipError_t vec_launch(const VecArgs& a, int G, hipStream_t stream) {
-  if (a.m <= 16) return vec_launch_t<I8, 1>(a, G, stream);
-  if (a.m <= 32) return vec_launch_t<I8, 2>(a, G, stream);
-  if (a.m <= 48) return vec_launch_t<I8, 3>(a, G, stream);
-  return vec_launch_t<I8, 4>(a, G, stream);
+hipError_t vec_launch(VecArgs a, int G, void* ws, hipStream_t stream) {
+  const VecPlan p = vec_plan(I8, a.m, a.n, a.k, G);
+  float* const y = a.y;
+  if (p.splits > 1) a.y = (float*)ws;
+  a.splits = p.splits, a.per_split = p.per_split;
+  hipError_t e = a.m <= 16   ? vec_launch_t<I8, 1>(a, p.r, G, stream)
+                 : a.m <= 32 ? vec_launch_t<I8, 2>(a, p.r, G, stream)
+                 : a.m <= 48 ? vec_launch_t<I8, 3>(a, p.r, G, stream)
+                             : vec_launch_t<I8, 4>(a, p.r, G, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return join_launch(a.y, I8 ? a.sx : nullptr, a.m, a.n, p.splits, y, stream);
 }
 
 }  // namespace w4vec

@@ -331,17 +331,6 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
     }
 }
 
-// Y = sx times the splits' products, added in split order.
-__global__ __launch_bounds__(256) void w4a8_join_kernel(const float* __restrict__ part,
-                                                        const float* __restrict__ sx, int64_t M,
-                                                        int N, int splits, float* __restrict__ Y) {
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (e >= M * N) return;
-  float v = part[e];
-  for (int s = 1; s < splits; ++s) v += part[s * M * N + e];
-  Y[e] = sx[e / N] * v;
-}
-
 struct Plan {
   int mi, splits, per_split;
   Layout l;
@@ -377,7 +366,9 @@ void launch(const MulArgs& a, int G, hipStream_t stream) {
 }  // namespace
 
 size_t w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
-  return m <= VEC_M ? 0 : plan_for(m, d_out, d_in, group_size).bytes;
+  if (m > VEC_M) return plan_for(m, d_out, d_in, group_size).bytes;
+  const int G = group_size == -1 ? 0 : group_size;
+  return w4vec::dot_takes(m, d_in) ? 0 : w4vec::vec_plan(true, m, d_out, d_in, G).ws_bytes;
 }
 
 hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_t ldx,
@@ -392,7 +383,7 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
     v.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
     v.vec = w4vec::scale_vec(scales_f16, zeros_f16, v.ng);
     return w4vec::dot_takes(m, d_in) ? w4vec::dot_launch<true>(v, G, stream)
-                                     : w4vec::vec_launch<true>(v, G, stream);
+                                     : w4vec::vec_launch<true>(v, G, ws, stream);
   }
   const Plan p = plan_for(m, d_out, d_in, group_size);
   const int vec = w4vec::scale_vec(scales_f16, zeros_f16, p.l.ng);
@@ -415,9 +406,7 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
   }
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  hipLaunchKernelGGL(w4a8_join_kernel, dim3((unsigned)ceil_div(m * d_out, 256)), dim3(256), 0,
-                     stream, a.y, x_scales, m, (int)d_out, p.splits, Y);
-  return hipGetLastError();
+  return w4vec::join_launch(a.y, x_scales, m, (int)d_out, p.splits, Y, stream);
 }
 
 }  // namespace gptq

@@ -72,7 +72,8 @@ def lib() -> ctypes.CDLL:
         "gptq_pack": (I, [P, P, P, I64, I64, I, I, I, P, P, P, P]),
         "gptq2d_round": (I, [P, P, P, I64, P, P, SZ, P]),
         "gptq_w4a16_matmul": (I, [P, I64, I64, P, P, P, I64, I64, I, I, P, P]),
-        "gptq_w4a16_matvec": (I, [P, I64, I64, P, P, P, I64, I64, I, I, P, P]),
+        "gptq_w4a16_matvec": (I, [P, I64, I64, P, P, P, I64, I64, I, I, P, P, SZ, P]),
+        "gptq_w4a16_matvec_workspace": (SZ, [I64, I64, I64, I]),
         "gptq_w4a8_matmul": (I, [P, P, I64, I64, P, P, P, I64, I64, I, I, P, P, SZ, P]),
         "gptq_w4a8_workspace": (SZ, [I64, I64, I64, I]),
         "gptq_add_rmsnorm": (I, [P, I, I64, P, I, I64, P, I64, P, I, D, I64, I64, P, I, I64, P,
@@ -489,6 +490,19 @@ def _flat(where: str, name: str, t: torch.Tensor, shape, dtypes, index: int):
                          f"{t.device}")
 
 
+def _scratch(where: str, ws, nbytes: int, X: torch.Tensor, stream):
+    """The caller's workspace, or one of the call's own where it needs any."""
+    if ws is None:
+        return _workspace(nbytes, X.device, stream)
+    if ws.device != X.device or not ws.is_contiguous():
+        raise ValueError(f"{where}: ws must be contiguous on {X.device}")
+    return ws
+
+
+def _span(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
 def _w4_checks(where, X, index, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream):
     """The packed weights' shapes against X's; returns (m, d_in, d_out, ldx, Y).  A group
     size that the library refuses is left to it: it reads nothing then."""
@@ -511,18 +525,25 @@ def _w4_checks(where, X, index, qweight, scales_f16, zeros_f16, group_size, sym,
     return m, d_in, d_out, X.stride(0) if m > 1 else d_in, Y
 
 
+@functools.lru_cache(maxsize=1024)
+def gptq_w4a16_matvec_workspace(m: int, d_out: int, d_in: int, group_size: int) -> int:
+    return int(lib().gptq_w4a16_matvec_workspace(m, d_out, d_in, group_size))
+
+
 def gptq_w4a16_matvec(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.Tensor,
                       zeros_f16: torch.Tensor | None, *, group_size: int, sym: bool,
-                      Y: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                      Y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
     """gptq_w4a16_matmul for the rows of a few tokens (m <= GPTQ_MATVEC_MAX_M), any d_in that is a
     multiple of 32: Y [m, d_out] fp32 = X [m, d_in] bf16 times the dequantized weights transposed."""
     where = "gptq_w4a16_matvec"
     index = _index(where, X, (torch.bfloat16,))
     m, d_in, d_out, ldx, Y = _w4_checks(where, X, index, qweight, scales_f16, zeros_f16,
                                         group_size, sym, Y, stream)
+    ws = _scratch(where, ws, gptq_w4a16_matvec_workspace(m, d_out, d_in, group_size), X, stream)
     _call(where, index, stream, X.data_ptr(), m, ldx, qweight.data_ptr(), scales_f16.data_ptr(),
           None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size, 1 if sym else 0,
-          Y.data_ptr())
+          Y.data_ptr(), *_span(ws))
     return Y
 
 
@@ -542,14 +563,10 @@ def gptq_w4a8_matmul(X: torch.Tensor, x_scales: torch.Tensor, qweight: torch.Ten
     m, d_in, d_out, ldx, Y = _w4_checks(where, X, index, qweight, scales_f16, zeros_f16,
                                         group_size, sym, Y, stream)
     _flat(where, "x_scales", x_scales, (m,), (torch.float32,), index)
-    if ws is None:
-        ws = _workspace(gptq_w4a8_workspace(m, d_out, d_in, group_size), X.device, stream)
-    elif ws.get_device() != index or not ws.is_contiguous():
-        raise ValueError(f"{where}: ws must be contiguous on GPU {index}")
+    ws = _scratch(where, ws, gptq_w4a8_workspace(m, d_out, d_in, group_size), X, stream)
     _call(where, index, stream, X.data_ptr(), x_scales.data_ptr(), m, ldx, qweight.data_ptr(),
           scales_f16.data_ptr(), None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size,
-          1 if sym else 0, Y.data_ptr(), None if ws is None else ws.data_ptr(),
-          0 if ws is None else ws.numel() * ws.element_size())
+          1 if sym else 0, Y.data_ptr(), *_span(ws))
     return Y
 
 

@@ -37,15 +37,21 @@ int main() {
   auto* x8 = (int8_t*)p;
   const int64_t big = std::numeric_limits<int64_t>::max();
   // a few tokens
-  EXPECT(gptq_w4a16_matvec(p, 1, 256, q, h, h, 8, 256, 128, 0, f, nullptr), GPTQ_OK, 1);
-  EXPECT(gptq_w4a16_matvec(p, 64, 256, q, h, nullptr, 8, 256, -1, 1, f, nullptr), GPTQ_OK, 1);
-  EXPECT(gptq_w4a16_matvec(p, 0, 256, q, h, h, 8, 256, 128, 0, f, nullptr), GPTQ_OK, 0);
-  EXPECT(gptq_w4a16_matvec(p, 65, 256, q, h, h, 8, 256, 128, 0, f, nullptr), GPTQ_EUNSUPPORTED, 0);
-  EXPECT(gptq_w4a16_matvec(p, 1, 256, q, h, nullptr, 8, 256, 128, 0, f, nullptr), GPTQ_EINVAL, 0);
-  EXPECT(gptq_w4a16_matvec(p, 1, big, q, h, h, 8, 256, 128, 0, f, nullptr), GPTQ_EINVAL, 0);
-  EXPECT(gptq_w4a16_matvec(p, big, 256, q, h, h, 8, 256, 128, 0, f, nullptr), GPTQ_EINVAL, 0);
-  EXPECT(gptq_w4a16_matvec(p, 1, 256, q, h, h, big, 256, 128, 0, f, nullptr), GPTQ_EINVAL, 0);
-  EXPECT(gptq_w4a16_matvec(p, 1, 256, q, h, h, 8, big, 128, 0, f, nullptr), GPTQ_EINVAL, 0);
+  EXPECT(gptq_w4a16_matvec(p, 1, 256, q, h, h, 8, 256, 128, 0, f, nullptr, 0, nullptr), GPTQ_OK, 1);
+  EXPECT(gptq_w4a16_matvec(p, 64, 256, q, h, nullptr, 8, 256, -1, 1, f, p, 2048, nullptr), GPTQ_OK, 1);
+  EXPECT(gptq_w4a16_matvec(p, 64, 256, q, h, nullptr, 8, 256, -1, 1, f, p, 2047, nullptr), GPTQ_EINVAL, 0);
+  EXPECT(gptq_w4a16_matvec(p, 64, 256, q, h, nullptr, 8, 256, -1, 1, f, nullptr, 2048, nullptr), GPTQ_EINVAL, 0);
+  EXPECT(gptq_w4a16_matvec(p, 64, 256, q, h, nullptr, 8, 256, -1, 1, f, buf + 128, 2048, nullptr), GPTQ_EINVAL, 0);
+  EXPECT((int)gptq_w4a16_matvec_workspace(64, 8, 256, 32), 2048, 0);
+  EXPECT((int)gptq_w4a16_matvec_workspace(65, 8, 256, 32), 0, 0);
+  EXPECT((int)gptq_w4a16_matvec_workspace(64, 8, 250, 32), 0, 0);
+  EXPECT(gptq_w4a16_matvec(p, 0, 256, q, h, h, 8, 256, 128, 0, f, nullptr, 0, nullptr), GPTQ_OK, 0);
+  EXPECT(gptq_w4a16_matvec(p, 65, 256, q, h, h, 8, 256, 128, 0, f, nullptr, 0, nullptr), GPTQ_EUNSUPPORTED, 0);
+  EXPECT(gptq_w4a16_matvec(p, 1, 256, q, h, nullptr, 8, 256, 128, 0, f, nullptr, 0, nullptr), GPTQ_EINVAL, 0);
+  EXPECT(gptq_w4a16_matvec(p, 1, big, q, h, h, 8, 256, 128, 0, f, nullptr, 0, nullptr), GPTQ_EINVAL, 0);
+  EXPECT(gptq_w4a16_matvec(p, big, 256, q, h, h, 8, 256, 128, 0, f, nullptr, 0, nullptr), GPTQ_EINVAL, 0);
+  EXPECT(gptq_w4a16_matvec(p, 1, 256, q, h, h, big, 256, 128, 0, f, nullptr, 0, nullptr), GPTQ_EINVAL, 0);
+  EXPECT(gptq_w4a16_matvec(p, 1, 256, q, h, h, 8, big, 128, 0, f, nullptr, 0, nullptr), GPTQ_EINVAL, 0);
   // 8-bit activations
   EXPECT(gptq_w4a8_matmul(x8, f, 1, 256, q, h, h, 8, 256, 32, 0, f, nullptr, 0, nullptr), GPTQ_OK, 1);
   EXPECT(gptq_w4a8_matmul(x8, f, 200, 256, q, h, h, 8, 256, 32, 0, f, p, 4096, nullptr), GPTQ_OK, 1);

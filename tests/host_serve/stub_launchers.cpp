@@ -19,10 +19,15 @@ bool to(const void* p, size_t n) { return p && (uintptr_t)p % n == 0; }
 
 namespace gptq {
 
+size_t w4a16_vec_workspace(int64_t m, int64_t d_out, int64_t d_in, int) {
+  need(m > 0 && m <= 64 && d_out > 0 && d_in > 0, "w4a16_vec_workspace sizes");
+  return m > 32 ? 2048 : 0;
+}
 hipError_t w4a16_vec_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
                             const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
-                            int64_t d_in, int group_size, float* Y, hipStream_t) {
+                            int64_t d_in, int group_size, float* Y, void* ws, hipStream_t) {
   need(to(X, 16) && to(qweight, 16) && to(scales_f16, 2) && to(Y, 4), "w4a16_vec pointers");
+  need(m <= 32 || to(ws, 256), "workspace");
   need(m > 0 && m <= 64 && d_out > 0 && d_in > 0 && d_in % 32 == 0 && d_in <= 65536, "sizes");
   need(ldx >= d_in && ldx % 8 == 0, "ldx");
   need(group_size == -1 || d_in % group_size == 0, "group");

@@ -22,7 +22,8 @@ def L():
 
 
 def matvec(L, **kw):
-    a = dict(X=A, m=4, ldx=256, qw=A, s=A, z=A, d_out=8, d_in=256, g=128, sym=0, Y=A) | kw
+    a = dict(X=A, m=4, ldx=256, qw=A, s=A, z=A, d_out=8, d_in=256, g=128, sym=0, Y=A,
+             ws=A, ws_bytes=1 << 40) | kw
     return L.gptq_w4a16_matvec(*a.values(), None)
 
 
@@ -74,18 +75,25 @@ def test_products_own_refusals(L):
     assert gptq.gptq_w4a8_workspace(4, 0, 256, 128) == 0
 
 
-def test_w4a8_workspace_is_required_where_it_is_reported(L):
-    asked = 0
-    for m in (1, 16, 64, 100, 300, 515, 1000, 4096):
-        for d_out, d_in in ((64, 4096), (4096, 4096), (4099, 11008), (11008, 4096)):
-            need = gptq.gptq_w4a8_workspace(m, d_out, d_in, 128 if d_in % 128 == 0 else 32)
+@pytest.mark.parametrize("call,query,ms", [
+    (matvec, gptq.gptq_w4a16_matvec_workspace, (1, 2, 5, 16, 17, 40, 64)),
+    (w4a8, gptq.gptq_w4a8_workspace, (1, 2, 16, 40, 64, 65, 100, 300, 515, 1000, 4096)),
+])
+def test_workspace_is_required_where_it_is_reported(L, call, query, ms):
+    asked = shapes = 0
+    for m in ms:
+        for d_out, d_in in ((64, 4096), (512, 12288), (4096, 4096), (4099, 11008), (11008, 4096)):
+            need = query(m, d_out, d_in, 128 if d_in % 128 == 0 else 32)
+            shapes += 1
             asked += need > 0
             if need:
                 kw = dict(m=m, d_out=d_out, d_in=d_in, ldx=d_in)
-                assert w4a8(L, **kw, ws_bytes=need - 1) == EINVAL
-                assert w4a8(L, **kw, ws=None, ws_bytes=need) == EINVAL
-                assert w4a8(L, **kw, ws=A + 64, ws_bytes=need) == EINVAL
-    print(f"{asked} of 32 shapes ask for a workspace")
+                assert call(L, **kw, ws_bytes=need - 1) == EINVAL
+                assert call(L, **kw, ws=None, ws_bytes=need) == EINVAL
+                assert call(L, **kw, ws=A + 64, ws_bytes=need) == EINVAL
+    print(f"{asked} of {shapes} shapes ask for a workspace")
+    assert asked
+    assert query(0, 64, 4096, 128) == 0 and query(4, 64, 4000, 128) == 0
 
 
 NORM = [
