@@ -127,7 +127,7 @@ struct Shape {
   static constexpr int STAGE = WBYTES + XBYTES;
   static constexpr int GPB = G == 0 ? 0 : KBLK / G;   // groups per block
   static constexpr int WAVE = wave_bytes(I8, NT, R, G);
-  static constexpr int WAVES = 8 * WAVE <= LDS_BYTES ? 8 : 4;
+  static constexpr int WAVES = LDS_BYTES / WAVE < 8 ? LDS_BYTES / WAVE : 8;
   static_assert(WAVES * WAVE <= LDS_BYTES, "LDS");
   static_assert(WAVE >= R * NT * 4 * 256, "the wave's sums reuse its buffers");
 };
@@ -466,8 +466,7 @@ inline hipError_t join_launch(const float* part, const float* sx, int64_t m, int
 template <bool I8, int NT, int R, int G>
 hipError_t vec_launch_one(const VecArgs& a, hipStream_t stream) {
   typedef Shape<I8, NT, R, G> S;
-  int waves = 1;  // no more than there are blocks
-  while (waves < S::WAVES && waves < a.per_split) waves *= 2;
+  const int waves = std::min(S::WAVES, a.per_split);  // no more than there are blocks
   const size_t lds = (size_t)waves * S::WAVE;
   hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G>), dim3((unsigned)ceil_div(a.n, 16 * R), a.splits),
                      dim3(64 * waves), lds, stream, a);
@@ -500,14 +499,14 @@ struct VecPlan {
 // has more than one block of k: a second launch adds their sums (some 2.5 us;
 // 64 tokens through 1024 x 8192: 12.1 us with four, 24.5 us with one).  With
 // more than 32 bf16 tokens, which take most of LDS, 32 rows in two splits beat
-// 16 in one (4096 x 11008: 31 and 46 us; 4096 x 4096: 14.7 and 14.8 us).
+// 16 in one (4096 x 11008: 30 and 45 us; 4096 x 4096: 14.8 and 14.7 us).
 inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
   VecPlan p;
   const int nt = (int)ceil_div(m, 16);
   const bool big_x = !i8 && nt > 2;
-  p.r = n >= 160 * 64 ? (big_x ? 2 : 4) : n <= 256 * 16 && !(big_x && n > 2048) ? 1 : 2;
+  p.r = n >= 160 * 64 ? 4 : n <= 256 * 16 && !(big_x && n > 2048) ? 1 : 2;
   const int nblk = (int)ceil_div(k, KBLK);
-  const int waves = 8 * wave_bytes(i8, nt, p.r, G) <= LDS_BYTES ? 8 : 4;
+  const int waves = std::min(8, LDS_BYTES / wave_bytes(i8, nt, p.r, G));
   const int64_t idle = 256 / ceil_div(n, 16 * p.r);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(idle, ceil_div(nblk, waves)));
   p.per_split = (int)ceil_div(nblk, p.splits);
@@ -518,8 +517,7 @@ inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
 
 template <bool I8, int NT>
 hipError_t vec_launch_t(const VecArgs& a, int r, int G, hipStream_t stream) {
-  constexpr int RMAX = !I8 && NT > 2 ? 2 : 4;
-  if (r == 4) return vec_launch_g<I8, NT, RMAX>(a, G, stream);
+  if (r == 4) return vec_launch_g<I8, NT, 4>(a, G, stream);
   if (r == 2) return vec_launch_g<I8, NT, 2>(a, G, stream);
   return vec_launch_g<I8, NT, 1>(a, G, stream);
 }

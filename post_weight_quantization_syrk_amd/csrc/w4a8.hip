@@ -14,7 +14,13 @@ typedef __attribute__((ext_vector_type(4))) int i32x4;
 typedef __attribute__((ext_vector_type(16))) int i32x16;
 
 constexpr int KCH = 128;           // k per chunk (bytes of a row of X, twice those of a weight row)
-constexpr int VEC_M = 64;          // up to here w4_vec.h's kernel
+
+// Where the kernels for a few tokens take over from the tiles below: 48 tokens
+// through 11008 x 4096 take 19.3 us there and 19.6 us here, 64 take 24 and 19.6
+// us; with fewer weight rows the tiles' two launches cost more than they save
+// (64 through 4096 x 4096: 8.2 and 14.0 us).
+bool few_tokens(int64_t m, int64_t d_out) { return m <= 48 || (m <= 64 && d_out <= 8192); }
+
 constexpr int PANEL = 32 * KCH;    // bytes of a panel: 32 rows of one chunk
 constexpr int TN = 128;            // weight rows of a tile
 constexpr int NST = 2;             // chunks in LDS
@@ -366,7 +372,7 @@ void launch(const MulArgs& a, int G, hipStream_t stream) {
 }  // namespace
 
 size_t w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
-  if (m > VEC_M) return plan_for(m, d_out, d_in, group_size).bytes;
+  if (!few_tokens(m, d_out)) return plan_for(m, d_out, d_in, group_size).bytes;
   const int G = group_size == -1 ? 0 : group_size;
   return w4vec::dot_takes(m, d_in) ? 0 : w4vec::vec_plan(true, m, d_out, d_in, G).ws_bytes;
 }
@@ -376,7 +382,7 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
                        const uint16_t* zeros_f16, int64_t d_out, int64_t d_in, int group_size,
                        float* Y, void* ws, hipStream_t stream) {
   const int G = group_size == -1 ? 0 : group_size;
-  if (m <= VEC_M) {
+  if (few_tokens(m, d_out)) {
     w4vec::VecArgs v;
     v.x = (const char*)X, v.sx = x_scales, v.q = qweight, v.s16 = scales_f16, v.z16 = zeros_f16;
     v.y = Y, v.ldx = ldx, v.m = (int)m, v.n = (int)d_out, v.k = (int)d_in;
