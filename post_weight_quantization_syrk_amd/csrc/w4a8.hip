@@ -22,7 +22,6 @@ constexpr int KCH = 128;           // k per chunk (bytes of a row of X, twice th
 bool few_tokens(int64_t m, int64_t d_out) { return m <= 48 || (m <= 64 && d_out <= 8192); }
 
 constexpr int PANEL = 32 * KCH;    // bytes of a panel: 32 rows of one chunk
-constexpr int TN = 128;            // weight rows of a tile
 constexpr int NST = 2;             // chunks in LDS
 
 // Where the product's tiles are in the workspace: X as panels of 32 rows by
@@ -37,11 +36,11 @@ struct Layout {
   size_t bytes;
 };
 
-Layout layout_of(int64_t m, int64_t d_out, int64_t d_in, int group_size, int tm) {
+Layout layout_of(int64_t m, int64_t d_out, int64_t d_in, int group_size, int tm, int tn) {
   Layout l;
   l.nch = (int)ceil_div(d_in, KCH);
   l.rows = ceil_div(m, tm) * tm;
-  l.cols = ceil_div(d_out, TN) * TN;
+  l.cols = ceil_div(d_out, tn) * tn;
   l.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
   l.sz_off = (size_t)l.rows * l.nch * KCH;
   l.bytes = l.sz_off + (size_t)l.ng * l.cols * 4;
@@ -148,13 +147,13 @@ struct MulArgs {
 // Four waves side by side, each 32 MI rows of X by 32 weight rows: a wave
 // takes the codes of its own weight rows apart, and none twice.  G: group
 // size, 0 for one group per row.
-template <int MI, int G>
+template <int MI, int NI, int G>
 __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
-  constexpr int TM = 32 * MI;
+  constexpr int TM = 32 * MI, TN = 128 * NI;
   constexpr int GPC = G == 0 ? 0 : KCH / G;  // groups per chunk
   constexpr int ABYTES = TM * KCH, BBYTES = TN * (KCH / 2), SZBYTES = GPC * TN * 4;
   constexpr int STAGE = ABYTES + BBYTES + SZBYTES;
-  constexpr int LOADS = MI + 2 + GPC;        // direct loads of a wave per chunk
+  constexpr int LOADS = MI + 2 * NI + GPC;        // direct loads of a wave per chunk
   __shared__ __attribute__((aligned(1024))) char lds[NST * STAGE];
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -177,11 +176,11 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
   // row's 64 bytes of a chunk go to units that put 16 rows on different banks
   const char* xbase = a.ws + (m0 >> 5) * nch * PANEL;
   const char* qbase = (const char*)a.q + (int64_t)n0 * a.row_bytes;
-  const uint32_t* sz = (const uint32_t*)(a.ws + a.l.sz_off) + n0 + 32 * wave;
-  uint32_t qrow[2];
+  const uint32_t* sz = (const uint32_t*)(a.ws + a.l.sz_off) + n0 + 32 * NI * wave;
+  uint32_t qrow[2 * NI];
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-    qrow[j] = (uint32_t)min(16 * (2 * wave + j) + (lane >> 2), a.N - 1 - n0) * a.row_bytes;
+  for (int j = 0; j < 2 * NI; ++j)
+    qrow[j] = (uint32_t)min(16 * (2 * NI * wave + j) + (lane >> 2), a.N - 1 - n0) * a.row_bytes;
   const uint32_t qu = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
   auto issue = [&](int c, int buf) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + buf * STAGE;
@@ -193,23 +192,26 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
     }
     const uint32_t k = min((uint32_t)c * (KCH / 2) + qu, (uint32_t)a.row_bytes - 16);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      dma16(qbase, qrow[j] + k, dst + ABYTES + (2 * wave + j) * 1024);
+    for (int j = 0; j < 2 * NI; ++j)
+      dma16(qbase, qrow[j] + k, dst + ABYTES + (2 * NI * wave + j) * 1024);
     if constexpr (G != 0) {
-      if (lane < 8) {  // this wave's 32 words of each group
+      if (lane < 8 * NI) {  // this wave's 32 NI words of each group
 #pragma unroll
         for (int g = 0; g < GPC; ++g)
           dma16(sz + (int64_t)min(c * GPC + g, a.l.ng - 1) * a.l.cols, lane * 16,
-                dst + ABYTES + BBYTES + (g * TN + 32 * wave) * 4);
+                dst + ABYTES + BBYTES + (g * TN + 32 * NI * wave) * 4);
       }
     }
   };
-  const uint32_t row_sz = G == 0 ? sz[l32] : 0u;
-
-  f32x16 tot[G == 0 ? 1 : MI];
-  i32x16 sum[G == 0 ? MI : 1];
+  uint32_t row_sz[NI];
 #pragma unroll
-  for (int mi = 0; mi < MI; ++mi)
+  for (int ni = 0; ni < NI; ++ni) row_sz[ni] = G == 0 ? sz[32 * ni + l32] : 0u;
+
+  constexpr int BL = MI * NI;  // 32 x 32 blocks of a wave, ni the faster index
+  f32x16 tot[G == 0 ? 1 : BL];
+  i32x16 sum[G == 0 ? BL : 1];
+#pragma unroll
+  for (int mi = 0; mi < BL; ++mi)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       if constexpr (G == 0)
@@ -231,34 +233,37 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
     __syncthreads();
     if (c + NST - 1 < c1) issue(c + NST - 1, buf == 0 ? NST - 1 : buf - 1);
     const char* la = lds + buf * STAGE;
-    const char* lb = lds + buf * STAGE + ABYTES + (32 * wave + l32) * (KCH / 2);
-    const uint32_t* lz = (const uint32_t*)(lds + buf * STAGE + ABYTES + BBYTES) + 32 * wave + l32;
+    const char* lb = lds + buf * STAGE + ABYTES + (32 * NI * wave + l32) * (KCH / 2);
+    const uint32_t* lz =
+        (const uint32_t*)(lds + buf * STAGE + ABYTES + BBYTES) + 32 * NI * wave + l32;
     buf = buf == NST - 1 ? 0 : buf + 1;
     const int sw = (l32 >> 2) & 3;
-    float scale[GPC ? GPC : 1];
-    uint32_t zc[GPC ? GPC : 1];
-#pragma unroll
-    for (int g = 0; g < (GPC ? GPC : 1); ++g) {
-      const uint32_t v = G == 0 ? row_sz : lz[g * TN];
-      scale[g] = w4vec::half_bits((uint16_t)v);
-      zc[g] = __builtin_amdgcn_perm(v, v, 0x02020202u);
-      asm("" : "+v"(scale[g]));  // or every product converts it again
-    }
     // MFMA q of a chunk takes, in lane half h, unit u of X: with groups of 32
     // the two halves share 32 consecutive k, otherwise 64
-    i32x4 bf[4];
-    {
+    float scale[NI][GPC ? GPC : 1];
+    i32x4 bf[NI][4];
+#pragma unroll
+    for (int ni = 0; ni < NI; ++ni) {
+      uint32_t zc[GPC ? GPC : 1];
+#pragma unroll
+      for (int g = 0; g < (GPC ? GPC : 1); ++g) {
+        const uint32_t v = G == 0 ? row_sz[ni] : lz[g * TN + 32 * ni];
+        scale[ni][g] = w4vec::half_bits((uint16_t)v);
+        zc[g] = __builtin_amdgcn_perm(v, v, 0x02020202u);
+        asm("" : "+v"(scale[ni][g]));  // or every product converts it again
+      }
+      const char* lw = lb + 32 * ni * (KCH / 2);
       uint32_t w[8];
       if constexpr (G == 32) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const uint2 v = *(const uint2*)(lb + 16 * (q ^ sw) + 8 * h);
+          const uint2 v = *(const uint2*)(lw + 16 * (q ^ sw) + 8 * h);
           w[2 * q] = v.x, w[2 * q + 1] = v.y;
         }
       } else {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint4 v = *(const uint4*)(lb + 16 * ((2 * j + h) ^ sw));
+          const uint4 v = *(const uint4*)(lw + 16 * ((2 * j + h) ^ sw));
           w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
         }
       }
@@ -267,7 +272,7 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
         int o[4];
         minus_zero(w[2 * q], zc[q * GPC / 4], o[0], o[1]);
         minus_zero(w[2 * q + 1], zc[q * GPC / 4], o[2], o[3]);
-        bf[q] = i32x4{o[0], o[1], o[2], o[3]};
+        bf[ni][q] = i32x4{o[0], o[1], o[2], o[3]};
       }
     }
     auto xfrag = [&](int mi, int q) __attribute__((always_inline)) {
@@ -278,36 +283,43 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          sum[mi] = __builtin_amdgcn_mfma_i32_32x32x32_i8(xfrag(mi, q), bf[q], sum[mi], 0, 0, 0);
+        for (int q = 0; q < 4; ++q) {
+          const i32x4 x = xfrag(mi, q);
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni)
+            sum[mi * NI + ni] = __builtin_amdgcn_mfma_i32_32x32x32_i8(x, bf[ni][q],
+                                                                      sum[mi * NI + ni], 0, 0, 0);
+        }
     } else {
-      // step s multiplies for one block of 32 rows and one group while the
-      // step before it is scaled into its total
-      constexpr int STEPS = MI * GPC, QPS = 4 / GPC;
-      i32x4 af[2][QPS];
+      // step s multiplies for one block and one group while the step before it
+      // is scaled into its total; the steps of 32 rows follow one another
+      constexpr int PER = NI * GPC, STEPS = MI * PER, QPS = 4 / GPC;
+      i32x4 af[2][4];
       i32x16 acc[2];
 #pragma unroll
-      for (int q = 0; q < QPS; ++q) af[0][q] = xfrag(0, q);
+      for (int q = 0; q < 4; ++q) af[0][q] = xfrag(0, q);
 #pragma unroll
       for (int s = 0; s <= STEPS; ++s) {
+        const int mi = s / PER, ni = s % PER / GPC, g = s % GPC;
         __builtin_amdgcn_sched_barrier(0);
-        if (s + 1 < STEPS) {
-#pragma unroll
-          for (int q = 0; q < QPS; ++q)
-            af[(s + 1) & 1][q] = xfrag((s + 1) / GPC, (s + 1) % GPC * QPS + q);
-        }
         if (s < STEPS) {
+          // its share of the next 32 rows' units
+          if (mi + 1 < MI) {
+#pragma unroll
+            for (int q = s % PER * 4 / PER; q < (s % PER + 1) * 4 / PER; ++q)
+              af[(mi + 1) & 1][q] = xfrag(mi + 1, q);
+          }
           acc[s & 1] = i32x16{};
 #pragma unroll
           for (int q = 0; q < QPS; ++q)
-            acc[s & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(af[s & 1][q], bf[s % GPC * QPS + q],
-                                                               acc[s & 1], 0, 0, 0);
+            acc[s & 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                af[mi & 1][g * QPS + q], bf[ni][g * QPS + q], acc[s & 1], 0, 0, 0);
         }
         if (s > 0) {
-          const int mi = (s - 1) / GPC, g = (s - 1) % GPC;
+          const int p = s - 1;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            tot[mi][i] = fmaf(scale[g], (float)acc[(s - 1) & 1][i], tot[mi][i]);
+            tot[p / GPC][i] = fmaf(scale[p % PER / GPC][p % GPC], (float)acc[p & 1][i], tot[p / GPC][i]);
         }
 #pragma unroll
         for (int q = 0; q < QPS; ++q) {
@@ -319,26 +331,30 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  const int col = n0 + 32 * wave + l32;
   float* const y = a.y + (int64_t)split * a.M * a.N;
-  if (col >= a.N) return;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int64_t row = m0 + 32 * mi + 8 * (i >> 2) + 4 * h + (i & 3);
       if (row >= a.M) continue;
-      float v;
-      if constexpr (G == 0)
-        v = w4vec::half_bits((uint16_t)row_sz) * (float)sum[mi][i];
-      else
-        v = tot[mi][i];
-      y[row * a.N + col] = a.splits > 1 ? v : a.sx[row] * v;
+      const float sx = a.splits > 1 ? 1.0f : a.sx[row];
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        const int col = n0 + 32 * (NI * wave + ni) + l32;
+        float v;
+        if constexpr (G == 0)
+          v = w4vec::half_bits((uint16_t)row_sz[ni]) * (float)sum[mi * NI + ni][i];
+        else
+          v = tot[mi * NI + ni][i];
+        if (col < a.N) y[row * a.N + col] = sx * v;
+      }
     }
 }
 
 struct Plan {
-  int mi, splits, per_split;
+  int mi, ni;  // tile: 32 mi rows of X by 128 ni weight rows
+  int splits, per_split;
   Layout l;
   size_t part_off, bytes;
 };
@@ -346,26 +362,29 @@ struct Plan {
 Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
   Plan p;
   const int nch = (int)ceil_div(d_in, KCH);
-  auto tiles = [&](int mi) { return ceil_div(m, 32 * mi) * ceil_div(d_out, TN); };
+  auto tiles = [&](int mi) { return ceil_div(m, 32 * mi) * ceil_div(d_out, 128); };
   p.mi = tiles(4) >= 384 ? 4 : tiles(2) >= 384 ? 2 : 1;
+  const int64_t wide = ceil_div(m, 128) * ceil_div(d_out, 256);
+  p.ni = 10 * wide >= 9 * 512 * ceil_div(wide, 512) ? 2 : 1;
+  if (p.ni == 2) p.mi = 4;
   int64_t splits = 1;
   while (splits < 16 && tiles(p.mi) * splits < 384 && nch >= 8 * splits) splits *= 2;
   p.per_split = (int)ceil_div(nch, splits);
   p.splits = (int)ceil_div(nch, p.per_split);
-  p.l = layout_of(m, d_out, d_in, group_size, 32 * p.mi);
+  p.l = layout_of(m, d_out, d_in, group_size, 32 * p.mi, 128 * p.ni);
   p.part_off = (p.l.bytes + 255) / 256 * 256;
   p.bytes = p.splits > 1 ? p.part_off + (size_t)p.splits * m * d_out * 4 : p.l.bytes;
   return p;
 }
 
-template <int MI>
+template <int MI, int NI>
 void launch(const MulArgs& a, int G, hipStream_t stream) {
   const dim3 grid((unsigned)(8 * ceil_div((int64_t)a.tiles_m * a.tiles_n * a.splits, 8)));
   switch (G) {
-    case 32: hipLaunchKernelGGL((w4a8_kernel<MI, 32>), grid, dim3(256), 0, stream, a); break;
-    case 64: hipLaunchKernelGGL((w4a8_kernel<MI, 64>), grid, dim3(256), 0, stream, a); break;
-    case 128: hipLaunchKernelGGL((w4a8_kernel<MI, 128>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((w4a8_kernel<MI, 0>), grid, dim3(256), 0, stream, a);
+    case 32: hipLaunchKernelGGL((w4a8_kernel<MI, NI, 32>), grid, dim3(256), 0, stream, a); break;
+    case 64: hipLaunchKernelGGL((w4a8_kernel<MI, NI, 64>), grid, dim3(256), 0, stream, a); break;
+    case 128: hipLaunchKernelGGL((w4a8_kernel<MI, NI, 128>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((w4a8_kernel<MI, NI, 0>), grid, dim3(256), 0, stream, a);
   }
 }
 
@@ -403,12 +422,12 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
   a.ws = (const char*)ws, a.sx = x_scales, a.q = qweight, a.l = p.l, a.M = m;
   a.y = p.splits > 1 ? (float*)((char*)ws + p.part_off) : Y;
   a.N = (int)d_out, a.row_bytes = (int)(d_in / 2);
-  a.tiles_m = (int)(p.l.rows / (32 * p.mi)), a.tiles_n = (int)(p.l.cols / TN);
+  a.tiles_m = (int)(p.l.rows / (32 * p.mi)), a.tiles_n = (int)(p.l.cols / (128 * p.ni));
   a.splits = p.splits, a.per_split = p.per_split;
   switch (p.mi) {
-    case 4: launch<4>(a, G, stream); break;
-    case 2: launch<2>(a, G, stream); break;
-    default: launch<1>(a, G, stream);
+    case 4: p.ni == 2 ? launch<4, 2>(a, G, stream) : launch<4, 1>(a, G, stream); break;
+    case 2: launch<2, 1>(a, G, stream); break;
+    default: launch<1, 1>(a, G, stream);
   }
   e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;

@@ -446,21 +446,22 @@ _W32_TYPES = (torch.int32, torch.uint32)
 _FLOATS = (torch.bfloat16, torch.float32)
 
 
-def _call(where: str, index: int, stream, *args):
-    """The library call, on the tensors' device and on one of its streams."""
+def _raw_stream(where: str, index: int, stream) -> int:
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)  # current_stream() without its object
-    elif stream.device.index != index:
+        return torch._C._cuda_getCurrentRawStream(index)  # current_stream() without its object
+    if stream.device.index != index:
         raise ValueError(f"{where}: the stream is on {stream.device}, the tensors on GPU {index}")
-    else:
-        raw = stream.cuda_stream
-    f = getattr(lib(), where)
+    return stream.cuda_stream
+
+
+def _call(where: str, index: int, f, *args):
+    """The library call with the tensors' device as the current one."""
     if index == torch._C._cuda_getDevice():
-        st = f(*args, raw)
+        st = f(*args)
     else:
         with torch.cuda.device(index):
-            st = f(*args, raw)
-    if st != GPTQ_OK:
+            st = f(*args)
+    if st:
         raise GPTQError(st, where)
 
 
@@ -493,7 +494,7 @@ def _flat(where: str, name: str, t: torch.Tensor, shape, dtypes, index: int):
 def _scratch(where: str, ws, nbytes: int, X: torch.Tensor, stream):
     """The caller's workspace, or one of the call's own where it needs any."""
     if ws is None:
-        return _workspace(nbytes, X.device, stream)
+        return _workspace(nbytes, X.device, stream) if nbytes else None
     if ws.device != X.device or not ws.is_contiguous():
         raise ValueError(f"{where}: ws must be contiguous on {X.device}")
     return ws
@@ -503,26 +504,40 @@ def _span(ws):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
-def _w4_checks(where, X, index, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream):
-    """The packed weights' shapes against X's; returns (m, d_in, d_out, ldx, Y).  A group
+def _w4_checks(where, X, x_dtype, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream):
+    """The packed weights' shapes against X's; returns (index, m, d_in, d_out, ldx, Y).  A group
     size that the library refuses is left to it: it reads nothing then."""
+    index = _index(where, X, (x_dtype,))
     m, d_in = X.shape
     d_out = qweight.shape[0]
-    _flat(where, "qweight", qweight, (d_out, d_in // 8), _W32_TYPES, index)
-    if group_size == -1 or (group_size > 0 and d_in % group_size == 0):
-        meta = (d_out, 1 if group_size == -1 else d_in // group_size)
+    if group_size == -1:
+        meta = (d_out, 1)
+    elif group_size > 0 and d_in % group_size == 0:
+        meta = (d_out, d_in // group_size)
+    else:
+        meta = scales_f16.shape
+    ldx, one = X.stride()
+    if not (qweight.shape == (d_out, d_in // 8) and qweight.dtype in _W32_TYPES
+            and qweight.is_contiguous() and qweight.get_device() == index
+            and scales_f16.shape == meta and scales_f16.dtype in _W16_TYPES
+            and scales_f16.is_contiguous() and scales_f16.get_device() == index
+            and (sym or (zeros_f16 is not None and zeros_f16.shape == meta
+                         and zeros_f16.dtype in _W16_TYPES and zeros_f16.is_contiguous()
+                         and zeros_f16.get_device() == index))
+            and (one == 1 or d_in == 1)):
+        _flat(where, "qweight", qweight, (d_out, d_in // 8), _W32_TYPES, index)
         _flat(where, "scales_f16", scales_f16, meta, _W16_TYPES, index)
         if not sym:
             if zeros_f16 is None:
                 raise ValueError(f"{where}: zeros_f16 is needed unless sym")
             _flat(where, "zeros_f16", zeros_f16, meta, _W16_TYPES, index)
-    if d_in > 1 and X.stride(1) != 1:
-        raise ValueError(f"{where}: X must be row-major")
+        raise ValueError(f"{where}: X must be row-major, got strides {X.stride()}")
     if Y is None:
         Y = _empty(stream, (m, d_out), dtype=torch.float32, device=X.device)
-    else:
+    elif not (Y.shape == (m, d_out) and Y.dtype is torch.float32 and Y.is_contiguous()
+              and Y.get_device() == index):
         _flat(where, "Y", Y, (m, d_out), (torch.float32,), index)
-    return m, d_in, d_out, X.stride(0) if m > 1 else d_in, Y
+    return index, m, d_in, d_out, ldx if m > 1 else d_in, Y
 
 
 @functools.lru_cache(maxsize=1024)
@@ -537,13 +552,12 @@ def gptq_w4a16_matvec(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.
     """gptq_w4a16_matmul for the rows of a few tokens (m <= GPTQ_MATVEC_MAX_M), any d_in that is a
     multiple of 32: Y [m, d_out] fp32 = X [m, d_in] bf16 times the dequantized weights transposed."""
     where = "gptq_w4a16_matvec"
-    index = _index(where, X, (torch.bfloat16,))
-    m, d_in, d_out, ldx, Y = _w4_checks(where, X, index, qweight, scales_f16, zeros_f16,
-                                        group_size, sym, Y, stream)
+    index, m, d_in, d_out, ldx, Y = _w4_checks(where, X, torch.bfloat16, qweight, scales_f16,
+                                               zeros_f16, group_size, sym, Y, stream)
     ws = _scratch(where, ws, gptq_w4a16_matvec_workspace(m, d_out, d_in, group_size), X, stream)
-    _call(where, index, stream, X.data_ptr(), m, ldx, qweight.data_ptr(), scales_f16.data_ptr(),
-          None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size, 1 if sym else 0,
-          Y.data_ptr(), *_span(ws))
+    _call(where, index, lib().gptq_w4a16_matvec, X.data_ptr(), m, ldx, qweight.data_ptr(),
+          scales_f16.data_ptr(), None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size,
+          1 if sym else 0, Y.data_ptr(), *_span(ws), _raw_stream(where, index, stream))
     return Y
 
 
@@ -559,14 +573,16 @@ def gptq_w4a8_matmul(X: torch.Tensor, x_scales: torch.Tensor, qweight: torch.Ten
     """Y [m, d_out] fp32 = x_scales [m] times X [m, d_in] int8 (gptq_add_rmsnorm's 8-bit output)
     times the dequantized 4-bit weights transposed."""
     where = "gptq_w4a8_matmul"
-    index = _index(where, X, (torch.int8,))
-    m, d_in, d_out, ldx, Y = _w4_checks(where, X, index, qweight, scales_f16, zeros_f16,
-                                        group_size, sym, Y, stream)
-    _flat(where, "x_scales", x_scales, (m,), (torch.float32,), index)
+    index, m, d_in, d_out, ldx, Y = _w4_checks(where, X, torch.int8, qweight, scales_f16,
+                                               zeros_f16, group_size, sym, Y, stream)
+    if not (x_scales.shape == (m,) and x_scales.dtype is torch.float32
+            and x_scales.is_contiguous() and x_scales.get_device() == index):
+        _flat(where, "x_scales", x_scales, (m,), (torch.float32,), index)
     ws = _scratch(where, ws, gptq_w4a8_workspace(m, d_out, d_in, group_size), X, stream)
-    _call(where, index, stream, X.data_ptr(), x_scales.data_ptr(), m, ldx, qweight.data_ptr(),
-          scales_f16.data_ptr(), None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size,
-          1 if sym else 0, Y.data_ptr(), *_span(ws))
+    _call(where, index, lib().gptq_w4a8_matmul, X.data_ptr(), x_scales.data_ptr(), m, ldx,
+          qweight.data_ptr(), scales_f16.data_ptr(), None if sym else zeros_f16.data_ptr(), d_out,
+          d_in, group_size, 1 if sym else 0, Y.data_ptr(), *_span(ws),
+          _raw_stream(where, index, stream))
     return Y
 
 
@@ -607,7 +623,8 @@ def gptq_add_rmsnorm(X: torch.Tensor, weight: torch.Tensor, *,
         out_scales = _empty(stream, m, dtype=torch.float32, device=X.device)
     else:
         _flat(where, "out_scales", out_scales, (m,), (torch.float32,), index)
-    _call(where, index, stream, X.data_ptr(), _dtype_code(X), X.stride(0) if m > 1 else d, r_ptr,
-          r_code, ldr, ro_ptr, ldro, weight.data_ptr(), _dtype_code(weight), float(eps), m, d,
-          out.data_ptr(), GPTQ_I8 if i8 else GPTQ_BF16, ldo, out_scales.data_ptr() if i8 else None)
+    _call(where, index, lib().gptq_add_rmsnorm, X.data_ptr(), _dtype_code(X),
+          X.stride(0) if m > 1 else d, r_ptr, r_code, ldr, ro_ptr, ldro, weight.data_ptr(),
+          _dtype_code(weight), float(eps), m, d, out.data_ptr(), GPTQ_I8 if i8 else GPTQ_BF16, ldo,
+          out_scales.data_ptr() if i8 else None, _raw_stream(where, index, stream))
     return out, out_scales, residual_out
