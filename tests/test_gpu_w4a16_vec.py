@@ -75,6 +75,19 @@ CASES = [
     (64, 8192, 96, 128, False, None),
     (64, 65536, 8, -1, False, None),
     (1, 65536, 3, 32, False, None),
+    # 32 and 64 weight rows per workgroup, whole and ragged
+    (3, 288, 4200, 32, False, None),
+    (20, 640, 4500, 128, True, None),
+    (50, 320, 5000, 64, False, 328),
+    (9, 512, 10250, -1, False, None),
+    (16, 1152, 10240, 128, False, None),
+    (33, 192, 10300, 64, True, None),
+    (64, 160, 11000, 32, False, None),
+    # k over several workgroups, with a last block that is not whole
+    (2, 7200, 70, 32, False, None),
+    (12, 9280, 40, 64, True, None),
+    (40, 6272, 300, 128, False, None),
+    (64, 5152, 2100, -1, False, None),
 ]
 
 
@@ -106,6 +119,50 @@ def test_matvec_identity_rows_give_w_hat(g, d_in):
     np.testing.assert_array_equal(torch.cat(rows).cpu().numpy(), What.T)
 
 
+@pytest.mark.parametrize("m", [1, 5, 40])
+@pytest.mark.parametrize("g,d_in", [(32, 1024), (64, 2048), (128, 1024), (-1, 512)])
+def test_matvec_scales_at_any_address(m, g, d_in):
+    # scales and zeros that start one element past an aligned address
+    X, x64, qw, s16, z16 = make(m, d_in, 70, g, False, seed=g + d_in + m)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    want = gptq.gptq_w4a16_matvec(X, Q, S, Z, group_size=g, sym=False)
+    for skew in (1, 2, 4):
+        def moved(t):
+            buf = torch.zeros(t.numel() + skew, dtype=t.dtype, device=DEV)
+            buf[skew:] = t.flatten()
+            return buf[skew:].view(t.shape)
+        assert torch.equal(gptq.gptq_w4a16_matvec(X, Q, moved(S), moved(Z), group_size=g, sym=False),
+                           want)
+    check(want, x64, qw, s16, z16, False, g)
+
+
+@pytest.mark.parametrize("m", [1, 12, 64])
+def test_matvec_rows_of_a_larger_layer(m):
+    # a slice of packed rows, as one of several layers packed together
+    X, x64, qw, s16, z16 = make(m, 4096, 90, 128, False, seed=m)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    Y = gptq.gptq_w4a16_matvec(X, Q[7:60], S[7:60], Z[7:60], group_size=128, sym=False)
+    check(Y, x64, qw[7:60], s16[7:60], z16[7:60], False, 128)
+
+
+def test_matvec_a_given_workspace_and_two_calls_at_once():
+    X, x64, qw, s16, z16 = make(40, 8192, 200, 128, False, seed=2)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    n = gptq.gptq_w4a16_matvec_workspace(40, 200, 8192, 128)
+    assert n > 0
+    want = gptq.gptq_w4a16_matvec(X, Q, S, Z, group_size=128, sym=False)
+    ws = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [gptq.gptq_w4a16_matvec(X, Q, S, Z, group_size=128, sym=False, ws=ws[i], stream=streams[i])
+           for i in (0, 1) for _ in range(5)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    check(want, x64, qw, s16, z16, False, 128)
+    with pytest.raises(gptq.GPTQError):
+        gptq.gptq_w4a16_matvec(X, Q, S, Z, group_size=128, sym=False, ws=ws[0][:n - 256])
+
+
 def test_matvec_zero_tokens_and_zero_rows():
     _, qw, s16, z16 = packed_weights(256, 24, 64, 9)
     Q, S, Z = dev_weights(qw, s16, z16)
@@ -135,8 +192,9 @@ def test_matvec_agrees_with_the_matmul_call():
     assert np.all(np.abs((a.double() - b.double()).cpu().numpy()) <= both)
 
 
-def test_matvec_on_another_stream_and_replayed():
-    X, x64, qw, s16, z16 = make(6, 2048, 300, 64, False, seed=21)
+@pytest.mark.parametrize("m,d_in", [(1, 2048), (6, 2048), (30, 8192)])
+def test_matvec_on_another_stream_and_replayed(m, d_in):
+    X, x64, qw, s16, z16 = make(m, d_in, 300, 64, False, seed=21)
     Q, S, Z = dev_weights(qw, s16, z16)
     want = gptq.gptq_w4a16_matvec(X, Q, S, Z, group_size=64, sym=False)
     torch.cuda.synchronize()

@@ -80,6 +80,30 @@ CASES = [
     (1000, 224, 1030, 32, False, None),
     (300, 65536, 136, -1, False, None),
     (2049, 256, 2051, 128, False, None),
+    # few tokens: 32 and 64 weight rows per workgroup
+    (3, 288, 4200, 32, False, None),
+    (20, 640, 4500, 128, True, None),
+    (50, 320, 5000, 64, False, 336),
+    (9, 512, 10250, -1, False, None),
+    (33, 192, 10300, 64, True, None),
+    (48, 160, 11000, 32, False, None),
+    (60, 64, 8192, 64, False, None),
+    # k over several workgroups
+    (2, 7200, 70, 32, False, None),
+    (12, 9280, 40, 64, True, None),
+    (40, 6272, 300, 128, False, None),
+    (64, 5152, 2100, -1, False, None),
+    (100, 4128, 136, 32, False, None),
+    # tiles: below 64 tokens with many weight rows, 128 rows of X, 256 weight rows
+    (60, 64, 8200, 64, False, None),
+    (3000, 224, 2100, 32, False, None),
+    (3000, 192, 2100, 64, True, None),
+    (2990, 256, 2090, 128, False, 272),
+    (2990, 160, 2090, -1, False, None),
+    (8190, 160, 2046, 32, False, None),
+    (8190, 192, 2046, 64, False, None),
+    (8190, 384, 2046, 128, True, None),
+    (8190, 352, 2046, -1, False, None),
 ]
 
 
@@ -132,6 +156,40 @@ def test_w4a8_identity_rows_give_w_hat(g, d_in):
         Y = gptq.gptq_w4a8_matmul(eye[:rows], torch.ones(rows, device=DEV), Q, S, Z, group_size=g,
                                   sym=False)
         np.testing.assert_array_equal(Y.cpu().numpy(), What.T[:rows])
+
+
+@pytest.mark.parametrize("m", [1, 5, 200])
+@pytest.mark.parametrize("g,d_in", [(32, 1024), (64, 2048), (128, 1024), (-1, 512)])
+def test_w4a8_scales_at_any_address(m, g, d_in):
+    # scales and zeros that start one element past an aligned address
+    X, XS, xi, xs, qw, s16, z16 = make(m, d_in, 70, g, False, seed=g + d_in + m)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    want = gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=g, sym=False)
+    for skew in (1, 2, 4):
+        def moved(t):
+            buf = torch.zeros(t.numel() + skew, dtype=t.dtype, device=DEV)
+            buf[skew:] = t.flatten()
+            return buf[skew:].view(t.shape)
+        assert torch.equal(gptq.gptq_w4a8_matmul(X, XS, Q, moved(S), moved(Z), group_size=g,
+                                                 sym=False), want)
+    check(want, xi, xs, qw, s16, z16, False, g)
+
+
+@pytest.mark.parametrize("m", [40, 200, 1500])
+def test_w4a8_a_given_workspace_and_two_calls_at_once(m):
+    d_in, d_out = 4096, 200
+    X, XS, xi, xs, qw, s16, z16 = make(m, d_in, d_out, 128, False, seed=2)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    n = gptq.gptq_w4a8_workspace(m, d_out, d_in, 128)
+    want = gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=128, sym=False)
+    ws = [torch.full((max(n, 256),), 0xFF, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [gptq.gptq_w4a8_matmul(X, XS, Q, S, Z, group_size=128, sym=False, ws=ws[i],
+                                 stream=streams[i]) for i in (0, 1) for _ in range(5)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    check(want, xi, xs, qw, s16, z16, False, 128)
 
 
 def test_w4a8_no_tokens():
