@@ -5,6 +5,7 @@
 #include "w4_dot.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 namespace gptq {
 
@@ -144,32 +145,27 @@ struct MulArgs {
   int splits, per_split;  // of the chunks
 };
 
-// Four waves side by side, each 32 MI rows of X by 32 weight rows: a wave
+template <int MI, int NI, int G>
+struct Shape {
+  static constexpr int TM = 32 * MI, TN = 128 * NI;
+  static constexpr int GPC = G == 0 ? 0 : KCH / G;  // groups per chunk
+  static constexpr int ABYTES = TM * KCH, BBYTES = TN * (KCH / 2), SZBYTES = GPC * TN * 4;
+  static constexpr int STAGE = ABYTES + BBYTES + SZBYTES;
+};
+
+// Four waves side by side, each 32 MI rows of X by 32 NI weight rows: a wave
 // takes the codes of its own weight rows apart, and none twice.  G: group
 // size, 0 for one group per row.
 template <int MI, int NI, int G>
-__global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
-  constexpr int TM = 32 * MI, TN = 128 * NI;
-  constexpr int GPC = G == 0 ? 0 : KCH / G;  // groups per chunk
-  constexpr int ABYTES = TM * KCH, BBYTES = TN * (KCH / 2), SZBYTES = GPC * TN * 4;
-  constexpr int STAGE = ABYTES + BBYTES + SZBYTES;
-  constexpr int LOADS = MI + 2 * NI + GPC;        // direct loads of a wave per chunk
-  __shared__ __attribute__((aligned(1024))) char lds[NST * STAGE];
+__device__ __forceinline__ void tile_product(const MulArgs& a, char* lds, int64_t m0, int n0,
+                                             int split) {
+  typedef Shape<MI, NI, G> S;
+  constexpr int TN = S::TN, GPC = S::GPC, ABYTES = S::ABYTES, BBYTES = S::BBYTES;
+  constexpr int STAGE = S::STAGE;
+  constexpr int LOADS = MI + 2 * NI + GPC;  // direct loads of a wave per chunk
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, l32 = lane & 31;
-  // consecutive workgroups go to the eight XCDs in turn: each XCD takes a run
-  // of tiles, eight tiles of weight rows wide, so that its L2 holds what they
-  // share
-  const int tiles = a.tiles_m * a.tiles_n, total = tiles * a.splits, per = (total + 7) / 8;
-  const int t0 = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
-  if (t0 >= min(total, ((int)(blockIdx.x & 7) + 1) * per)) return;
-  const int split = t0 / tiles, t = t0 - split * tiles;
-  const int sup = t / (8 * a.tiles_m), rest = t - sup * 8 * a.tiles_m;
-  const int wide = min(8, a.tiles_n - 8 * sup);
-  const int tm = rest / wide, tn = 8 * sup + rest - tm * wide;
-  const int64_t m0 = (int64_t)tm * TM;
-  const int n0 = tn * TN;
   const int nch = a.l.nch, c0 = split * a.per_split, c1 = min(nch, c0 + a.per_split);
 
   // direct loads: X panels and group words are copied as they are; a weight
@@ -203,6 +199,10 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
       }
     }
   };
+  // the scale of row threadIdx.x, for the end
+  float sx_mine = 1.0f;
+  if (a.splits == 1 && threadIdx.x < 32 * MI)
+    sx_mine = a.sx[min(m0 + (int64_t)threadIdx.x, a.M - 1)];
   uint32_t row_sz[NI];
 #pragma unroll
   for (int ni = 0; ni < NI; ++ni) row_sz[ni] = G == 0 ? sz[32 * ni + l32] : 0u;
@@ -331,25 +331,63 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  float* const y = a.y + (int64_t)split * a.M * a.N;
+  // The rows' scales by way of LDS: read where they are used, each row's store
+  // waited for its load (12 us of every workgroup's time).
+  __syncthreads();
+  float* const ls = (float*)lds;
+  if (threadIdx.x < 32 * MI) ls[threadIdx.x] = sx_mine;
+  __syncthreads();
+  float* const y = a.y + (int64_t)split * a.M * a.N + m0 * a.N + n0;
+  const int rows = (int)min((int64_t)(32 * MI), a.M - m0);
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int64_t row = m0 + 32 * mi + 8 * (i >> 2) + 4 * h + (i & 3);
-      if (row >= a.M) continue;
-      const float sx = a.splits > 1 ? 1.0f : a.sx[row];
+    for (int i = 0; i < 16; i += 4) {
+      const int r0 = 32 * mi + 2 * i + 4 * h;
+      const float4 sx4 = *(const float4*)(ls + r0);
+      const float sx[4] = {sx4.x, sx4.y, sx4.z, sx4.w};
 #pragma unroll
       for (int ni = 0; ni < NI; ++ni) {
-        const int col = n0 + 32 * (NI * wave + ni) + l32;
-        float v;
-        if constexpr (G == 0)
-          v = w4vec::half_bits((uint16_t)row_sz[ni]) * (float)sum[mi * NI + ni][i];
-        else
-          v = tot[mi * NI + ni][i];
-        if (col < a.N) y[row * a.N + col] = sx * v;
+        const int col = 32 * (NI * wave + ni) + l32;
+        const bool in = n0 + col < a.N;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v;
+          if constexpr (G == 0)
+            v = w4vec::half_bits((uint16_t)row_sz[ni]) * (float)sum[mi * NI + ni][i + e];
+          else
+            v = tot[mi * NI + ni][i + e];
+          if (in && r0 + e < rows) y[(int64_t)(r0 + e) * a.N + col] = sx[e] * v;
+        }
       }
     }
+}
+
+template <int MI, int NI, int G>
+__global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
+  constexpr int TM = 32 * MI, TN = 128 * NI;
+  __shared__ __attribute__((aligned(1024))) char lds[NST * Shape<MI, NI, G>::STAGE];
+  // consecutive workgroups go to the eight XCDs in turn: each XCD takes a run
+  // of tiles, eight tiles of weight rows wide, so that its L2 holds what they
+  // share
+  const int tiles = a.tiles_m * a.tiles_n, total = tiles * a.splits, per = (total + 7) / 8;
+  const int t0 = (int)(blockIdx.x & 7) * per + (int)(blockIdx.x >> 3);
+  if (t0 >= min(total, ((int)(blockIdx.x & 7) + 1) * per)) return;
+  const int split = t0 / tiles, t = t0 - split * tiles;
+  const int sup = t / (8 * a.tiles_m), rest = t - sup * 8 * a.tiles_m;
+  const int wide = min(8, a.tiles_n - 8 * sup);
+  const int tm = rest / wide, tn = 8 * sup + rest - tm * wide;
+  const int64_t m0 = (int64_t)tm * TM;
+  const int n0 = tn * TN;
+  // the last rows' tile does the work of the rows that are there
+  const int64_t left = a.M - m0;
+  if constexpr (MI >= 4) {
+    if (left <= 8 * MI) return tile_product<MI / 4, NI, G>(a, lds, m0, n0, split);
+  }
+  if constexpr (MI >= 2) {
+    if (left <= 16 * MI) return tile_product<MI / 2, NI, G>(a, lds, m0, n0, split);
+  }
+  tile_product<MI, NI, G>(a, lds, m0, n0, split);
 }
 
 struct Plan {
@@ -363,7 +401,9 @@ Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
   Plan p;
   const int nch = (int)ceil_div(d_in, KCH);
   auto tiles = [&](int mi) { return ceil_div(m, 32 * mi) * ceil_div(d_out, 128); };
+  static int emi = getenv("MI") ? atoi(getenv("MI")) : 0;
   p.mi = tiles(4) >= 384 ? 4 : tiles(2) >= 384 ? 2 : 1;
+  if (emi) p.mi = emi;
   const int64_t wide = ceil_div(m, 128) * ceil_div(d_out, 256);
   p.ni = 10 * wide >= 9 * 512 * ceil_div(wide, 512) ? 2 : 1;
   if (p.ni == 2) p.mi = 4;
