@@ -5,7 +5,6 @@
 #include "w4_dot.h"
 
 #include <algorithm>
-#include <cstdlib>
 
 namespace gptq {
 
@@ -397,18 +396,32 @@ struct Plan {
   size_t part_off, bytes;
 };
 
+// Tiles of 128 x 256 (X by weight rows) where they fill rounds of two per CU;
+// else 128, 64 or 32 rows of X by 128, and k over several workgroups, by the
+// least of a time in us: k workgroups share a CU, a tile takes `alone` by
+// itself and no CU does better than one per `shared` (each measured at 32
+// chunks of groups of 128); splits add a launch and their sums' bytes at some
+// 4 TB/s.  4096 columns through 4096 weight rows: 2048 tokens take 56 us with
+// 128 rows and 59 with 64; 1024 tokens 44 and 35; 256 tokens 23.3 us with 32
+// rows in one piece, 21.2 in two.
 Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
+  constexpr double shared[3] = {9.5, 14.0, 25.0}, alone[3] = {18.0, 25.0, 38.0};
   Plan p;
   const int nch = (int)ceil_div(d_in, KCH);
-  auto tiles = [&](int mi) { return ceil_div(m, 32 * mi) * ceil_div(d_out, 128); };
-  static int emi = getenv("MI") ? atoi(getenv("MI")) : 0;
-  p.mi = tiles(4) >= 384 ? 4 : tiles(2) >= 384 ? 2 : 1;
-  if (emi) p.mi = emi;
   const int64_t wide = ceil_div(m, 128) * ceil_div(d_out, 256);
-  p.ni = 10 * wide >= 9 * 512 * ceil_div(wide, 512) ? 2 : 1;
-  if (p.ni == 2) p.mi = 4;
+  p.mi = 4, p.ni = 2;
   int64_t splits = 1;
-  while (splits < 16 && tiles(p.mi) * splits < 384 && nch >= 8 * splits) splits *= 2;
+  if (10 * wide < 9 * 512 * ceil_div(wide, 512)) {
+    p.ni = 1;
+    double best = 0.0;
+    for (int s = 1; s <= 16 && (s == 1 || s <= nch / 2); s *= 2)
+      for (int i = 0; i < 3; ++i) {
+        const int64_t n = ceil_div(m, 32 << i) * ceil_div(d_out, 128) * s;
+        double us = std::max((double)ceil_div(n, 256) * shared[i], alone[i]) * nch / 32 / s;
+        if (s > 1) us += 3.0 + 1e-6 * (double)(m * d_out) * (s + 1);
+        if (best == 0.0 || us < best) best = us, p.mi = 1 << i, splits = s;
+      }
+  }
   p.per_split = (int)ceil_div(nch, splits);
   p.splits = (int)ceil_div(nch, p.per_split);
   p.l = layout_of(m, d_out, d_in, group_size, 32 * p.mi, 128 * p.ni);
