@@ -218,14 +218,14 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
     Piece s[LD], z[LD];
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const int e = (64 * i + lane) & (16 * R * P - 1);
+      const int e = min(64 * i + lane, 16 * R * P - 1);
       const int64_t o = (int64_t)min(n0 + e / P, a.n - 1) * a.ng + min(b * S::GPB + (e % P) * V, a.ng - V);
       s[i] = *(const Piece*)(a.s16 + o);
       if (a.z16) z[i] = *(const Piece*)(a.z16 + o);
     }
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const int e = (64 * i + lane) & (16 * R * P - 1);
+      const int e = min(64 * i + lane, 16 * R * P - 1);
 #pragma unroll
       for (int v = 0; v < V; ++v)
         sc[((e % P) * V + v) * 16 * R + e / P] =
@@ -489,28 +489,35 @@ struct VecPlan {
   size_t ws_bytes;
 };
 
-// Weight rows per workgroup: more of them read X fewer times, fewer of them use
-// more CUs.  64 while that leaves some 160 workgroups (16 tokens through 11008
-// x 4096: 11.4 us, against 14.3 and 16.6 us with 32 and 16), else 16 while they
-// find room at once on 256 CUs (4096 x 4096: 5.8 us, against 6.7 and 8.9 us),
-// else 32 (37 tokens through 4099 x 11008 in 8 bits: 26 us, against 36 us with
-// 16, whose 257th workgroup waits).
-// The row's k go to several workgroups where that leaves CUs idle and a wave
-// has more than one block of k: a second launch adds their sums (some 2.5 us;
-// 64 tokens through 1024 x 8192: 12.1 us with four, 24.5 us with one).  With
-// more than 32 bf16 tokens, which take most of LDS, 32 rows in two splits beat
-// 16 in one (4096 x 11008: 30 and 45 us; 4096 x 4096: 14.8 and 14.7 us).
+// Weight rows per workgroup (16 r) and workgroups that share a row's k, by the
+// least of a time in us.  A step of a workgroup's waves takes 0.27 (2 + r) us
+// with 16 tokens and a third more with every 16 further ones (4096 x 4096, 16
+// tokens: 0.8, 1.1 and 1.6 us for r = 1, 2, 4); workgroups beyond what the 256
+// CUs hold wait for a round of their own; splits add a launch and their sums'
+// bytes.  More rows read X fewer times, fewer of them spread further: 16
+// tokens through 11008 x 4096 take 16.1, 13.9, 10.6 and 11.7 us with r = 1 to
+// 4, through 4096 x 4096 5.6, 6.7 and 8.9 us with 1, 2 and 4; 64 tokens
+// through 1024 x 8192 12.1 us in four splits and 24.5 in one, through 4096 x
+// 11008 30 us with r = 2 in two splits and 45 with r = 1 in one.
 inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
-  VecPlan p;
-  const int nt = (int)ceil_div(m, 16);
-  const bool big_x = !i8 && nt > 2;
-  p.r = n >= 160 * 64 ? 4 : n <= 256 * 16 && !(big_x && n > 2048) ? 1 : 2;
-  const int nblk = (int)ceil_div(k, KBLK);
-  const int waves = std::min(8, LDS_BYTES / wave_bytes(i8, nt, p.r, G));
-  const int64_t idle = 256 / ceil_div(n, 16 * p.r);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(idle, ceil_div(nblk, waves)));
-  p.per_split = (int)ceil_div(nblk, p.splits);
-  p.splits = (int)ceil_div(nblk, p.per_split);
+  VecPlan p = {1, 1, 1, 0};
+  const int nt = (int)ceil_div(m, 16), nblk = (int)ceil_div(k, KBLK);
+  double least = 0.0;
+  for (int r = 1; r <= 4; ++r)
+    for (int s = 1; s <= 8 && s <= nblk; ++s) {
+      const int per = (int)ceil_div(nblk, s);
+      const int waves = std::min(per, std::min(8, LDS_BYTES / wave_bytes(i8, nt, r, G)));
+      const int64_t groups = ceil_div(n, 16 * r) * s;
+      const bool several = 2 * waves * wave_bytes(i8, nt, r, G) <= LDS_BYTES;  // per CU
+      const double rounds = several ? std::max(1.0, groups / 256.0) : (double)ceil_div(groups, 256);
+      const double steps = 2.0 * (ceil_div(per, waves) + (double)per / waves);  // most and mean
+      double us = rounds * 0.27 * (2 + r) * (1.0 + 0.35 * (nt - 1)) * steps;
+      if (s > 1) us += 2.5 + 1e-6 * (double)(m * n) * (s + 1);
+      if (least == 0.0 || us < least) {
+        least = us;
+        p.r = r, p.per_split = per, p.splits = (int)ceil_div(nblk, per);
+      }
+    }
   p.ws_bytes = p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
   return p;
 }
@@ -518,6 +525,7 @@ inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
 template <bool I8, int NT>
 hipError_t vec_launch_t(const VecArgs& a, int r, int G, hipStream_t stream) {
   if (r == 4) return vec_launch_g<I8, NT, 4>(a, G, stream);
+  if (r == 3) return vec_launch_g<I8, NT, 3>(a, G, stream);
   if (r == 2) return vec_launch_g<I8, NT, 2>(a, G, stream);
   return vec_launch_g<I8, NT, 1>(a, G, stream);
 }

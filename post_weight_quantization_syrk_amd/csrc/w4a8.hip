@@ -15,11 +15,13 @@ typedef __attribute__((ext_vector_type(16))) int i32x16;
 
 constexpr int KCH = 128;           // k per chunk (bytes of a row of X, twice those of a weight row)
 
-// Where the kernels for a few tokens take over from the tiles below: 48 tokens
-// through 11008 x 4096 take 19.3 us there and 19.6 us here, 64 take 24 and 19.6
-// us; with fewer weight rows the tiles' two launches cost more than they save
-// (64 through 4096 x 4096: 8.2 and 14.0 us).
-bool few_tokens(int64_t m, int64_t d_out) { return m <= 48 || (m <= 64 && d_out <= 8192); }
+// Up to here the kernels for a few tokens, past it the tiles below, whose two
+// or three launches have to pay (48 tokens through 11008 x 4096: 13.9 and 23.1
+// us; through 28672 x 8192: 64 and 48 us; 64 tokens through 4096 x 4096: 8.4
+// and 13.8 us, through 8192 x 8192: 25.0 and 21.4 us).
+bool few_tokens(int64_t m, int64_t d_out, int64_t d_in) {
+  return m <= 32 || (m <= 64 && d_out * d_in < 60000000);
+}
 
 constexpr int PANEL = 32 * KCH;    // bytes of a panel: 32 rows of one chunk
 constexpr int NST = 2;             // chunks in LDS
@@ -444,7 +446,7 @@ void launch(const MulArgs& a, int G, hipStream_t stream) {
 }  // namespace
 
 size_t w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
-  if (!few_tokens(m, d_out)) return plan_for(m, d_out, d_in, group_size).bytes;
+  if (!few_tokens(m, d_out, d_in)) return plan_for(m, d_out, d_in, group_size).bytes;
   const int G = group_size == -1 ? 0 : group_size;
   return w4vec::dot_takes(m, d_in) ? 0 : w4vec::vec_plan(true, m, d_out, d_in, G).ws_bytes;
 }
@@ -454,7 +456,7 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
                        const uint16_t* zeros_f16, int64_t d_out, int64_t d_in, int group_size,
                        float* Y, void* ws, hipStream_t stream) {
   const int G = group_size == -1 ? 0 : group_size;
-  if (few_tokens(m, d_out)) {
+  if (few_tokens(m, d_out, d_in)) {
     w4vec::VecArgs v;
     v.x = (const char*)X, v.sx = x_scales, v.q = qweight, v.s16 = scales_f16, v.z16 = zeros_f16;
     v.y = Y, v.ldx = ldx, v.m = (int)m, v.n = (int)d_out, v.k = (int)d_in;
