@@ -102,10 +102,11 @@ constexpr int KBLK = 512;  // k per block: whole scale runs for every group size
 
 // Direct global -> LDS load of 16 bytes per lane: lane l's bytes land at
 // lds + 16 l.  In asm, as the compiler would wait for every load in flight
-// before any LDS read; the loop waits by count itself.
+// before any LDS read; the loop waits by count itself.  (M0 may be used for
+// LDS one wait state after it is written.)
 __device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
   const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds);
-  __asm__ volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off"
+  __asm__ volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
                    :
                    : "v"(p), "s"(lbase)
                    : "memory", "m0");

@@ -24,7 +24,6 @@ bool few_tokens(int64_t m, int64_t d_out, int64_t d_in) {
 }
 
 constexpr int PANEL = 32 * KCH;    // bytes of a panel: 32 rows of one chunk
-constexpr int NST = 2;             // chunks in LDS
 
 // Where the product's tiles are in the workspace: X as panels of 32 rows by
 // 128 columns, and per group and weight row a word with the scale's binary16
@@ -119,7 +118,7 @@ __device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t 
   const uint32_t bhi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
   const void* sbase = (const void*)(uintptr_t)(((uint64_t)bhi << 32) | blo);
   const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds_off);
-  __asm__ volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1"
+  __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                    :
                    : "v"(voff), "s"(sbase), "s"(lbase)
                    : "memory", "m0");
@@ -163,7 +162,6 @@ __device__ __forceinline__ void tile_product(const MulArgs& a, char* lds, int64_
   typedef Shape<MI, NI, G> S;
   constexpr int TN = S::TN, GPC = S::GPC, ABYTES = S::ABYTES, BBYTES = S::BBYTES;
   constexpr int STAGE = S::STAGE;
-  constexpr int LOADS = MI + 2 * NI + GPC;  // direct loads of a wave per chunk
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, l32 = lane & 31;
@@ -220,24 +218,17 @@ __device__ __forceinline__ void tile_product(const MulArgs& a, char* lds, int64_
       else
         tot[mi][i] = 0.0f;
     }
-#pragma unroll
-  for (int s = 0; s < NST - 1; ++s)
-    if (c0 + s < c1) issue(c0 + s, s);
-  int buf = 0;
+  issue(c0, 0);
   for (int c = c0; c < c1; ++c) {
-    // chunk c has landed (the newer chunks' loads may be on their way), and
-    // chunk c - 1's buffer is read
-    if (c + NST - 2 < c1)
-      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((NST - 2) * LOADS) : "memory");
-    else
-      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int buf = (c - c0) & 1;
+    // chunk c has landed, and chunk c - 1's buffer is read
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (c + NST - 1 < c1) issue(c + NST - 1, buf == 0 ? NST - 1 : buf - 1);
+    if (c + 1 < c1) issue(c + 1, buf ^ 1);
     const char* la = lds + buf * STAGE;
     const char* lb = lds + buf * STAGE + ABYTES + (32 * NI * wave + l32) * (KCH / 2);
     const uint32_t* lz =
         (const uint32_t*)(lds + buf * STAGE + ABYTES + BBYTES) + 32 * NI * wave + l32;
-    buf = buf == NST - 1 ? 0 : buf + 1;
     const int sw = (l32 >> 2) & 3;
     // MFMA q of a chunk takes, in lane half h, unit u of X: with groups of 32
     // the two halves share 32 consecutive k, otherwise 64
@@ -367,7 +358,7 @@ __device__ __forceinline__ void tile_product(const MulArgs& a, char* lds, int64_
 template <int MI, int NI, int G>
 __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
   constexpr int TM = 32 * MI, TN = 128 * NI;
-  __shared__ __attribute__((aligned(1024))) char lds[NST * Shape<MI, NI, G>::STAGE];
+  __shared__ __attribute__((aligned(1024))) char lds[2 * Shape<MI, NI, G>::STAGE];
   // consecutive workgroups go to the eight XCDs in turn: each XCD takes a run
   // of tiles, eight tiles of weight rows wide, so that its L2 holds what they
   // share
