@@ -513,11 +513,13 @@ inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
       const double rounds = several ? std::max(1.0, groups / 256.0) : (double)ceil_div(groups, 256);
       const double steps = 2.0 * (ceil_div(per, waves) + (double)per / waves);  // most and mean
       double us = rounds * 0.27 * (2 + r) * (1.0 + 0.35 * (nt - 1)) * steps;
+      if (!several) us += 2.0 * (rounds - 1.0);  // a round's start and end
       if (s > 1) us += 2.5 + 1e-6 * (double)(m * n) * (s + 1);
       if (least == 0.0 || us < least) {
         least = us;
         p.r = r, p.per_split = per, p.splits = (int)ceil_div(nblk, per);
       }
+      if (per <= waves) break;  // a wave has one block: no fewer steps
     }
   p.ws_bytes = p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
   return p;
