@@ -339,7 +339,9 @@ size_t gptq_w4a16_matvec_workspace(int64_t m, int64_t d_out, int64_t d_in, int g
  *     mean square is summed.  A row with P = 0, or whose scale rounds to 0 in
  *     float32, gets scale 1 and zero codes (the rule of a zero range in
  *     gptq_quantize_layer).
- * A row whose mean square plus eps is 0 gives zeros.
+ * A row whose mean square plus eps is 0 gives zeros.  An infinity or a NaN in
+ * h or weight: the 8-bit scale of the row is NaN (the codes mean nothing), the
+ * bf16 output is what the formula gives.
  *
  * X           [m x ldx] of x_dtype (bf16 or float32), row-major; columns
  *             0..d-1 are used (so for R, R_out and out with their leading

@@ -197,6 +197,62 @@ def test_add_rmsnorm_rows_of_zeros_and_extreme_values(d):
     assert bool((out == 0).all()) and bool((s == 1.0).all())
 
 
+@pytest.mark.parametrize("ok", ["i8", "bf16"])
+@pytest.mark.parametrize("d", [40, 41, 16385])
+def test_add_rmsnorm_values_that_are_not_finite(d, ok):
+    """A NaN or an infinity in a row makes its 8-bit scale NaN, never a row of plausible codes;
+    in bf16 it comes out as the formula gives it.  The other rows do not notice."""
+    rng = np.random.default_rng(d)
+    x, r = values(rng, 6, d, "bf16"), values(rng, 6, d, "bf16")
+    w = values(rng, 1, d, "f32")[0]
+    x[1, d - 1] = np.nan
+    x[2, 0] = np.inf
+    x[3, 7], r[3, 7] = np.inf, -np.inf
+    r[4, d // 2] = -np.inf
+    out, sc, _ = gptq.gptq_add_rmsnorm(dev(x, "bf16"), torch.from_numpy(w).to(DEV),
+                                       residual=dev(r, "bf16"), out_dtype=T[ok])
+    bad, good = [1, 2, 3, 4], [0, 5]
+    check(x[good], r[good], w, "bf16", 1e-6, ok, out[good], sc[good] if ok == "i8" else None, None)
+    if ok == "i8":
+        assert torch.isnan(sc[bad]).all()
+    else:
+        assert torch.isnan(out[[1, 3]]).all()
+        for i, c in ((2, 0), (4, d // 2)):  # inf / inf, and finite / inf
+            assert torch.isnan(out[i, c]) and int((out[i] != 0).sum()) == 1
+
+    # the weight's own
+    for v in (np.nan, np.inf):
+        w2 = w.copy()
+        w2[3] = v
+        x0 = x[[0, 5]].copy()
+        x0[0, 3] = 0.0
+        out, sc, _ = gptq.gptq_add_rmsnorm(dev(x0, "bf16"), torch.from_numpy(w2).to(DEV),
+                                           out_dtype=T[ok])
+        if ok == "i8":
+            assert torch.isnan(sc).all()
+        else:
+            assert torch.isnan(out[0, 3]) and not torch.isfinite(out[1, 3])
+            keep = [c for c in range(d) if c != 3]
+            assert torch.isfinite(out[:, keep]).all()
+
+
+@pytest.mark.parametrize("ok", ["i8", "bf16"])
+def test_add_rmsnorm_more_rows_than_one_launch_takes(ok):
+    m = (1 << 26) + 3  # 64 threads each: past 2^32 threads
+    x = torch.arange(m, device=DEV, dtype=torch.int32).remainder_(251).sub_(125).float()
+    w = torch.full((1,), 0.5, device=DEV)
+    out, sc, h = gptq.gptq_add_rmsnorm(torch.ones_like(x, dtype=torch.bfloat16).unsqueeze(1), w,
+                                       residual=(x - 1).unsqueeze(1), eps=0.0, out_dtype=T[ok])
+    # one column: h = x, y = +-0.5 or 0; code +-127 with scale 0.5 / 127, or 0 with scale 1
+    assert torch.equal(h[:, 0], x)
+    if ok == "bf16":
+        assert torch.equal(out[:, 0], (0.5 * torch.sign(x)).to(torch.bfloat16))
+        return
+    assert torch.equal(out[:, 0], (127 * torch.sign(x)).to(torch.int8))
+    want = torch.where(x == 0, 1.0, 0.5 / 127)  # two roundings apart
+    assert float(((sc - want).abs() / want).max()) <= 2.0 ** -23
+
+
 def test_add_rmsnorm_no_rows():
     W = torch.ones(64, dtype=torch.bfloat16, device=DEV)
     out, s, _ = gptq.gptq_add_rmsnorm(torch.empty((0, 64), device=DEV), W)
