@@ -28,7 +28,7 @@ struct NormArgs {
   char* out;
   float* scales;
   int64_t ldx, ldr, ldro, ldo;  // elements
-  double eps;
+  double eps, inv_d;
   int d;
   int out_i8;
 };
@@ -67,6 +67,21 @@ __device__ __forceinline__ double wave_fold(double v, F f) {
   return f(__hiloint2double(hi32[0], lo32[0]), __hiloint2double(hi32[1], lo32[1]));
 }
 
+// 1 / x in float64: the instruction's estimate (at least 22 bits) and one
+// iteration, which doubles them.  x in the range of 127 / x's use.
+__device__ __forceinline__ double reciprocal(double x) {
+  const double r = __builtin_amdgcn_rcp(x);
+  return fma(r, fma(-x, r, 1.0), r);
+}
+
+// 1 / sqrt(x) of a positive number, with an iteration of third order: to the
+// last bits of a float64.
+__device__ __forceinline__ double reciprocal_root(double x) {
+  double r = __builtin_amdgcn_rsq(x);
+  const double e = fma(-x * r, r, 1.0);
+  return fma(r * e, fma(e, 0.375, 0.5), r);
+}
+
 // Sum of `sum` and maximum of `top` over the workgroup, in every thread; the
 // waves' parts are joined in wave order.
 __device__ __forceinline__ void fold_row(double& sum, double& top, double (*red)[16]) {
@@ -77,9 +92,15 @@ __device__ __forceinline__ void fold_row(double& sum, double& top, double (*red)
     if (lane == 0) red[0][wave] = sum, red[1][wave] = top;
     __syncthreads();
     sum = 0.0;
-    for (int i = 0; i < waves; ++i) {
-      sum += red[0][i];
-      top = fmax(top, red[1][i]);
+    for (int i = 0; i < waves; i += 4) {  // four at a time, read together
+      double p[4], q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) p[j] = red[0][i + j], q[j] = red[1][i + j];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum += i + j < waves ? p[j] : 0.0;
+        top = fmax(top, i + j < waves ? q[j] : 0.0);
+      }
     }
   }
 }
@@ -214,8 +235,8 @@ __global__ __launch_bounds__((VPT == 4 ? 512 : 1024)) void add_rmsnorm_kernel(No
     }
   if (a.out_i8) sum += odd;
   fold_row(sum, top, red);
-  const double ms = sum / a.d + a.eps;
-  const double rstd = ms == 0.0 ? 0.0 : 1.0 / sqrt(ms);
+  const double ms = fma(sum, a.inv_d, a.eps);
+  const double rstd = ms == 0.0 || ms == INFINITY ? 0.0 : reciprocal_root(ms);
 
   if (!a.out_i8) {
     uint16_t* o = (uint16_t*)a.out + row * a.ldo;
@@ -240,36 +261,43 @@ __global__ __launch_bounds__((VPT == 4 ? 512 : 1024)) void add_rmsnorm_kernel(No
     }
     return;
   }
-  const float scale = (float)(top * rstd / 127.0);
+  const float scale = (float)(top * rstd * (1.0 / 127.0));
   const bool empty = scale == 0.0f;
   if (tid == 0) a.scales[row] = empty ? 1.0f : scale;
-  // A code from float32: h w, 127 / P and their product are off by half a step
-  // each, so t by less than 127 * 3 * 2^-24 < 2^-15, and unless t is that close
-  // to a border its nearest integer is the code.  Otherwise, and where float32
-  // could overflow or go subnormal, the float64 quotient decides.
-  const float c127 = (float)(127.0 / top);
+  // A code from float32: adding 1.5 2^23 leaves the nearest whole number (ties
+  // to even) in a float's low bits.  h w and 127 / P are off by half a step each,
+  // so their product (formed within a fused addition, not rounded) by less than
+  // 127 * 2.1 * 2^-24 < 2^-15: unless it is that close to a border, its nearest
+  // whole number is the code.  Otherwise, and where float32 could overflow or go
+  // subnormal, the float64 quotient decides.
+  constexpr float MAGIC = 12582912.0f;
+  const float c127 = (float)(127.0 * reciprocal(top));
   const bool plain = top > 1e-25 && top < 1e30;
   int8_t* o = (int8_t*)a.out + row * a.ldo;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
-    int q[8];
-    bool near = !plain;
+    uint32_t q[8];
+    float off = 0.0f;  // farthest from a whole number
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float t = h[v][e] * element(w[v], e) * c127, k = rintf(t);
-      near |= fabsf(fabsf(t - k) - 0.5f) <= 3.0517578125e-05f;
-      q[e] = (int)k;
+      const float hw = h[v][e] * element(w[v], e), k = fmaf(hw, c127, MAGIC);
+      off = fmaxf(off, fabsf(fmaf(hw, c127, MAGIC - k)));
+      q[e] = __float_as_uint(k);
     }
-    if (near) {
+    if (off >= 0.5f - 3.0517578125e-05f || !plain) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        q[e] = empty ? 0 : (int)rint(127.0 * ((double)h[v][e] * (double)element(w[v], e)) / top);
+        q[e] = empty ? 0u
+                     : (uint32_t)(int)rint(127.0 * ((double)h[v][e] * (double)element(w[v], e)) / top);
     }
     if constexpr (VEC) {
       const int c = column<VEC>(v, 0);
-      uint32_t b[2] = {0u, 0u};
+      uint32_t b[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) b[e / 4] |= ((uint32_t)q[e] & 0xffu) << (8 * (e & 3));
+      for (int e = 0; e < 2; ++e)
+        b[e] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[4 * e + 3], q[4 * e + 2], 0x0c0c0400u),
+                                     __builtin_amdgcn_perm(q[4 * e + 1], q[4 * e], 0x0c0c0400u),
+                                     0x05040100u);
       if (c < a.d) *(uint2*)(o + c) = make_uint2(b[0], b[1]);
     } else {
 #pragma unroll
@@ -307,9 +335,9 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_long_kernel(NormArgs a, int 
   }
   if (a.out_i8) sum += odd;
   fold_row(sum, top, red);
-  const double ms = sum / a.d + a.eps;
-  const double rstd = ms == 0.0 ? 0.0 : 1.0 / sqrt(ms);
-  const float scale = (float)(top * rstd / 127.0);
+  const double ms = fma(sum, a.inv_d, a.eps);
+  const double rstd = ms == 0.0 || ms == INFINITY ? 0.0 : reciprocal_root(ms);
+  const float scale = (float)(top * rstd * (1.0 / 127.0));
   const bool empty = scale == 0.0f;
   if (a.out_i8 && tid == 0) a.scales[row] = empty ? 1.0f : scale;
   for (int c = tid; c < a.d; c += 1024) {
@@ -368,7 +396,7 @@ hipError_t add_rmsnorm_launch(const void* X, int x_dtype, int64_t ldx, const voi
   NormArgs a;
   a.x = (const char*)X, a.r = (const char*)R, a.r_out = (char*)R_out, a.w = (const char*)weight;
   a.out = (char*)out, a.scales = out_scales, a.ldx = ldx, a.ldr = ldr, a.ldro = ldro, a.ldo = ldo;
-  a.eps = eps, a.d = (int)d, a.out_i8 = out_dtype == GPTQ_I8;
+  a.eps = eps, a.inv_d = 1.0 / (double)d, a.d = (int)d, a.out_i8 = out_dtype == GPTQ_I8;
   const bool xf = x_dtype == GPTQ_F32, rf = r_dtype == GPTQ_F32, wf = w_dtype == GPTQ_F32;
   // 16-byte pieces: every row starts on one, and the row is whole eights
   auto rows16 = [&](const void* p, int64_t ld, int size) {
