@@ -373,11 +373,14 @@ __global__ __launch_bounds__(256, 2) void w4a8_kernel(MulArgs a) {
   const int n0 = tn * TN;
   // the last rows' tile does the work of the rows that are there
   const int64_t left = a.M - m0;
-  if constexpr (MI >= 4) {
-    if (left <= 8 * MI) return tile_product<MI / 4, NI, G>(a, lds, m0, n0, split);
-  }
   if constexpr (MI >= 2) {
-    if (left <= 16 * MI) return tile_product<MI / 2, NI, G>(a, lds, m0, n0, split);
+    if (left <= 32) return tile_product<1, NI, G>(a, lds, m0, n0, split);
+  }
+  if constexpr (MI >= 3) {
+    if (left <= 64) return tile_product<2, NI, G>(a, lds, m0, n0, split);
+  }
+  if constexpr (MI >= 4) {
+    if (left <= 96) return tile_product<3, NI, G>(a, lds, m0, n0, split);
   }
   tile_product<MI, NI, G>(a, lds, m0, n0, split);
 }
@@ -390,15 +393,16 @@ struct Plan {
 };
 
 // Tiles of 128 x 256 (X by weight rows) where they fill rounds of two per CU;
-// else 128, 64 or 32 rows of X by 128, and k over several workgroups, by the
-// least of a time in us: k workgroups share a CU, a tile takes `alone` by
+// else 128, 96, 64 or 32 rows of X by 128, and k over several workgroups, by
+// the least of a time in us: workgroups share a CU, a tile takes `alone` by
 // itself and no CU does better than one per `shared` (each measured at 32
 // chunks of groups of 128); splits add a launch and their sums' bytes at some
 // 4 TB/s.  4096 columns through 4096 weight rows: 2048 tokens take 56 us with
-// 128 rows and 59 with 64; 1024 tokens 44 and 35; 256 tokens 23.3 us with 32
-// rows in one piece, 21.2 in two.
+// 128 rows, 57 with 96 and 60 with 64; 1024 tokens 36, 41 and 34; 256 tokens
+// 23.3 us with 32 rows in one piece, 21.2 in two.  1500 tokens through 4096 x
+// 11008 in groups of 64: 142, 127 and 133 us with 128, 96 and 64.
 Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
-  constexpr double shared[3] = {9.5, 14.0, 25.0}, alone[3] = {18.0, 25.0, 38.0};
+  constexpr double shared[4] = {9.5, 14.0, 19.5, 25.0}, alone[4] = {18.0, 25.0, 31.0, 38.0};
   Plan p;
   const int nch = (int)ceil_div(d_in, KCH);
   const int64_t wide = ceil_div(m, 128) * ceil_div(d_out, 256);
@@ -408,11 +412,11 @@ Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
     p.ni = 1;
     double best = 0.0;
     for (int s = 1; s <= 16 && (s == 1 || s <= nch / 2); s *= 2)
-      for (int i = 0; i < 3; ++i) {
-        const int64_t n = ceil_div(m, 32 << i) * ceil_div(d_out, 128) * s;
+      for (int i = 0; i < 4; ++i) {
+        const int64_t n = ceil_div(m, 32 * (i + 1)) * ceil_div(d_out, 128) * s;
         double us = std::max((double)ceil_div(n, 256) * shared[i], alone[i]) * nch / 32 / s;
         if (s > 1) us += 3.0 + 1e-6 * (double)(m * d_out) * (s + 1);
-        if (best == 0.0 || us < best) best = us, p.mi = 1 << i, splits = s;
+        if (best == 0.0 || us < best) best = us, p.mi = i + 1, splits = s;
       }
   }
   p.per_split = (int)ceil_div(nch, splits);
@@ -472,6 +476,7 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
   a.splits = p.splits, a.per_split = p.per_split;
   switch (p.mi) {
     case 4: p.ni == 2 ? launch<4, 2>(a, G, stream) : launch<4, 1>(a, G, stream); break;
+    case 3: launch<3, 1>(a, G, stream); break;
     case 2: launch<2, 1>(a, G, stream); break;
     default: launch<1, 1>(a, G, stream);
   }

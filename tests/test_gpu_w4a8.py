@@ -100,6 +100,13 @@ CASES = [
     (3000, 192, 2100, 64, True, None),
     (2990, 256, 2090, 128, False, 272),
     (2990, 160, 2090, -1, False, None),
+    # 96 rows of X, and what may be left for the last tile
+    (2800, 160, 2100, 32, False, None),
+    (2830, 192, 2100, 64, False, 208),
+    (2850, 256, 2050, 128, True, None),
+    (2800, 96, 2060, -1, False, None),
+    (3030, 128, 2100, 64, False, None),
+    (3030, 160, 2100, -1, True, None),
     (8190, 160, 2046, 32, False, None),
     (8190, 192, 2046, 64, False, None),
     (8190, 384, 2046, 128, True, None),
