@@ -307,12 +307,14 @@ int gptq_w4a16_matmul(const void* X, int64_t m, int64_t ldx, const uint32_t* qwe
  *               GPTQ_EUNSUPPORTED: gptq_w4a16_matmul takes any m).
  *   qweight     16-byte aligned.
  *   ws          gptq_w4a16_matvec_workspace(m, d_out, d_in, group_size) bytes
- *               (0 for most shapes); its contents on entry do not matter.
+ *               (0 for most shapes); its contents on entry do not matter, and
+ *               calls in flight together need one each.
  * The weights are read once.  Per group, sum x q and sum x are formed with
  * exact products and fp32 sums and joined as s (sum x q - z sum x); groups
  * are added in fp32.  The order of every sum is fixed: the same inputs give
  * the same bits, though not those of gptq_w4a16_matmul, which adds in another
- * order.
+ * order.  An infinity in a row of X gives infinities or NaN in that row of Y,
+ * not always those of the formula; other rows do not notice.
  * ------------------------------------------------------------------------- */
 #define GPTQ_MATVEC_MAX_M 64
 int gptq_w4a16_matvec(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
@@ -379,14 +381,18 @@ int gptq_add_rmsnorm(const void* X, int x_dtype, int64_t ldx, const void* R, int
  *             qweight 16-byte aligned.
  * Y           [m x d_out] float32 out.
  * d_in        a multiple of 32 (GPTQ_EUNSUPPORTED otherwise), <= 65536.
- * m           0 (no-op) or more.
- * ws          gptq_w4a8_workspace(m, d_out, d_in, group_size) bytes (0 for
- *             most shapes); its contents on entry do not matter.
- * A group's sum of x q and of x is exact (32-bit integers, at most 8192 terms
- * before it is taken into float32, where it is exact too); with the integer
- * zeros that gptq_pack writes sum x q - z sum x is exact as well, so only the
- * scaling by s and x_scales and the addition of groups round, in float32.
- * The order of those sums is fixed: the same inputs give the same bits.
+ * m           0 (no-op) .. 2^30.
+ * ws          gptq_w4a8_workspace(m, d_out, d_in, group_size) bytes: 0 for most
+ *             shapes of a few tokens; for more, X and the scales laid out for
+ *             the matrix cores (about m d_in + 4 d_out n_groups bytes), and
+ *             parts of Y where k is split.  Its contents on entry do not
+ *             matter; calls in flight together need one each.
+ * Zeros are whole numbers, as gptq_pack writes them; here a zero is rounded to
+ * one and kept within -100 .. 100.  Sums of x (q - z) over runs of k inside a
+ * group are exact 32-bit integers, each taken into float32 once (exactly up to
+ * 2^24); only the scaling by s and x_scales and the addition of runs and groups
+ * round, in float32.  The order of those sums is fixed: the same inputs give the
+ * same bits.
  * ------------------------------------------------------------------------- */
 int gptq_w4a8_matmul(const int8_t* X, const float* x_scales, int64_t m, int64_t ldx,
                      const uint32_t* qweight, const uint16_t* scales_f16,

@@ -10,6 +10,13 @@
 // registers as the matrix instructions want them, neighbouring lanes are in
 // different rows, and the vector cache takes one lane per cycle: measured 63
 // accesses per load, 26 us for 16 tokens through 11008 x 4096.)
+// Bound: with one scale per row, weights as they arrive; with groups, the
+// vector units (taking codes apart, scaling each group's sums: 16 tokens through
+// 11008 x 4096 take 9.4 us with one scale per row, 10.5 in groups of 64; the
+// weights alone 5.0 at 4.9 TB/s), and the start and end of a workgroup (its
+// first loads and the waves' sums, some 2 us).  Three or four buffers per wave,
+// four waves with more rows each, and runs of consecutive k per wave in place of
+// blocks in turn (8 tokens through 28672 x 8192: 36 us for 33) were no faster.
 // For int8 X the zero is taken off the codes, four at a time.  For bf16 X that
 // would cost an operation per code: x q and x are summed apart (the sum of x by
 // the same instruction against ones, shared by all rows), and joined per group.
@@ -494,8 +501,8 @@ struct VecPlan {
 // least of a time in us.  A step of a workgroup's waves takes 0.27 (2 + r) us
 // with 16 tokens and a third more with every 16 further ones (4096 x 4096, 16
 // tokens: 0.8, 1.1 and 1.6 us for r = 1, 2, 4); workgroups beyond what the 256
-// CUs hold wait for a round of their own; splits add a launch and their sums'
-// bytes.  More rows read X fewer times, fewer of them spread further: 16
+// CUs hold wait for a round of their own, which costs 2 us to start and end;
+// splits add a launch and their sums' bytes.  More rows read X fewer times, fewer of them spread further: 16
 // tokens through 11008 x 4096 take 16.1, 13.9, 10.6 and 11.7 us with r = 1 to
 // 4, through 4096 x 4096 5.6, 6.7 and 8.9 us with 1, 2 and 4; 64 tokens
 // through 1024 x 8192 12.1 us in four splits and 24.5 in one, through 4096 x

@@ -1,5 +1,26 @@
 // Product of the packed 4-bit weights with 8-bit activations (W4A8):
-//   Y[i][n] = sx[i] sum_k X[i][k] s[n][k/g] (q[n][k] - z[n][k/g])
+//   Y[i][n] = sx[i] sum_g s[n][g] sum_{k in g} X[i][k] (q[n][k] - z[n][g])
+//
+// Few tokens: w4_dot.h and w4_vec.h.  More: q - z, within int8, multiplies X on
+// the matrix cores, a group's sum an exact 32-bit integer; every group ends with
+// two vector operations per sum (to float32, times s into the total), shared by
+// nothing: with groups of 128 they take the vector units about as long as the
+// products take the matrix cores, with 64 twice as long, with 32 four times.  So
+// one group's products run while the one before it is scaled, and what else the
+// vector units do is kept small: codes are taken apart by masks, four to an
+// operation, once for all rows of X (the four waves of a workgroup stand side by
+// side along the weight rows), zeros are taken off four at a time, and X and the
+// scales are laid out before (w4a8_layout_kernel), so that both come by direct
+// loads and need no further work.
+// 8192 tokens through 28672 x 8192, groups of 128: 2.14 ms, 1.80 POP/s (1.86 ms,
+// 2.07 POP/s with one group per row; a library int8 product of 8192^3 reaches
+// 2.08), the vector units busy 75% of the cycles and the matrix cores 48%, at the
+// 1.7 GHz that the chip's power allows.  515 tokens through 11008 x 4096, groups
+// of 64: 58 us.
+// Tried and slower or no faster: three buffers (515 tokens 59 -> 61 us), the
+// next chunk's codes taken apart ahead (2048 tokens through 11008 x 4096: 161 ->
+// 171), two by two waves, eight waves on 256 x 256 (2.36 -> 2.34 ms), scales as
+// halves in mixed operations (4 to 7% slower).
 #include "common.h"
 #include "kernels.h"
 #include "w4_dot.h"
@@ -53,6 +74,8 @@ Layout layout_of(int64_t m, int64_t d_out, int64_t d_in, int group_size, int tm,
 // order once: 0 2 4 6 1 3 5 7 within every eight.  A panel's 16-byte units are
 // stored so that 16 rows read at the same unit fall on different LDS banks.
 // Rows past m and columns past d_in are zeros: they add nothing to any sum.
+// (8192 x 8192 and 28672 x 64 parameters: 29 us; 515 x 4096: 7.5, mostly a
+// launch and the parameters' reads, short pieces of long rows.)
 __global__ __launch_bounds__(256) void w4a8_layout_kernel(
     const int8_t* __restrict__ X, int64_t ldx, int64_t M, int N, int K, Layout l,
     const uint16_t* __restrict__ S16, const uint16_t* __restrict__ Z16, int vec,
