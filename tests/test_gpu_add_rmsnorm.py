@@ -198,6 +198,22 @@ def test_add_rmsnorm_rows_of_zeros_and_extreme_values(d):
 
 
 @pytest.mark.parametrize("ok", ["i8", "bf16"])
+@pytest.mark.parametrize("eps", [0.0, 5e-324, 1e-310, 1e-30, 1e29])
+@pytest.mark.parametrize("d", [64, 67])
+def test_add_rmsnorm_smallest_and_largest_eps(d, eps, ok):
+    """The square root's whole range: mean squares from float64's subnormals (rows of zeros) up."""
+    rng = np.random.default_rng(d)
+    x = values(rng, 4, d, "f32")
+    x[0] = 0.0
+    x[1] *= np.float32(1e-20)
+    x[2] *= np.float32(1e-38)  # subnormal entries
+    w = values(rng, 1, d, "f32")[0]
+    out, sc, _ = gptq.gptq_add_rmsnorm(dev(x, "f32"), torch.from_numpy(w).to(DEV), eps=eps,
+                                       out_dtype=T[ok])
+    check(x, None, w, None, eps, ok, out, sc, None)
+
+
+@pytest.mark.parametrize("ok", ["i8", "bf16"])
 @pytest.mark.parametrize("d", [40, 41, 16385])
 def test_add_rmsnorm_values_that_are_not_finite(d, ok):
     """A NaN or an infinity in a row makes its 8-bit scale NaN, never a row of plausible codes;
