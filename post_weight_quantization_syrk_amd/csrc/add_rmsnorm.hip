@@ -9,7 +9,7 @@
 // Bound by memory: x and r are read once, h and the output written once.  A
 // workgroup holds a row in registers between the one reduction (of sum h^2 and
 // max |p|, together) and the output, so no row is read twice and no second
-// launch is needed; 16-byte loads where rows allow them.  The reductions are in
+// launch is needed.  The reductions are in
 // float64: its operations run at the rate of float32 ones here, and squares
 // neither overflow nor vanish.  The vector units come next (61% busy at 16384 x
 // 8192 with bf16 output): divisions are done as reciprocals with an iteration,
@@ -113,19 +113,29 @@ __device__ __forceinline__ void fold_row(double& sum, double& top, double (*red)
   }
 }
 
-// Eight elements of a row as they are in memory.  VEC: consecutive ones from
-// element 8 (v T + tid), as 16-byte loads; otherwise one in T, from element 8 v
-// T + tid, each on its own.
+// Eight consecutive elements of a row as they are in memory.
 template <Kind K>
 struct Raw {
   uint32_t u[K == F32 ? 8 : 4];
 };
 
+// Pieces at an address that only the elements' own size divides: global loads
+// and stores take those (4096 x 5003 bf16 to 8 bits: 43 us; 95 by elements, one
+// per lane; 4096 x 5000, aligned: 35).
+typedef uint32_t any_u32x4_2 __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t any_u32x4_4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t any_u32x2_4 __attribute__((ext_vector_type(2), aligned(4)));
+typedef uint32_t any_u32x2_2 __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t any_u32x2_1 __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t any_u32_2 __attribute__((aligned(2)));
+typedef uint32_t any_u32_1 __attribute__((aligned(1)));
+typedef uint16_t any_u16_1 __attribute__((aligned(1)));
+
+// Elements c .. c + 7 of a row of d.  VEC: the row starts on 16 bytes and d is
+// whole eights; otherwise any address, and the row's last piece by elements.
 template <Kind K, bool VEC>
-__device__ __forceinline__ void load8(const char* row, int v, int d, Raw<K>& o) {
-  const int T = blockDim.x, tid = threadIdx.x;
+__device__ __forceinline__ void load8(const char* row, int c, int d, Raw<K>& o) {
   if constexpr (VEC) {
-    const int c = 8 * (v * T + tid);
     const uint4* p = (const uint4*)(row + (int64_t)(c < d ? c : 0) * (K == F32 ? 4 : 2));
     const uint4 a = p[0];
     o.u[0] = a.x, o.u[1] = a.y, o.u[2] = a.z, o.u[3] = a.w;
@@ -133,10 +143,37 @@ __device__ __forceinline__ void load8(const char* row, int v, int d, Raw<K>& o) 
       const uint4 b = p[1];
       o.u[4] = b.x, o.u[5] = b.y, o.u[6] = b.z, o.u[7] = b.w;
     }
+  } else if (d >= 8) {
+    // the last piece from the row's last eight, moved down: what does not belong
+    // to it (and may be written by others meanwhile) falls out
+    const int at = min(c, d - 8), by = c - at;
+    if constexpr (K == F32) {
+      const any_u32x4_4* p = (const any_u32x4_4*)(row + 4 * (int64_t)at);
+      const any_u32x4_4 a = p[0], b = p[1];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.u[e] = a[e], o.u[4 + e] = b[e];
+    } else {
+      const any_u32x4_2 a = *(const any_u32x4_2*)(row + 2 * (int64_t)at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.u[e] = a[e];
+    }
+    if (by > 0) {
+      constexpr int WORDS = K == F32 ? 8 : 4;
+#pragma unroll
+      for (int s = 4; s >= 1; s /= 2) {
+        const int w = K == F32 ? s : s / 2;
+#pragma unroll
+        for (int e = 0; e < WORDS; ++e) {
+          const uint32_t up = e + w < WORDS ? o.u[e + w] : 0u;
+          const uint32_t half = e + 1 < WORDS ? o.u[e + 1] : 0u;
+          o.u[e] = !(by & s) ? o.u[e] : w ? up : __builtin_amdgcn_alignbit(half, o.u[e], 16);
+        }
+      }
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = (8 * v + e) * T + tid, cc = c < d ? c : 0;
+      const int cc = c + e < d ? c + e : 0;
       if constexpr (K == F32) {
         o.u[e] = ((const uint32_t*)row)[cc];
       } else {
@@ -144,6 +181,76 @@ __device__ __forceinline__ void load8(const char* row, int v, int d, Raw<K>& o) 
         o.u[e / 2] = e & 1 ? o.u[e / 2] | b << 16 : b;
       }
     }
+  }
+}
+
+template <Kind K, bool VEC>
+__device__ __forceinline__ void store8(char* row, int c, int d, const Raw<K>& o) {
+  if (VEC ? c < d : c + 8 <= d) {
+    if constexpr (VEC) {
+      uint4* p = (uint4*)(row + (int64_t)c * (K == F32 ? 4 : 2));
+      p[0] = make_uint4(o.u[0], o.u[1], o.u[2], o.u[3]);
+      if constexpr (K == F32) p[1] = make_uint4(o.u[4], o.u[5], o.u[6], o.u[7]);
+    } else if constexpr (K == F32) {
+      any_u32x4_4* p = (any_u32x4_4*)(row + 4 * (int64_t)c);
+      p[0] = any_u32x4_4{o.u[0], o.u[1], o.u[2], o.u[3]};
+      p[1] = any_u32x4_4{o.u[4], o.u[5], o.u[6], o.u[7]};
+    } else {
+      *(any_u32x4_2*)(row + 2 * (int64_t)c) = any_u32x4_2{o.u[0], o.u[1], o.u[2], o.u[3]};
+    }
+  } else if constexpr (!VEC) {
+    // the row's last one to seven, as four, two and one
+    const int n = d - c;
+    char* p = row + (int64_t)c * (K == F32 ? 4 : 2);
+    uint32_t u0 = o.u[0], u1 = o.u[1];
+    if (n <= 0) return;
+    if constexpr (K == F32) {
+      uint32_t u2 = o.u[2];
+      if (n & 4) {
+        *(any_u32x4_4*)p = any_u32x4_4{u0, u1, o.u[2], o.u[3]};
+        u0 = o.u[4], u1 = o.u[5], u2 = o.u[6], p += 16;
+      }
+      if (n & 2) {
+        *(any_u32x2_4*)p = any_u32x2_4{u0, u1};
+        u0 = u2, p += 8;
+      }
+      if (n & 1) *(uint32_t*)p = u0;
+    } else {
+      if (n & 4) {
+        *(any_u32x2_2*)p = any_u32x2_2{u0, u1};
+        u0 = o.u[2], u1 = o.u[3], p += 8;
+      }
+      if (n & 2) {
+        *(any_u32_2*)p = u0;
+        u0 = u1, p += 4;
+      }
+      if (n & 1) *(uint16_t*)p = (uint16_t)u0;
+    }
+  }
+}
+
+// The low bytes of q as elements c .. c + 7.
+template <bool VEC>
+__device__ __forceinline__ void store8_codes(char* row, int c, int d, const uint32_t q[8]) {
+  uint32_t b[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    b[e] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[4 * e + 3], q[4 * e + 2], 0x0c0c0400u),
+                                 __builtin_amdgcn_perm(q[4 * e + 1], q[4 * e], 0x0c0c0400u),
+                                 0x05040100u);
+  if (VEC ? c < d : c + 8 <= d) {
+    if constexpr (VEC)
+      *(uint2*)(row + c) = make_uint2(b[0], b[1]);
+    else
+      *(any_u32x2_1*)(row + c) = any_u32x2_1{b[0], b[1]};
+  } else if constexpr (!VEC) {
+    const int n = d - c;
+    char* p = row + c;
+    uint32_t u = b[0];
+    if (n <= 0) return;
+    if (n & 4) *(any_u32_1*)p = u, u = b[1], p += 4;
+    if (n & 2) *(any_u16_1*)p = (uint16_t)u, u >>= 16, p += 2;
+    if (n & 1) *p = (char)u;
   }
 }
 
@@ -155,212 +262,199 @@ __device__ __forceinline__ float element(const Raw<K>& o, int e) {
     return __uint_as_float(e & 1 ? o.u[e / 2] & 0xffff0000u : o.u[e / 2] << 16);
 }
 
-template <bool VEC>
-__device__ __forceinline__ int column(int v, int e) {
-  const int T = blockDim.x, tid = threadIdx.x;
-  return VEC ? 8 * (v * T + tid) + e : (8 * v + e) * T + tid;
+// h of eight elements; those past the row's end are 0.
+template <Kind X, Kind R, bool VEC>
+__device__ __forceinline__ void sum8(const Raw<X>& x, const Raw<R == NONE ? BF16 : R>& r, int c,
+                                     int d, float h[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float s = element(x, e);
+    if constexpr (R != NONE) s += element(r, e);
+    if constexpr (R == BF16) s = __uint_as_float(bf16_bits(s) << 16);
+    h[e] = (VEC ? c : c + e) < d ? s : 0.0f;
+  }
+}
+
+// h as it is stored.
+template <Kind R>
+__device__ __forceinline__ Raw<R> raw_of(const float h[8]) {
+  Raw<R> o;
+#pragma unroll
+  for (int e = 0; e < (R == F32 ? 8 : 4); ++e)
+    o.u[e] = R == F32 ? __float_as_uint(h[e])
+                      : __builtin_amdgcn_perm(__float_as_uint(h[2 * e + 1]),
+                                              __float_as_uint(h[2 * e]), 0x07060302u);
+  return o;
+}
+
+// Sum of h^2, maximum of |p|, and 0 p, which is nothing unless p is an infinity
+// or a NaN: a maximum passes over NaN, so for the 8-bit scale this joins the
+// sum and makes it NaN.  (0 w in float32 would do and is slower: 192 us where
+// this takes 182, 16384 x 8192 bf16.)
+template <Kind W>
+__device__ __forceinline__ void gather8(const float h[8], const Raw<W>& w, double& sum, double& top,
+                                        double& odd) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const double hd = (double)h[e], p = hd * (double)element(w, e);
+    sum = fma(hd, hd, sum);
+    top = fmax(top, fabs(p));
+    odd = fma(p, 0.0, odd);
+  }
+}
+
+// What the row's sums give the output.
+struct RowOut {
+  double rstd, top;
+  float c127;
+  bool empty, plain;
+};
+
+__device__ __forceinline__ RowOut row_out(const NormArgs& a, double sum, double top) {
+  RowOut o;
+  const double ms = fma(sum, a.inv_d, a.eps);
+  o.rstd = ms == 0.0 || ms == INFINITY ? 0.0 : reciprocal_root(ms);
+  o.top = top;
+  o.c127 = (float)(127.0 * reciprocal(top));
+  o.plain = top > 1e-25 && top < 1e30;
+  const float scale = (float)(top * o.rstd * (1.0 / 127.0));
+  o.empty = scale == 0.0f;
+  if (a.out_i8 && threadIdx.x == 0) a.scales[blockIdx.x] = o.empty ? 1.0f : scale;
+  return o;
+}
+
+// A code from float32: adding 1.5 2^23 leaves the nearest whole number (ties to
+// even) in a float's low bits.  h w and 127 / P are off by half a step each, so
+// their product (formed within a fused addition, not rounded) by less than
+// 127 * 2.1 * 2^-24 < 2^-15: unless it is that close to a border, its nearest
+// whole number is the code.  Otherwise, and where float32 could overflow or go
+// subnormal, the float64 quotient decides.
+template <Kind W>
+__device__ __forceinline__ void codes8(const RowOut& o, const float h[8], const Raw<W>& w,
+                                       uint32_t q[8]) {
+  constexpr float MAGIC = 12582912.0f;
+  float off = 0.0f;  // farthest from a whole number
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float hw = h[e] * element(w, e), k = fmaf(hw, o.c127, MAGIC);
+    off = fmaxf(off, fabsf(fmaf(hw, o.c127, MAGIC - k)));
+    q[e] = __float_as_uint(k);
+  }
+  if (off >= 0.5f - 3.0517578125e-05f || !o.plain) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      q[e] = o.empty ? 0u
+                     : (uint32_t)(int)rint(127.0 * ((double)h[e] * (double)element(w, e)) / o.top);
+  }
+}
+
+template <Kind W>
+__device__ __forceinline__ Raw<BF16> bf16_of(const RowOut& o, const float h[8], const Raw<W>& w) {
+  Raw<BF16> y;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint32_t b[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      b[f] = bf16_bits((float)((double)h[2 * e + f] * (double)element(w, 2 * e + f) * o.rstd));
+    y.u[e] = b[0] | b[1] << 16;
+  }
+  return y;
 }
 
 // X, R, W: their types (R NONE: no residual); VPT: elements per thread / 8.
 template <Kind X, Kind R, Kind W, int VPT, bool VEC>
 __global__ __launch_bounds__((VPT == 4 ? 512 : 1024)) void add_rmsnorm_kernel(NormArgs a) {
   __shared__ double red[2][16];
+  constexpr int RB = R == F32 ? 4 : 2;
   const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
-  const char* xp = a.x + row * a.ldx * (X == F32 ? 4 : 2);
+  auto at = [&](int v) __attribute__((always_inline)) {
+    return 8 * (v * (int)blockDim.x + (int)threadIdx.x);
+  };
   float h[VPT][8];
   Raw<W> w[VPT];
   {
     Raw<X> x[VPT];
     Raw<R == NONE ? BF16 : R> r[VPT];
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) load8<X, VEC>(xp, v, a.d, x[v]);
+    for (int v = 0; v < VPT; ++v)
+      load8<X, VEC>(a.x + row * a.ldx * (X == F32 ? 4 : 2), at(v), a.d, x[v]);
     if constexpr (R != NONE) {
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) load8<R, VEC>(a.r + row * a.ldr * (R == F32 ? 4 : 2), v, a.d, r[v]);
+      for (int v = 0; v < VPT; ++v) load8<R, VEC>(a.r + row * a.ldr * RB, at(v), a.d, r[v]);
     }
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) load8<W, VEC>(a.w, v, a.d, w[v]);
+    for (int v = 0; v < VPT; ++v) load8<W, VEC>(a.w, at(v), a.d, w[v]);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float s = element(x[v], e);
-        if constexpr (R != NONE) s += element(r[v], e);
-        if constexpr (R == BF16) s = __uint_as_float(bf16_bits(s) << 16);
-        h[v][e] = column<VEC>(v, e) < a.d ? s : 0.0f;
-      }
+    for (int v = 0; v < VPT; ++v) sum8<X, R, VEC>(x[v], r[v], at(v), a.d, h[v]);
   }
   if constexpr (R != NONE) {
     if (a.r_out) {  // R_out may be R: these elements of it have been read
-      char* o = a.r_out + row * a.ldro * (R == F32 ? 4 : 2);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        if constexpr (VEC) {
-          const int c = column<VEC>(v, 0);
-          if (c < a.d) {
-            if constexpr (R == F32) {
-              ((float4*)(o + 4 * (int64_t)c))[0] = make_float4(h[v][0], h[v][1], h[v][2], h[v][3]);
-              ((float4*)(o + 4 * (int64_t)c))[1] = make_float4(h[v][4], h[v][5], h[v][6], h[v][7]);
-            } else {
-              uint32_t u[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                u[e] = __builtin_amdgcn_perm(__float_as_uint(h[v][2 * e + 1]),
-                                             __float_as_uint(h[v][2 * e]), 0x07060302u);
-              *(uint4*)(o + 2 * (int64_t)c) = make_uint4(u[0], u[1], u[2], u[3]);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int c = column<VEC>(v, e);
-            if (c < a.d) {
-              if constexpr (R == F32)
-                ((float*)o)[c] = h[v][e];
-              else
-                ((uint16_t*)o)[c] = (uint16_t)(__float_as_uint(h[v][e]) >> 16);
-            }
-          }
-        }
-      }
+      for (int v = 0; v < VPT; ++v)
+        store8<R, VEC>(a.r_out + row * a.ldro * RB, at(v), a.d, raw_of<R>(h[v]));
     }
   }
-
-  // A maximum passes over NaN: for the 8-bit scale, 0 p of every p goes into
-  // the sum, nothing unless p is an infinity or a NaN, which make it NaN.  (0 w
-  // in float32 would do and is slower: 192 us where this takes 182, 16384 x
-  // 8192 bf16.)
   double sum = 0.0, top = 0.0, odd = 0.0;
 #pragma unroll
-  for (int v = 0; v < VPT; ++v)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double hd = (double)h[v][e], p = hd * (double)element(w[v], e);
-      sum = fma(hd, hd, sum);
-      top = fmax(top, fabs(p));
-      odd = fma(p, 0.0, odd);
-    }
+  for (int v = 0; v < VPT; ++v) gather8<W>(h[v], w[v], sum, top, odd);
   if (a.out_i8) sum += odd;
   fold_row(sum, top, red);
-  const double ms = fma(sum, a.inv_d, a.eps);
-  const double rstd = ms == 0.0 || ms == INFINITY ? 0.0 : reciprocal_root(ms);
-
+  const RowOut o = row_out(a, sum, top);
   if (!a.out_i8) {
-    uint16_t* o = (uint16_t*)a.out + row * a.ldo;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      uint32_t b[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        b[e] = bf16_bits((float)((double)h[v][e] * (double)element(w[v], e) * rstd));
-      if constexpr (VEC) {
-        const int c = column<VEC>(v, 0);
-        if (c < a.d)
-          *(uint4*)(o + c) = make_uint4(b[0] | b[1] << 16, b[2] | b[3] << 16, b[4] | b[5] << 16,
-                                        b[6] | b[7] << 16);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = column<VEC>(v, e);
-          if (c < a.d) o[c] = (uint16_t)b[e];
-        }
-      }
-    }
+    for (int v = 0; v < VPT; ++v)
+      store8<BF16, VEC>(a.out + row * a.ldo * 2, at(v), a.d, bf16_of<W>(o, h[v], w[v]));
     return;
   }
-  const float scale = (float)(top * rstd * (1.0 / 127.0));
-  const bool empty = scale == 0.0f;
-  if (tid == 0) a.scales[row] = empty ? 1.0f : scale;
-  // A code from float32: adding 1.5 2^23 leaves the nearest whole number (ties
-  // to even) in a float's low bits.  h w and 127 / P are off by half a step each,
-  // so their product (formed within a fused addition, not rounded) by less than
-  // 127 * 2.1 * 2^-24 < 2^-15: unless it is that close to a border, its nearest
-  // whole number is the code.  Otherwise, and where float32 could overflow or go
-  // subnormal, the float64 quotient decides.
-  constexpr float MAGIC = 12582912.0f;
-  const float c127 = (float)(127.0 * reciprocal(top));
-  const bool plain = top > 1e-25 && top < 1e30;
-  int8_t* o = (int8_t*)a.out + row * a.ldo;
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     uint32_t q[8];
-    float off = 0.0f;  // farthest from a whole number
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float hw = h[v][e] * element(w[v], e), k = fmaf(hw, c127, MAGIC);
-      off = fmaxf(off, fabsf(fmaf(hw, c127, MAGIC - k)));
-      q[e] = __float_as_uint(k);
-    }
-    if (off >= 0.5f - 3.0517578125e-05f || !plain) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        q[e] = empty ? 0u
-                     : (uint32_t)(int)rint(127.0 * ((double)h[v][e] * (double)element(w[v], e)) / top);
-    }
-    if constexpr (VEC) {
-      const int c = column<VEC>(v, 0);
-      uint32_t b[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        b[e] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(q[4 * e + 3], q[4 * e + 2], 0x0c0c0400u),
-                                     __builtin_amdgcn_perm(q[4 * e + 1], q[4 * e], 0x0c0c0400u),
-                                     0x05040100u);
-      if (c < a.d) *(uint2*)(o + c) = make_uint2(b[0], b[1]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = column<VEC>(v, e);
-        if (c < a.d) o[c] = (int8_t)q[e];
-      }
-    }
+    codes8<W>(o, h[v], w[v], q);
+    store8_codes<VEC>(a.out + row * a.ldo, at(v), a.d, q);
   }
 }
 
-// Rows longer than REG_D: h is formed twice, from x and r again.
-__global__ __launch_bounds__(1024) void add_rmsnorm_long_kernel(NormArgs a, int x_f32, int r_f32,
-                                                                int w_f32) {
+// Rows longer than REG_D: h is formed twice, from x and r again (R_out, which
+// may be R, is written the second time).
+template <Kind X, Kind R, Kind W>
+__global__ __launch_bounds__(1024) void add_rmsnorm_long_kernel(NormArgs a) {
   __shared__ double red[2][16];
+  constexpr int RB = R == F32 ? 4 : 2;
   const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
-  auto load = [](const char* p, int64_t i, int f32) __attribute__((always_inline)) {
-    return f32 ? ((const float*)p)[i] : bf16_bits_to_float(((const uint16_t*)p)[i]);
+  auto load = [&](int c, float h[8], Raw<W>& w) __attribute__((always_inline)) {
+    Raw<X> x;
+    Raw<R == NONE ? BF16 : R> r;
+    load8<X, false>(a.x + row * a.ldx * (X == F32 ? 4 : 2), c, a.d, x);
+    if constexpr (R != NONE) load8<R, false>(a.r + row * a.ldr * RB, c, a.d, r);
+    load8<W, false>(a.w, c, a.d, w);
+    sum8<X, R, false>(x, r, c, a.d, h);
   };
-  auto h_at = [&](int c) __attribute__((always_inline)) {
-    float h = load(a.x, row * a.ldx + c, x_f32);
-    if (a.r) {
-      h += load(a.r, row * a.ldr + c, r_f32);
-      if (!r_f32) h = __uint_as_float(bf16_bits(h) << 16);
-    }
-    return h;
-  };
+  const int step = 8 * blockDim.x;
   double sum = 0.0, top = 0.0, odd = 0.0;
-  for (int c = tid; c < a.d; c += 1024) {
-    const double hd = (double)h_at(c), p = hd * (double)load(a.w, c, w_f32);
-    sum = fma(hd, hd, sum);
-    top = fmax(top, fabs(p));
-    odd = fma(p, 0.0, odd);
+  for (int c = 8 * threadIdx.x; c < a.d; c += step) {
+    float h[8];
+    Raw<W> w;
+    load(c, h, w);
+    gather8<W>(h, w, sum, top, odd);
   }
   if (a.out_i8) sum += odd;
   fold_row(sum, top, red);
-  const double ms = fma(sum, a.inv_d, a.eps);
-  const double rstd = ms == 0.0 || ms == INFINITY ? 0.0 : reciprocal_root(ms);
-  const float scale = (float)(top * rstd * (1.0 / 127.0));
-  const bool empty = scale == 0.0f;
-  if (a.out_i8 && tid == 0) a.scales[row] = empty ? 1.0f : scale;
-  for (int c = tid; c < a.d; c += 1024) {
-    const float h = h_at(c);
-    const double p = (double)h * (double)load(a.w, c, w_f32);
-    if (a.r_out) {  // R_out may be R: this element of it has been read
-      if (r_f32)
-        ((float*)a.r_out)[row * a.ldro + c] = h;
-      else
-        ((uint16_t*)a.r_out)[row * a.ldro + c] = (uint16_t)(__float_as_uint(h) >> 16);
+  const RowOut o = row_out(a, sum, top);
+  for (int c = 8 * threadIdx.x; c < a.d; c += step) {
+    float h[8];
+    Raw<W> w;
+    load(c, h, w);
+    if constexpr (R != NONE) {
+      if (a.r_out) store8<R, false>(a.r_out + row * a.ldro * RB, c, a.d, raw_of<R>(h));
     }
-    if (a.out_i8)
-      ((int8_t*)a.out)[row * a.ldo + c] = empty ? 0 : (int8_t)(int)rint(127.0 * p / top);
-    else
-      ((uint16_t*)a.out)[row * a.ldo + c] = (uint16_t)bf16_bits((float)(p * rstd));
+    if (a.out_i8) {
+      uint32_t q[8];
+      codes8<W>(o, h, w, q);
+      store8_codes<false>(a.out + row * a.ldo, c, a.d, q);
+    } else {
+      store8<BF16, false>(a.out + row * a.ldo * 2, c, a.d, bf16_of<W>(o, h, w));
+    }
   }
 }
 
@@ -376,6 +470,11 @@ void launch(const NormArgs& a, int64_t m, int threads, bool vec, hipStream_t str
 
 template <Kind X, Kind R, Kind W>
 void launch_sized(const NormArgs& a, int64_t m, bool vec, hipStream_t stream) {
+  if (a.d > REG_D) {
+    hipLaunchKernelGGL((add_rmsnorm_long_kernel<X, R, W>), dim3((unsigned)m), dim3(1024), 0, stream,
+                       a);
+    return;
+  }
   // Enough rows to fill the chip: 256 threads, each with more loads in flight
   // (16384 x 8192 bf16: 181 us with 32 elements per thread, 200 and 249 us with
   // 16 and 8).  Few rows: more threads finish a row sooner, to a point (one row
@@ -418,10 +517,7 @@ hipError_t add_rmsnorm_launch(const void* X, int x_dtype, int64_t ldx, const voi
   constexpr int64_t ROWS = (int64_t)1 << 21;
   for (int64_t left = m; left > 0; left -= ROWS) {
     const int64_t n = left < ROWS ? left : ROWS;
-    if (d > REG_D)
-      hipLaunchKernelGGL(add_rmsnorm_long_kernel, dim3((unsigned)n), dim3(1024), 0, stream, a, xf,
-                         rf, wf);
-    else if (!R)
+    if (!R)
       xf ? launch_w<F32, NONE>(a, n, wf, vec, stream) : launch_w<BF16, NONE>(a, n, wf, vec, stream);
     else if (rf)
       xf ? launch_w<F32, F32>(a, n, wf, vec, stream) : launch_w<BF16, F32>(a, n, wf, vec, stream);

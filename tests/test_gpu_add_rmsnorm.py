@@ -133,6 +133,25 @@ def test_add_rmsnorm_matches_oracle(m, d, xk, rk, wk, ok, pad, skew):
         np.testing.assert_array_equal(R.float().cpu().numpy(), oracle.residual_sum(x, r, rk))
 
 
+@pytest.mark.parametrize("xk,rk,wk,ok", [("bf16", "bf16", "f32", "i8"), ("f32", "bf16", "bf16", "bf16"),
+                                         ("bf16", "f32", "bf16", "i8"), ("f32", "f32", "f32", "bf16")])
+@pytest.mark.parametrize("near", [8, 16, 512, 1024, 4096, 16384, 16896])
+def test_add_rmsnorm_every_last_piece(near, xk, rk, wk, ok):
+    """Rows that end one to eight elements into their last piece, the first of a wave or a thread's
+    next; updated in place, with a guard behind every row."""
+    rng = np.random.default_rng(near)
+    for d in range(near - 1, near + 8):
+        x, r, w = values(rng, 3, d, xk), values(rng, 3, d, rk), values(rng, 1, d, wk)[0]
+        X, W = dev(x, xk, 1, 1), dev(w[None], wk, 0, 1)[0]
+        rbuf, R = out_buffer(3, d, rk, 3, 1)
+        R.copy_(dev(r, rk))
+        obuf, out = out_buffer(3, d, ok, 3, 1)
+        o, s, h = gptq.gptq_add_rmsnorm(X, W, residual=R, residual_out=R, out_dtype=T[ok], out=out)
+        torch.cuda.synchronize()
+        check(x, r, w, rk, 1e-6, ok, o, s, h)
+        assert untouched(obuf, out) and untouched(rbuf, R)
+
+
 def test_add_rmsnorm_residual_sum_not_stored():
     rng = np.random.default_rng(2)
     for d in (96, 97):
