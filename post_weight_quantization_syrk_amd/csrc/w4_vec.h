@@ -4,7 +4,12 @@
 //
 // A workgroup owns 16 R weight rows and all tokens.  Its waves take blocks of
 // 512 k in turn, each with two buffers of its own in LDS, so that no wave
-// waits for another, and their sums meet at the end, in wave order.  A step is
+// waits for another, and their sums meet at the end, in wave order.  (Past 32
+// tokens of bf16 those buffers leave room for three or four waves, and the
+// tokens, read again for every 16 R rows, are more than the weights: in large
+// layers four waves of different rows share them, with a barrier per step.  64
+// tokens through 28672 x 8192: 115 us without, 68 with; through 4096 x 11008,
+// 28 and 24.)  A step is
 // 128 k: 64 bytes of each weight row and the tokens' pieces, loaded straight
 // into LDS with four neighbouring lanes on 64 consecutive bytes.  (Loaded into
 // registers as the matrix instructions want them, neighbouring lanes are in
@@ -121,43 +126,61 @@ __device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
 
 constexpr int LDS_BYTES = 160 * 1024;
 
-// LDS of a wave: two steps' words and tokens, and a word with the scale and
-// zero of each row and group of a block.
-constexpr int wave_bytes(bool i8, int nt, int r, int G) {
-  return 2 * (1024 * r + 16 * nt * KCH * (i8 ? 1 : 2)) + (G == 0 ? 0 : KBLK / G * 16 * r * 4);
+// LDS of a wave: two steps' words, and a word with the scale and zero of each
+// row and group of a block; and of the waves that share them two steps' tokens.
+constexpr int words_bytes(int r, int G) {
+  return 2 * 1024 * r + (G == 0 ? 0 : KBLK / G * 16 * r * 4);
+}
+constexpr int tokens_bytes(bool i8, int nt) { return 2 * 16 * nt * KCH * (i8 ? 1 : 2); }
+
+// LDS of a workgroup of `slots` times rs waves; their sums go where the buffers
+// were.
+constexpr int group_bytes(bool i8, int nt, int r, int G, int rs, int slots) {
+  const int sums = slots * rs * r * nt * 4 * 256;
+  const int bytes = slots * (rs * words_bytes(r, G) + tokens_bytes(i8, nt));
+  return bytes > sums ? bytes : sums;
 }
 
-template <bool I8, int NT, int R, int G>
+// Slots that fit: eight waves at most.
+constexpr int most_slots(bool i8, int nt, int r, int G, int rs) {
+  int slots = 8 / rs;
+  while (slots > 1 && group_bytes(i8, nt, r, G, rs, slots) > LDS_BYTES) --slots;
+  return slots;
+}
+
+template <bool I8, int NT, int R, int G, int RS>
 struct Shape {
   static constexpr int XB = I8 ? 1 : 2;
   static constexpr int WBYTES = 1024 * R;             // a step's words
   static constexpr int XBYTES = 16 * NT * KCH * XB;   // a step's tokens
-  static constexpr int STAGE = WBYTES + XBYTES;
   static constexpr int GPB = G == 0 ? 0 : KBLK / G;   // groups per block
-  static constexpr int WAVE = wave_bytes(I8, NT, R, G);
-  static constexpr int WAVES = LDS_BYTES / WAVE < 8 ? LDS_BYTES / WAVE : 8;
-  static_assert(WAVES * WAVE <= LDS_BYTES, "LDS");
-  static_assert(WAVE >= R * NT * 4 * 256, "the wave's sums reuse its buffers");
+  static constexpr int WORDS = words_bytes(R, G);
+  static constexpr int SLOT = RS * WORDS + 2 * XBYTES;
+  static constexpr int SLOTS = most_slots(I8, NT, R, G, RS);
+  static_assert(group_bytes(I8, NT, R, G, RS, SLOTS) <= LDS_BYTES, "LDS");
 };
 
 // I8: int8 X; NT: tiles of 16 tokens; R: tiles of 16 weight rows; G: group
-// size, 0 for one group per row.
-template <bool I8, int NT, int R, int G>
-__global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kernel(VecArgs a) {
+// size, 0 for one group per row; RS: waves that share the tokens' buffers.
+template <bool I8, int NT, int R, int G, int RS>
+__global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4_vec_kernel(VecArgs a) {
   typedef typename Types<I8>::acc_t acc_t;
-  typedef Shape<I8, NT, R, G> S;
+  typedef Shape<I8, NT, R, G, RS> S;
   constexpr bool TR = G == 32 || G == 64;
   constexpr int GPC = G == 0 ? 1 : KCH / G;  // groups per step
   constexpr int XB = S::XB;
-  constexpr int XD = NT * XB * 2;            // direct loads of a step's tokens
+  constexpr int XD = (NT * XB * 2 + RS - 1) / RS;  // a wave's direct loads of a step's tokens
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+  const int lane = threadIdx.x & 63, w0 = threadIdx.x >> 6;
+  const int wave = w0 / RS, waves = (int)(blockDim.x >> 6) / RS, rs = w0 % RS;  // k slot; rows
   const int l16 = lane & 15, h = lane >> 4;
-  const int n0 = blockIdx.x * 16 * R;
+  const int n0 = (blockIdx.x * RS + rs) * 16 * R;
   const int row_bytes = a.k / 2;
-  char* const mine = smem + wave * S::WAVE;
-  const uint32_t mine_off = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)mine;
-  uint32_t* const sc = (uint32_t*)(mine + 2 * S::STAGE);
+  char* const words = smem + wave * S::SLOT + rs * S::WORDS;
+  char* const tokens = smem + wave * S::SLOT + RS * S::WORDS;
+  const uint32_t words_off = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)words;
+  const uint32_t tokens_off = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)tokens;
+  uint32_t* const sc = (uint32_t*)(words + 2 * S::WBYTES);
 
   // steps of this wave: blocks wave, wave + waves, ...; only the row's last
   // block may hold fewer than four
@@ -183,11 +206,12 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
   int xu[XD];
 #pragma unroll
   for (int i = 0; i < XD; ++i) {
-    const int t = I8 ? 8 * i + (lane >> 3) : 4 * i + (lane >> 4);
+    const int ii = RS * i + rs, t = I8 ? 8 * ii + (lane >> 3) : 4 * ii + (lane >> 4);
     xrow[i] = a.x + (int64_t)min(t, a.m - 1) * a.ldx;
     xu[i] = 16 * (I8 ? (lane & 7) ^ ((t >> 1) & 7) : (lane & 15) ^ (t & 15));
   }
-  const int nx = I8 ? (a.m + 7) / 8 : (a.m + 3) / 4;  // loads of tokens that are there
+  // loads of tokens that are there
+  const int nx = ((I8 ? (a.m + 7) / 8 : (a.m + 3) / 4) + RS - 1 - rs) / RS;
   auto wait_older = [&]() __attribute__((always_inline)) {
     // all but the newest step's R + nx loads (or fewer: that waits longer)
     if (nx == XD)
@@ -199,7 +223,8 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
   };
   auto issue = [&](int i) __attribute__((always_inline)) {
     const int c = chunk(i);
-    const uint32_t dst = mine_off + (i & 1) * S::STAGE;
+    const uint32_t dst = words_off + (i & 1) * S::WBYTES;
+    const uint32_t xdst = tokens_off + (i & 1) * S::XBYTES + 1024 * rs;
 #pragma unroll
     for (int r = 0; r < R; ++r)
       dma16_at(qrow[r] + min(c * (KCH / 2) + qu, row_bytes - 16), dst + 1024 * r);
@@ -208,7 +233,7 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
       // (whole loads past the last token are left out: their rows hold whatever
       // is there, in sums that are not stored)
       if (j < nx)
-        dma16_at(xrow[j] + min(c * KCH * XB + xu[j], a.k * XB - 16), dst + S::WBYTES + 1024 * j);
+        dma16_at(xrow[j] + min(c * KCH * XB + xu[j], a.k * XB - 16), xdst + 1024 * RS * j);
     }
   };
   auto zero_bits = [](uint16_t z) __attribute__((always_inline)) {
@@ -284,8 +309,8 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
 
   auto compute = [&](int i) __attribute__((always_inline)) {
     const int c = chunk(i);
-    const char* st = mine + (i & 1) * S::STAGE;
-    const char* xs = st + S::WBYTES;
+    const char* st = words + (i & 1) * S::WBYTES;
+    const char* xs = tokens + (i & 1) * S::XBYTES;
     const bool tail = (c + 1) * KCH > a.k;  // pieces past the row's end count as zeros
     uint32_t w[R][4];
 #pragma unroll
@@ -410,17 +435,31 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
   };
 
   if (nst > 0) issue(0);
-  for (int i = 0; i < nst; ++i) {
-    // every read of the other buffer has returned before it is written again
-    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if ((i & 3) == 0) scales(chunk(i) >> 2);
-    if (i + 1 < nst) {
-      issue(i + 1);
-      wait_older();
-    } else {
-      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if constexpr (RS == 1) {
+    for (int i = 0; i < nst; ++i) {
+      // every read of the other buffer has returned before it is written again
+      __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if ((i & 3) == 0) scales(chunk(i) >> 2);
+      if (i + 1 < nst) {
+        issue(i + 1);
+        wait_older();
+      } else {
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      compute(i);
     }
-    compute(i);
+  } else {
+    // slot 0 has the most steps, and every wave comes to each step's barrier
+    const int most = 4 * ((nblk - 1) / waves + 1);
+    for (int i = 0; i < most; ++i) {
+      if ((i & 3) == 0 && i < nst) scales(chunk(i) >> 2);
+      // this wave's loads have landed and its reads have returned; behind the
+      // barrier that holds for all of them
+      __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (i + 1 < nst) issue(i + 1);
+      if (i < nst) compute(i);
+    }
   }
   if constexpr (G == 0) {
 #pragma unroll
@@ -431,7 +470,12 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
         for (int e = 0; e < 4; ++e) tot[r][t][e] = join(0.0f, row_sz[r], acc0[r][t][e], one0[t][e]);
   }
   constexpr int PER = R * NT * 4;
-  float* const out = (float*)mine;  // this wave's buffers are done with
+  // sums over the buffers: a wave's own, or, where they are shared, all of them
+  // once every wave is done
+  constexpr int OUT = RS == 1 ? S::SLOT / 4 : PER * 64;  // floats
+  static_assert(OUT >= PER * 64, "the wave's sums reuse its buffers");
+  if constexpr (RS > 1) __syncthreads();
+  float* const out = (float*)smem + (rs * waves + wave) * OUT;
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
@@ -441,7 +485,7 @@ __global__ __launch_bounds__((64 * Shape<I8, NT, R, G>::WAVES)) void w4_vec_kern
   __syncthreads();
   for (int e = wave; e < PER; e += waves) {
     float v = 0.0f;
-    for (int w = 0; w < waves; ++w) v += ((const float*)(smem + w * S::WAVE))[e * 64 + lane];
+    for (int w = 0; w < waves; ++w) v += ((const float*)smem)[(rs * waves + w) * OUT + e * 64 + lane];
     const int i = e & 3, t = (e >> 2) % NT, r = (e >> 2) / NT;
     const int token = 16 * t + 4 * h + i, n = n0 + 16 * r + l16;
     if (token < a.m && n < a.n) {
@@ -471,73 +515,92 @@ inline hipError_t join_launch(const float* part, const float* sx, int64_t m, int
   return hipGetLastError();
 }
 
-template <bool I8, int NT, int R, int G>
+template <bool I8, int NT, int R, int G, int RS>
 hipError_t vec_launch_one(const VecArgs& a, hipStream_t stream) {
-  typedef Shape<I8, NT, R, G> S;
-  const int waves = std::min(S::WAVES, a.per_split);  // no more than there are blocks
-  const size_t lds = (size_t)waves * S::WAVE;
-  hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G>), dim3((unsigned)ceil_div(a.n, 16 * R), a.splits),
-                     dim3(64 * waves), lds, stream, a);
+  typedef Shape<I8, NT, R, G, RS> S;
+  const int slots = std::min(S::SLOTS, a.per_split);  // no more than there are blocks
+  hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G, RS>),
+                     dim3((unsigned)ceil_div(a.n, 16 * R * RS), a.splits), dim3(64 * RS * slots),
+                     group_bytes(I8, NT, R, G, RS, slots), stream, a);
   return hipGetLastError();
 }
 
-template <bool I8, int NT, int R>
+template <bool I8, int NT, int R, int RS>
 hipError_t vec_launch_g(const VecArgs& a, int G, hipStream_t stream) {
   switch (G) {
-    case 32: return vec_launch_one<I8, NT, R, 32>(a, stream);
-    case 64: return vec_launch_one<I8, NT, R, 64>(a, stream);
-    case 128: return vec_launch_one<I8, NT, R, 128>(a, stream);
-    default: return vec_launch_one<I8, NT, R, 0>(a, stream);
+    case 32: return vec_launch_one<I8, NT, R, 32, RS>(a, stream);
+    case 64: return vec_launch_one<I8, NT, R, 64, RS>(a, stream);
+    case 128: return vec_launch_one<I8, NT, R, 128, RS>(a, stream);
+    default: return vec_launch_one<I8, NT, R, 0, RS>(a, stream);
   }
 }
 
+// Waves share the tokens' buffers only where these are large: bf16, past 32
+// tokens (17 to 32: 32 tokens through 28672 x 8192 take 51 us either way).
+constexpr int SHARE = 4;
+constexpr bool may_share(bool i8, int nt) { return !i8 && nt >= 3; }
+
 struct VecPlan {
-  int r;  // tiles of 16 weight rows per workgroup
+  int r;   // tiles of 16 weight rows per wave
+  int rs;  // waves that share the tokens' buffers
   int splits, per_split;
   size_t ws_bytes;
 };
 
-// Weight rows per workgroup (16 r) and workgroups that share a row's k, by the
-// least of a time in us.  A step of a workgroup's waves takes 0.27 (2 + r) us
-// with 16 tokens and a third more with every 16 further ones (4096 x 4096, 16
-// tokens: 0.8, 1.1 and 1.6 us for r = 1, 2, 4); workgroups beyond what the 256
-// CUs hold wait for a round of their own, which costs 2 us to start and end;
-// splits add a launch and their sums' bytes.  More rows read X fewer times, fewer of them spread further: 16
+// Weight rows per workgroup (16 r, or 64 r where waves share the tokens) and
+// workgroups that share a row's k, by the least of a time in us.  A step of a
+// workgroup's waves takes 0.27 (2 + r) us with 16 tokens and a third more with
+// every 16 further ones (4096 x 4096, 16 tokens: 0.8, 1.1 and 1.6 us for r = 1,
+// 2, 4); with sharing waves also 6 us to start and end, and more for small
+// groups, which are hidden less.  Workgroups beyond what the 256 CUs hold wait
+// for a round of their own, which costs 2 us; splits add a launch and their
+// sums' bytes.  More rows read X fewer times, fewer of them spread further: 16
 // tokens through 11008 x 4096 take 16.1, 13.9, 10.6 and 11.7 us with r = 1 to
-// 4, through 4096 x 4096 5.6, 6.7 and 8.9 us with 1, 2 and 4; 64 tokens
-// through 1024 x 8192 12.1 us in four splits and 24.5 in one, through 4096 x
-// 11008 30 us with r = 2 in two splits and 45 with r = 1 in one.
+// 4, through 4096 x 4096 5.6, 6.7 and 8.9 us with 1, 2 and 4; 64 tokens through
+// 1024 x 8192 12.1 us in four splits and 24.5 in one; through 11008 x 4096 23 us
+// and 25 with sharing waves, through 8192 x 8192 32 and 29.5, through 16384 x
+// 12288 98 and 67.
 inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
-  VecPlan p = {1, 1, 1, 0};
+  VecPlan p = {1, 1, 1, 1, 0};
   const int nt = (int)ceil_div(m, 16), nblk = (int)ceil_div(k, KBLK);
   double least = 0.0;
-  for (int r = 1; r <= 4; ++r)
-    for (int s = 1; s <= 8 && s <= nblk; ++s) {
-      const int per = (int)ceil_div(nblk, s);
-      const int waves = std::min(per, std::min(8, LDS_BYTES / wave_bytes(i8, nt, r, G)));
-      const int64_t groups = ceil_div(n, 16 * r) * s;
-      const bool several = 2 * waves * wave_bytes(i8, nt, r, G) <= LDS_BYTES;  // per CU
-      const double rounds = several ? std::max(1.0, groups / 256.0) : (double)ceil_div(groups, 256);
-      const double steps = 2.0 * (ceil_div(per, waves) + (double)per / waves);  // most and mean
-      double us = rounds * 0.27 * (2 + r) * (1.0 + 0.35 * (nt - 1)) * steps;
-      if (!several) us += 2.0 * (rounds - 1.0);  // a round's start and end
-      if (s > 1) us += 2.5 + 1e-6 * (double)(m * n) * (s + 1);
-      if (least == 0.0 || us < least) {
-        least = us;
-        p.r = r, p.per_split = per, p.splits = (int)ceil_div(nblk, per);
+  for (int rs = 1; rs <= SHARE; rs += SHARE - 1)
+    for (int r = rs == 1 ? 1 : 2; r <= 4; ++r)
+      for (int s = 1; s <= 8 && s <= nblk; ++s) {
+        if (rs > 1 && !may_share(i8, nt)) continue;
+        const int per = (int)ceil_div(nblk, s), waves = std::min(per, most_slots(i8, nt, r, G, rs));
+        const int64_t groups = ceil_div(n, 16 * r * rs) * s;
+        const bool several = 2 * group_bytes(i8, nt, r, G, rs, waves) <= LDS_BYTES;  // per CU
+        const double rounds =
+            several ? std::max(1.0, groups / 256.0) : (double)ceil_div(groups, 256);
+        const double steps = 2.0 * (ceil_div(per, waves) + (double)per / waves);  // most and mean
+        double us = rounds * 0.27 * (2 + r) * (1.0 + 0.35 * (nt - 1)) * steps;
+        if (rs > 1) us = 6.0 + us * (G == 32 ? 1.4 : G == 64 ? 1.25 : 1.0);
+        if (!several) us += 2.0 * (rounds - 1.0);  // a round's start and end
+        if (s > 1) us += 2.5 + 1e-6 * (double)(m * n) * (s + 1);
+        if (least == 0.0 || us < least) {
+          least = us;
+          p.r = r, p.rs = rs, p.per_split = per, p.splits = (int)ceil_div(nblk, per);
+        }
+        if (per <= waves) break;  // a wave has one block: no fewer steps
       }
-      if (per <= waves) break;  // a wave has one block: no fewer steps
-    }
   p.ws_bytes = p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
   return p;
 }
 
 template <bool I8, int NT>
-hipError_t vec_launch_t(const VecArgs& a, int r, int G, hipStream_t stream) {
-  if (r == 4) return vec_launch_g<I8, NT, 4>(a, G, stream);
-  if (r == 3) return vec_launch_g<I8, NT, 3>(a, G, stream);
-  if (r == 2) return vec_launch_g<I8, NT, 2>(a, G, stream);
-  return vec_launch_g<I8, NT, 1>(a, G, stream);
+hipError_t vec_launch_t(const VecArgs& a, int r, int rs, int G, hipStream_t stream) {
+  if constexpr (may_share(I8, NT)) {
+    if (rs > 1) {
+      if (r == 4) return vec_launch_g<I8, NT, 4, SHARE>(a, G, stream);
+      if (r == 3) return vec_launch_g<I8, NT, 3, SHARE>(a, G, stream);
+      return vec_launch_g<I8, NT, 2, SHARE>(a, G, stream);
+    }
+  }
+  if (r == 4) return vec_launch_g<I8, NT, 4, 1>(a, G, stream);
+  if (r == 3) return vec_launch_g<I8, NT, 3, 1>(a, G, stream);
+  if (r == 2) return vec_launch_g<I8, NT, 2, 1>(a, G, stream);
+  return vec_launch_g<I8, NT, 1, 1>(a, G, stream);
 }
 
 template <bool I8>
@@ -546,10 +609,10 @@ hipError_t vec_launch(VecArgs a, int G, void* ws, hipStream_t stream) {
   float* const y = a.y;
   if (p.splits > 1) a.y = (float*)ws;
   a.splits = p.splits, a.per_split = p.per_split;
-  hipError_t e = a.m <= 16   ? vec_launch_t<I8, 1>(a, p.r, G, stream)
-                 : a.m <= 32 ? vec_launch_t<I8, 2>(a, p.r, G, stream)
-                 : a.m <= 48 ? vec_launch_t<I8, 3>(a, p.r, G, stream)
-                             : vec_launch_t<I8, 4>(a, p.r, G, stream);
+  hipError_t e = a.m <= 16   ? vec_launch_t<I8, 1>(a, p.r, p.rs, G, stream)
+                 : a.m <= 32 ? vec_launch_t<I8, 2>(a, p.r, p.rs, G, stream)
+                 : a.m <= 48 ? vec_launch_t<I8, 3>(a, p.r, p.rs, G, stream)
+                             : vec_launch_t<I8, 4>(a, p.r, p.rs, G, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   return join_launch(a.y, I8 ? a.sx : nullptr, a.m, a.n, p.splits, y, stream);
 }

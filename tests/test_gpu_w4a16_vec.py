@@ -88,6 +88,25 @@ CASES = [
     (12, 9280, 40, 64, True, None),
     (40, 6272, 300, 128, False, None),
     (64, 5152, 2100, -1, False, None),
+    # past 32 tokens of larger layers: waves that share the tokens' buffers, over every group size
+    # and number of rows; a last split, block and step that are not whole
+    (49, 5216, 4099, 32, False, None),
+    (64, 5184, 4100, 64, False, None),
+    (50, 5248, 4101, 128, False, 5272),
+    (49, 5152, 6100, -1, True, None),
+    (33, 8160, 4100, -1, False, None),
+    (49, 8128, 4100, 64, False, None),
+    (33, 8064, 4100, 128, False, None),
+    (49, 8160, 4100, 32, True, 8248),
+    (33, 6176, 9001, -1, False, None),
+    (33, 6144, 9000, 32, False, None),
+    (49, 4160, 12290, 64, False, None),
+    (49, 6272, 8190, 128, True, None),
+    (40, 5216, 9000, 32, False, 5240),
+    (64, 6176, 8190, -1, False, None),
+    (49, 8064, 4100, 128, True, None),
+    (49, 8032, 4100, -1, False, None),
+    (40, 8256, 9000, 64, False, None),
 ]
 
 
