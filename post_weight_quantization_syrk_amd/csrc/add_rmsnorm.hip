@@ -9,12 +9,12 @@
 // Bound by memory: x and r are read once, h and the output written once.  A
 // workgroup holds a row in registers between the one reduction (of sum h^2 and
 // max |p|, together) and the output, so no row is read twice and no second
-// launch is needed.  The reductions are in
-// float64: its operations run at the rate of float32 ones here, and squares
-// neither overflow nor vanish.  The vector units come next (61% busy at 16384 x
-// 8192 with bf16 output): divisions are done as reciprocals with an iteration,
-// and a code takes six operations (4096 x 4096, 31.6 us with divisions, rounding
-// and conversions as such, 27.5 so).
+// launch is needed.  The reductions are in float64: its operations run at the
+// rate of float32 ones here, and squares neither overflow nor vanish.  The
+// vector units come next (57% busy at 16384 x 8192 with bf16 output): divisions
+// are done as reciprocals with an iteration, and a code takes six operations
+// (4096 x 4096 to 8 bits, 31.6 us with divisions, rounding and conversions as
+// such, 27.5 so).
 // Measured, residual and all, GPU time per call in a replayed graph: 16384 x
 // 8192 bf16 181 us (5.9 TB/s; a large copy reaches 4.9), in 8 bits 165 (5.7);
 // 4096 x 4096 in 8 bits 27.5 (4.3); 1000 x 5003 float32, unaligned rows, 14.3
