@@ -307,7 +307,8 @@ int gptq_w4a16_matmul(const void* X, int64_t m, int64_t ldx, const uint32_t* qwe
  *               GPTQ_EUNSUPPORTED: gptq_w4a16_matmul takes any m).
  *   qweight     16-byte aligned.
  *   ws          gptq_w4a16_matvec_workspace(m, d_out, d_in, group_size) bytes
- *               (0 for most shapes); its contents on entry do not matter, and
+ *               (0 unless a row's k is split, over workgroups, for few rows or
+ *               many tokens); its contents on entry do not matter, and
  *               calls in flight together need one each.
  * The weights are read once.  Per group, sum x q and sum x are formed with
  * exact products and fp32 sums and joined as s (sum x q - z sum x); groups
