@@ -241,3 +241,18 @@ def test_matvec_weights_past_two_gigabytes():
         qw = Q[rows].cpu().numpy().view(np.uint32)
         s16 = S[rows].cpu().numpy().view(np.uint16)
         check(Y[:, rows], X.double().cpu().numpy(), qw, s16, None, True, g)
+
+
+@pytest.mark.parametrize("m,d_in,d_out,g", [(5, 544, 70, -1), (17, 1056, 65, 32), (40, 640, 97, 64),
+                                            (49, 5216, 4099, 32)])
+def test_matvec_values_that_are_not_finite_stay_in_their_row(m, d_in, d_out, g):
+    X, x64, qw, s16, z16 = make(m, d_in, d_out, g, False, seed=m)
+    Q, S, Z = dev_weights(qw, s16, z16)
+    want = gptq.gptq_w4a16_matvec(X, Q, S, Z, group_size=g, sym=False)
+    bad = [1, m - 1]
+    X[1, d_in - 1] = float("inf")
+    X[m - 1, 0] = float("nan")
+    got = gptq.gptq_w4a16_matvec(X, Q, S, Z, group_size=g, sym=False)
+    keep = [i for i in range(m) if i not in bad]
+    assert torch.equal(got[keep], want[keep])
+    assert not torch.isfinite(got[bad]).any()
