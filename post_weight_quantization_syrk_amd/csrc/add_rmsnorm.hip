@@ -319,9 +319,9 @@ __device__ __forceinline__ RowOut row_out(const NormArgs& a, double sum, double 
   o.rstd = ms == 0.0 || ms == INFINITY ? 0.0 : reciprocal_root(ms);
   o.top = top;
   o.c127 = (float)(127.0 * reciprocal(top));
-  o.plain = top > 1e-25 && top < 1e30;
   const float scale = (float)(top * o.rstd * (1.0 / 127.0));
-  o.empty = scale == 0.0f;
+  o.empty = scale == 0.0f;  // also with an ordinary top, where the mean square is large enough
+  o.plain = !o.empty && top > 1e-25 && top < 1e30;
   if (a.out_i8 && threadIdx.x == 0) a.scales[blockIdx.x] = o.empty ? 1.0f : scale;
   return o;
 }

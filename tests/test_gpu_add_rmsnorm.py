@@ -216,6 +216,50 @@ def test_add_rmsnorm_rows_of_zeros_and_extreme_values(d):
     assert bool((out == 0).all()) and bool((s == 1.0).all())
 
 
+@pytest.mark.parametrize("d", [40, 41, 4096, 4099, 16392])
+def test_add_rmsnorm_scale_that_rounds_to_zero(d):
+    """Rows whose codes would be ordinary ones (the largest |p| far above float32's smallest values)
+    but whose scale rounds to 0: scale 1 and zero codes.  The large entry that makes the scale
+    vanish carries a weight of 0, or every weight is subnormal.  These scales lie ten times or more
+    below the border, and the last two rows' far above it."""
+    rng = np.random.default_rng(d)
+    tail = rng.standard_normal((6, d)).astype(np.float32)
+    x = np.zeros((6, d), dtype=np.float32)
+    x[0, :2] = 3e38, 1e-9
+    x[1] = np.float32(1e-9) * tail[1]
+    x[1, 0] = 3e38
+    x[2] = np.float32(1e-20) * tail[2]
+    x[2, 0] = -1e30
+    x[3] = np.float32(1e-24) * tail[3]
+    x[3, 0] = 1e33
+    x[4] = np.float32(1e-20) * tail[4]  # a scale among the subnormals, not 0: codes as ever
+    x[4, 0] = 1e19
+    x[5] = tail[5]
+    w = np.ones(d, dtype=np.float32)
+    w[0] = 0.0
+    q, s = oracle.norm_codes(x, w, 1e-5)
+    assert (s[:4] == 1.0).all() and not q[:4].any() and (np.abs(q[4:]).max(1) == 127).all()
+    for xk in ("f32", "bf16"):
+        xv = oracle.round_bf16(x) if xk == "bf16" else x
+        for wk in ("f32", "bf16"):
+            W = dev(w[None], wk)[0]
+            out, sc, _ = gptq.gptq_add_rmsnorm(dev(xv, xk), W, eps=1e-5)
+            check(xv, None, w, None, 1e-5, "i8", out, sc, None)
+            assert bool((out[:4] == 0).all()) and bool((sc[:4] == 1.0).all())
+            zero = np.zeros_like(x)
+            for rk in ("f32", "bf16"):  # the same row by way of the residual, updated in place
+                R = dev(oracle.round_bf16(x) if rk == "bf16" else x, rk)
+                r = R.float().cpu().numpy()
+                out, sc, h = gptq.gptq_add_rmsnorm(dev(zero, xk), W, residual=R, residual_out=R,
+                                                   eps=1e-5)
+                check(zero, r, w, rk, 1e-5, "i8", out, sc, h)
+    w[:] = np.float32(2.0 ** -149)
+    x = (np.float32(1e25) * tail).astype(np.float32)
+    out, sc, _ = gptq.gptq_add_rmsnorm(dev(x, "f32"), dev(w[None], "f32")[0], eps=1e-5)
+    check(x, None, w, None, 1e-5, "i8", out, sc, None)
+    assert bool((out == 0).all()) and bool((sc == 1.0).all())
+
+
 @pytest.mark.parametrize("ok", ["i8", "bf16"])
 @pytest.mark.parametrize("eps", [0.0, 5e-324, 1e-310, 1e-30, 1e29])
 @pytest.mark.parametrize("d", [64, 67])
