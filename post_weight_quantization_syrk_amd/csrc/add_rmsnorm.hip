@@ -6,10 +6,10 @@
 // The norm's own factor cancels in the codes, so they depend on no sum's
 // order; p is exact in float64 and the quotient is formed there.
 //
-// Bound by memory: x and r are read once, h and the output written once.  A
-// workgroup holds a row in registers between the one reduction (of sum h^2 and
-// max |p|, together) and the output, so no row is read twice and no second
-// launch is needed.  The reductions are in float64: its operations run at the
+// Bound by memory.  A workgroup holds a row of up to 16384 in registers between
+// the one reduction (of sum h^2 and max |p|, together) and the output: x and r
+// are read once, h and the output written once.  (Longer rows are read twice, in
+// the same launch.)  The reductions are in float64: its operations run at the
 // rate of float32 ones here, and squares neither overflow nor vanish.  The
 // vector units come next (57% busy at 16384 x 8192 with bf16 output): divisions
 // are done as reciprocals with an iteration, and a code takes six operations

@@ -9,7 +9,8 @@
 // added over lanes, and over the waves that share a row, are final terms.
 //
 // Bound by reading the weights: 28672 x 8192, one scale per row, takes 24 us
-// (4.9 TB/s, what a large copy reaches).  Dot-product instructions, two bf16 or
+// (4.9 TB/s, what a large copy reaches; the norm's kernel, which writes half of
+// its bytes, reaches 5.9).  Dot-product instructions, two bf16 or
 // four int8 terms each, keep the vector units below that; matrix instructions
 // would do sixteen tokens' work for one, and their operands' layout spreads a
 // load over sixteen rows.  4096 x 4096 in groups of 128 takes 3.8 us, of which

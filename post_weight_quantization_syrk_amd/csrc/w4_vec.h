@@ -5,23 +5,30 @@
 // A workgroup owns 16 R weight rows and all tokens.  Its waves take blocks of
 // 512 k in turn, each with two buffers of its own in LDS, so that no wave
 // waits for another, and their sums meet at the end, in wave order.  (Past 32
-// tokens of bf16 those buffers leave room for three or four waves, and the
-// tokens, read again for every 16 R rows, are more than the weights: in large
-// layers four waves of different rows share them, with a barrier per step.  64
-// tokens through 28672 x 8192: 115 us without, 68 with; through 4096 x 11008,
-// 28 and 24.)  A step is
-// 128 k: 64 bytes of each weight row and the tokens' pieces, loaded straight
-// into LDS with four neighbouring lanes on 64 consecutive bytes.  (Loaded into
-// registers as the matrix instructions want them, neighbouring lanes are in
-// different rows, and the vector cache takes one lane per cycle: measured 63
-// accesses per load, 26 us for 16 tokens through 11008 x 4096.)
-// Bound: with one scale per row, weights as they arrive; with groups, the
-// vector units (taking codes apart, scaling each group's sums: 16 tokens through
-// 11008 x 4096 take 9.4 us with one scale per row, 10.5 in groups of 64; the
-// weights alone 5.0 at 4.9 TB/s), and the start and end of a workgroup (its
-// first loads and the waves' sums, some 2 us).  Three or four buffers per wave,
-// four waves with more rows each, and runs of consecutive k per wave in place of
-// blocks in turn (8 tokens through 28672 x 8192: 36 us for 33) were no faster.
+// tokens of bf16 those buffers leave room for four to six waves, past 48 for
+// three or four, and the tokens, read again for every 16 R rows, are more than
+// the weights: in large layers four waves of different rows share them, with a
+// barrier per step.  64 tokens through 28672 x 8192: 115 us without, 68 with;
+// through 4096 x 11008, 28 and 24.)  A step is 128 k: 64 bytes of each weight row
+// and the tokens' pieces, loaded straight into LDS with four neighbouring lanes on
+// 64 consecutive bytes.  (Loaded into registers as the matrix instructions want
+// them, neighbouring lanes are in different rows, and the vector cache takes one
+// lane per cycle: measured 63 accesses per load, 26 us for 16 tokens through 11008
+// x 4096.)
+// Bound: by no unit alone, but by waits that two waves per SIMD or fewer leave
+// open (counters).  16 tokens through 11008 x 4096 take 9.4 us with one scale per
+// row, 10.5 in groups of 64 (the weights alone 4.2 at 5.9 TB/s): waves wait for
+// loads and barriers 46% of their time (a workgroup's first loads and the waves'
+// sums at its end, some 2 us, among it) and for their turn to issue another 19%;
+// vector units (codes taken apart, groups' sums scaled) are busy 35% of the time
+// over the chip, matrix cores 7%.  37 tokens of int8 through 4099 x 11008 in
+// groups of 32: 172 workgroups of seven waves on 256 CUs; waits 37%, vector units
+// 37% over the chip, 55% on the CUs that have a workgroup.  32 and 64 tokens of
+// bf16 through 28672 x 8192 (50 and 65 us; the weights alone 21): waits 31 and
+// 36%, vector units 35 and 34%, matrix cores 16 and 24%.  Three or four
+// buffers per wave, four waves with more rows each, and runs of consecutive k per
+// wave in place of blocks in turn (8 tokens through 28672 x 8192: 36 us for 33)
+// were no faster.
 // For int8 X the zero is taken off the codes, four at a time.  For bf16 X that
 // would cost an operation per code: x q and x are summed apart (the sum of x by
 // the same instruction against ones, shared by all rows), and joined per group.

@@ -12,9 +12,10 @@
 // side along the weight rows), zeros are taken off four at a time, and X and the
 // scales are laid out before (w4a8_layout_kernel), so that both come by direct
 // loads and need no further work.
-// 8192 tokens through 28672 x 8192, groups of 128: 2.14 ms, 1.80 POP/s (1.86 ms,
-// 2.07 POP/s with one group per row; a library int8 product of 8192^3 reaches
-// 2.08), the vector units busy 75% of the cycles and the matrix cores 48%, at the
+// 8192 tokens through 28672 x 8192, groups of 128: 2.14 ms, 1.80 POP/s, calls
+// back to back and the layout's 28 us included (1.86 ms, 2.07 POP/s with one
+// group per row; a library int8 product of 8192^3 reaches 2.08; launches apart
+// under a tracer spread from 2.18 to 2.36 ms), the vector units busy 75% of the cycles and the matrix cores 48%, at the
 // 1.7 GHz that the chip's power allows.  515 tokens through 11008 x 4096, groups
 // of 64: 58 us.
 // Tried and slower or no faster: three buffers (515 tokens 59 -> 61 us), the
