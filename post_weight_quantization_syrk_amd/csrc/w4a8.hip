@@ -14,8 +14,8 @@
 // loads and need no further work.
 // 8192 tokens through 28672 x 8192, groups of 128: 2.14 ms, 1.80 POP/s, calls
 // back to back and the layout's 28 us included (1.86 ms, 2.07 POP/s with one
-// group per row; a library int8 product of 8192^3 reaches 2.08; launches apart
-// under a tracer spread from 2.18 to 2.36 ms), the vector units busy 75% of the cycles and the matrix cores 48%, at the
+// group per row; a library int8 product of 8192^3 reaches 2.08; 2.04 ms on
+// another card, and launches apart under a tracer 2.18 to 2.36), the vector units busy 75% of the cycles and the matrix cores 48%, at the
 // 1.7 GHz that the chip's power allows.  515 tokens through 11008 x 4096, groups
 // of 64: 58 us.
 // Tried and slower or no faster: three buffers (515 tokens 59 -> 61 us), the
