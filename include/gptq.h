@@ -402,6 +402,139 @@ int gptq_w4a8_matmul(const int8_t* X, const float* x_scales, int64_t m, int64_t 
 size_t gptq_w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size);
 
 /* ---------------------------------------------------------------------------
+ * The product with packed 4-bit weights (W4A16) and what follows it in a block:
+ * bias, activation, gate and residual.
+ *
+ *   v[i][n] = sum_k X[i][k] W_hat[n][k] + bias[n]
+ *   gated = 0:  Y[i][n] = act(v[i][n]) + residual[i][n],  0 <= n < d_out
+ *   gated = 1:  Y[i][n] = act(v[i][n]) v[i][F + n] + residual[i][n],
+ *               0 <= n < F = d_out / 2: weight rows 0..F-1 are the gate's, rows
+ *               F..2F-1 the up projection's, stacked as gptq_quantize_layers
+ *               leaves them.
+ *
+ * X           [m x ldx] bf16, row-major; 16-byte aligned, ldx a multiple of 8.
+ * qweight, scales_f16, zeros_f16, group_size, sym: as gptq_w4a16_matvec.  Zeros
+ *             are whole numbers, as gptq_pack writes them.
+ * bias        [d_out] of bias_dtype (bf16 or float32), or NULL: none.
+ * activation  a gptq_activation; GELU is v/2 (1 + erf(v / sqrt 2)),
+ *             GELU_TANH v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))).
+ * residual    [m x ldr] of res_dtype (bf16 or float32), or NULL: none.  It may be
+ *             Y itself (with ldr = ldy and one type): updated in place.  No other
+ *             overlap of Y with an input is allowed.
+ * Y           [m x ldy] out of y_dtype (bf16 or float32); columns past the used
+ *             ones are left as they were.
+ * m           0 (no-op) .. 2^30; d_in a multiple of 32, <= 65536.
+ * ws          gptq_w4a16_linear_workspace(...) bytes: 0 for most shapes of a few
+ *             tokens (m <= 64); for more, the scales laid out by groups, and parts
+ *             of the sums where k is split.  Its contents on entry do not matter;
+ *             calls in flight together need one each.
+ * Products are exact; sums, the group scaling and everything behind them are
+ * float32, rounded once to Y's type.  The order of every sum is fixed: the same
+ * inputs give the same bits.  An infinity or a NaN in a row of X does not reach
+ * other rows.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+  GPTQ_ACT_NONE = 0,
+  GPTQ_ACT_RELU = 1,
+  GPTQ_ACT_SILU = 2,
+  GPTQ_ACT_GELU = 3,
+  GPTQ_ACT_GELU_TANH = 4
+} gptq_activation;
+int gptq_w4a16_linear(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
+                      const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
+                      int64_t d_in, int group_size, int sym, const void* bias, int bias_dtype,
+                      int activation, int gated, const void* residual, int res_dtype, int64_t ldr,
+                      void* Y, int y_dtype, int64_t ldy, void* ws, size_t ws_bytes,
+                      gptq_stream stream);
+size_t gptq_w4a16_linear_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size,
+                                   int gated);
+
+/* ---------------------------------------------------------------------------
+ * Norms of queries and keys for each head, their rotation by position, and the
+ * writes of keys and values to their rows (of a cache): what stands between the
+ * query/key/value product and attention.
+ *
+ *   y = x weight / sqrt(mean(x^2) + eps) over a head's hd columns (a NULL weight:
+ *       y = x), for queries and keys
+ *   then for each pair (a, b) of the first rot_dim columns, pair i turned by
+ *       angle = positions[t] inv_freq[i]:
+ *       out_a = y_a cos - y_b sin, out_b = y_b cos + y_a sin;
+ *       (a, b) = (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved = 1
+ *   everything in float32 (the angle in float64), rounded once to bf16.  Values
+ *       are only rounded.
+ *
+ * Q, K, V     x_dtype (bf16 or float32): value d of head h of token t at
+ *             t ld + h hs + d, for all arrays here: ld* between tokens and hs*
+ *             between heads, in elements, both multiples of 16 bytes, ld < 2^23.
+ *             hq heads of Q, hk of K and V.  V (with V_out) may be NULL.
+ * hd          a multiple of 8, <= 256; rot_dim a multiple of 16, 0 .. hd
+ *             (0: positions and inv_freq may be NULL).
+ * positions   [m] int32, any value.
+ * inv_freq    [rot_dim / 2] float64, radians per position.
+ * q_weight, k_weight  [hd] of w_dtype (bf16 or float32), or NULL.
+ * slots       [m] int64: token t's keys and values go to row slots[t] of K_out
+ *             and V_out; a slot outside 0 .. kv_rows-1 writes nothing (padding).
+ *             Two tokens of one call with the same slot leave either's values,
+ *             not always one token's whole row.  NULL: row t.
+ * kv_rows     rows of K_out and V_out.  Rows that no slot names are left as they
+ *             were.
+ * Q_out, K_out, V_out  bf16 out; no two of an output's values may share a place.
+ *             Q_out may be Q, and without slots K_out may be K and V_out V (bf16,
+ *             the same strides); no other overlap is allowed.
+ * All arrays 16-byte aligned (positions, inv_freq, slots and weights as their
+ * elements).
+ * ------------------------------------------------------------------------- */
+int gptq_qk_norm_rope(const void* Q, int64_t ldq, int64_t hsq, const void* K, int64_t ldk,
+                      int64_t hsk, const void* V, int64_t ldv, int64_t hsv, int x_dtype, int64_t m,
+                      int hq, int hk, int hd, const int32_t* positions, const double* inv_freq,
+                      int rot_dim, int interleaved, const void* q_weight, const void* k_weight,
+                      int w_dtype, double eps, const int64_t* slots, int64_t kv_rows, void* Q_out,
+                      int64_t ldqo, int64_t hsqo, void* K_out, int64_t ldko, int64_t hsko,
+                      void* V_out, int64_t ldvo, int64_t hsvo, gptq_stream stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over packed sequences: whole prompts, pieces of prompts behind what a
+ * cache holds, or the next tokens of sequences, in one call.
+ *
+ *   out[i] = sum_j p_ij V[j] / sum_j p_ij,  p_ij = exp(scale Q[i] . K[j] - max)
+ *
+ * over the keys j that query i of its sequence sees: all lk of them, or, causal,
+ * j <= i + lk - lq (the last query sees all).  Query head h uses key head
+ * h / (hq / hk).  A query that sees no key gives zeros.
+ *
+ * Q, out      [total_q] queries x hq heads; K, V [kv_rows] x hk heads; bf16, laid
+ *             out by ld* and hs* as above.  hq a multiple of hk.  out may not
+ *             overlap an input.
+ * cu_q        [batch + 1] int32: sequence s has the queries cu_q[s] ..
+ *             cu_q[s + 1] - 1 (not decreasing).  Rows of out outside all sequences
+ *             are left as they were.
+ * kv_start, kv_len  [batch] int64 and int32: sequence s's keys are the rows
+ *             kv_start[s] .. kv_start[s] + kv_len[s] - 1 of K and V.  Both NULL:
+ *             its queries' own rows.  Offsets and lengths past the arrays are cut
+ *             off at their ends: nothing outside is read or written.
+ * max_kv_len  the longest kv_len as the caller knows it: it decides how keys are
+ *             split over workgroups, and with it only speed and the order of sums;
+ *             longer sequences are computed all the same.
+ * hd          a multiple of 8, <= 256.  scale > 0.
+ * ws          gptq_attention_workspace(...) bytes (0 where keys are not split);
+ *             its contents on entry do not matter; calls in flight together need
+ *             one each.
+ * Scores, maxima and sums are float32; the weights p are rounded to bf16, relative
+ * to a maximum that the row's own exceeds by less than a factor of 2^8, and their
+ * sum is that of the rounded values.  The order of every sum is fixed.  Keys and
+ * values that a query does not see do not reach it, whatever they hold.
+ * total_q * hq / 32 + batch * hk is bounded by 2^25 (GPTQ_EUNSUPPORTED past it).
+ * ------------------------------------------------------------------------- */
+int gptq_attention(const void* Q, int64_t ldq, int64_t hsq, const void* K, int64_t ldk, int64_t hsk,
+                   const void* V, int64_t ldv, int64_t hsv, int64_t total_q, int64_t kv_rows,
+                   int64_t batch, int hq, int hk, int hd, const int32_t* cu_q,
+                   const int64_t* kv_start, const int32_t* kv_len, int64_t max_kv_len, int causal,
+                   double scale, void* out, int64_t ldo, int64_t hso, void* ws, size_t ws_bytes,
+                   gptq_stream stream);
+size_t gptq_attention_workspace(int64_t total_q, int64_t batch, int hq, int hk, int hd,
+                                int64_t max_kv_len);
+
+/* ---------------------------------------------------------------------------
  * Two-sided adaptive rounding.  "GPTQ-2D: 三次时间复杂度的双侧自适应舍入",
  * 方法 steps 1-3 (anti-diagonal order, entries of one anti-diagonal in
  * parallel, errors carried through the two bases' triangular factors) and

@@ -23,6 +23,7 @@ from .gptq2d_oracle import two_sided_quartic, two_sided_antidiagonal
 from .act_order import activation_order, gptq_ordered
 from .dequant_gemm import dequantize, dequant_matmul
 from .norm_quant import residual_sum, rms_norm, norm_codes, round_bf16
+from .decoder_block import activate, epilogue, norm_rope, attention_weights, attention
 
 __all__ = [
     "NotSPD", "hessian", "hessian_entry", "prepare", "reversed_route_U", "group_params",
@@ -31,4 +32,5 @@ __all__ = [
     "unpack_rows", "words_per_row", "fp16_bits", "two_sided_quartic",
     "two_sided_antidiagonal", "activation_order", "gptq_ordered", "dequantize",
     "dequant_matmul", "residual_sum", "rms_norm", "norm_codes", "round_bf16",
+    "activate", "epilogue", "norm_rope", "attention_weights", "attention",
 ]

@@ -16,7 +16,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["syrk.hip", "prepare.hip", "quant.hip", "gptq2d.hip", "act_order.hip",
            "w4a16.hip", "w4a16_vec.hip", "w4a8.hip", "add_rmsnorm.hip", "gptq_abi.cpp",
-           "serve_abi.cpp"]
+           "serve_abi.cpp", "w4a16_linear.hip", "w4a16_linear_vec.hip",
+           "qk_norm_rope.hip", "attention.hip", "block_abi.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -31,7 +32,8 @@ FLAGS = [
 # plain VALU arithmetic; MFMA results kept in ordinary VGPRs spare the moves
 # to and from the accumulation registers around every rescale.
 FILE_FLAGS = {"w4a16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-              "w4a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+              "w4a8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+              "w4a16_linear.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -51,7 +53,7 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def build(verbose: bool = False, jobs: int = 4) -> str:
+def build(verbose: bool = False, jobs: int = 8) -> str:
     """Compile every source and link the shared library; returns its path."""
     if not shutil.which(HIPCC) and not os.path.exists(HIPCC):
         raise RuntimeError(f"hipcc not found at {HIPCC}")

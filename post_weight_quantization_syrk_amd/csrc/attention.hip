@@ -1,0 +1,576 @@
+// Attention over packed queries and runs of keys, grouped heads:
+//   out[i] = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i k_j - m_i),
+// over the keys that query i sees; a query that sees none gives zeros.
+//
+// The query heads of a key head are rows of one tile (row = query x group +
+// head), so keys and values are read once for all of them, and a single token is
+// the same work with fewer rows.  Scores are formed transposed, S^T = K Q^T
+// (v_mfma_f32_32x32x16_bf16): a lane then holds scores of one query only, its
+// maximum and sum are in-lane but for one exchange of the two lane halves, and
+// exp(S^T), rounded to bf16, is already laid out as the right operand of
+// O^T = V^T P^T.  (A lane's scores are of keys 4 h .. 4 h + 3 of every eight, and
+// the contraction takes keys in any order: V^T's fragments are read in that order
+// by the LDS transpose read.)  Scores, maxima, sums and O stay in float32; P is
+// rounded to bf16 for the matrix cores and its sum is taken over the rounded
+// values, so that a row's weights add up to one.
+#include "common.h"
+#include "kernels.h"
+
+#include <algorithm>
+
+namespace gptq {
+
+namespace {
+
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+
+constexpr float NO_MAX = -3.0e38f;  // of a row that has seen no key yet
+// O is scaled again only when a row's maximum has grown by more than 2^GROWTH
+// since the last time: p is then at most 2^GROWTH, with the same relative
+// rounding, and sums stay far inside float32.
+constexpr float GROWTH = 8.0f;
+
+// Unit (16 bytes) u of row r of a tile in LDS stands at u ^ swizzle(r): eight rows
+// read at one unit, and four rows read at two, fall on different banks.
+template <int DB>
+__device__ __forceinline__ int swizzle(int r) {
+  if constexpr (DB % 2 == 0)
+    return ((r & 3) << 1) | ((r >> 2) & 1);
+  else  // rows of 64 bytes more or less than a multiple of 128
+    return (r & 2) | ((r >> 2) & 1);
+}
+
+// Direct global -> LDS load of 16 bytes per lane at a uniform base and a lane's
+// offset: lane l's bytes land at lds_off + 16 l.  In asm, since the compiler
+// would wait for every load in flight before any LDS read; the loops wait for
+// them themselves.  (M0 may be used for LDS one wait state after it is written.)
+__device__ __forceinline__ void dma16(const void* base, uint32_t voff, uint32_t lds_off) {
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  const uint32_t blo = __builtin_amdgcn_readfirstlane((uint32_t)b);
+  const uint32_t bhi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  const void* sbase = (const void*)(uintptr_t)(((uint64_t)bhi << 32) | blo);
+  const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds_off);
+  __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                   :
+                   : "v"(voff), "s"(sbase), "s"(lbase)
+                   : "memory", "m0");
+}
+
+__device__ __forceinline__ float other_half(float v) {  // of the lane 32 away
+  const u32x2 r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return (threadIdx.x & 32) ? __uint_as_float(r[0]) : __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The sequence that a tile of rows belongs to, and its place.  Sequence s has
+// its tiles from slot floor(cu[s] group / rows) + s on, which leaves room for
+// them all: no prefix sum over the sequences is needed, only a search.
+struct Place {
+  int64_t q0;     // first query of the sequence
+  int64_t start;  // first row of its keys
+  int lq, lk;     // queries and keys
+  int64_t row0;   // first row of the tile within the sequence
+};
+
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)v >> 32)) << 32 |
+                   __builtin_amdgcn_readfirstlane((uint32_t)v));
+}
+
+// Offsets and lengths that do not fit the arrays are brought inside them.
+__device__ __forceinline__ Place find(const AttnArgs& a, int group, int tile_rows, int64_t slot) {
+  const int lane = threadIdx.x & 63;
+  auto cu = [&](int s) __attribute__((always_inline)) {
+    return min(max((int64_t)a.cu_q[s], (int64_t)0), a.tq);
+  };
+  int lo = 0, n = a.batch;
+  while (n > 1) {
+    const int step = (n + 63) / 64, at = lane * step;
+    const bool le = at < n && cu(lo + min(at, n - 1)) * group / tile_rows + lo + at <= slot;
+    const int i = max(__builtin_popcountll(__ballot(le)) - 1, 0);
+    lo += i * step;
+    n = min(step, n - i * step);
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  Place p;
+  p.q0 = uniform(cu(lo));
+  p.lq = (int)max(uniform(cu(lo + 1)) - p.q0, (int64_t)0);
+  p.row0 = (slot - (p.q0 * group / tile_rows + lo)) * tile_rows;
+  if (a.kv_start) {
+    p.start = min(max(uniform(a.kv_start[lo]), (int64_t)0), a.kv_rows);
+    p.lk = (int)min((int64_t)max(__builtin_amdgcn_readfirstlane(a.kv_len[lo]), 0), a.kv_rows - p.start);
+  } else {
+    p.start = min(p.q0, a.kv_rows);
+    p.lk = (int)min((int64_t)p.lq, a.kv_rows - p.start);
+  }
+  return p;
+}
+
+// What a wave keeps of 32 rows: lane l and lane l + 32 hold row l.
+template <int DB>
+struct Rows {
+  bf16x8 q[2 * DB];  // columns 16 i + 8 h ..
+  f32x16 o[DB];      // O^T: columns 32 b + 8 (i / 4) + 4 h + i % 4
+  float mc, l;       // maximum times c (log2 units); this half's sum
+};
+
+template <int DB>
+__device__ __forceinline__ void start_rows(Rows<DB>& w, const uint16_t* qrow, int hd, int h) {
+#pragma unroll
+  for (int i = 0; i < 2 * DB; ++i) {
+    const int d = 16 * i + 8 * h;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (d < hd) v = *(const uint4*)(qrow + d);
+    __builtin_memcpy(&w.q[i], &v, 16);
+  }
+#pragma unroll
+  for (int b = 0; b < DB; ++b) w.o[b] = f32x16{};
+  w.mc = NO_MAX, w.l = 0.0f;
+}
+
+// One tile of 32 KB keys, in LDS at lk and lv.  rel: the last key that the lane's
+// row sees, less the tile's first; masked: some row does not see all of them.
+template <int DB, int KB>
+__device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const char* lv, float c,
+                                          int rel, bool masked) {
+  constexpr int RB = 64 * DB;
+  const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
+  f32x16 s[KB];
+  const int ksw = swizzle<DB>(l32);
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb) {
+    s[kb] = f32x16{};
+#pragma unroll
+    for (int i = 0; i < 2 * DB; ++i) {
+      const bf16x8 k = *(const bf16x8*)(lk + (32 * kb + l32) * RB + 16 * ((2 * i + h) ^ ksw));
+      s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, w.q[i], s[kb], 0, 0, 0);
+    }
+  }
+  if (masked) {
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (32 * kb + 8 * (i >> 2) + 4 * h + (i & 3) > rel) s[kb][i] = -INFINITY;
+  }
+  float mx = s[0][0];
+#pragma unroll
+  for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
+  mx = fmaxf(mx, other_half(mx)) * c;
+  if (__any(mx > w.mc + GROWTH)) {
+    const float mc = fmaxf(w.mc, mx), f = exp2_of(w.mc - mc);
+    w.mc = mc, w.l *= f;
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w.o[b][i] *= f;
+  }
+  const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
+  const int i16 = lane & 15, trow = 4 * h + (i16 >> 2), tu = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+#pragma unroll
+  for (int kc = 0; kc < 2 * KB; ++kc) {  // 16 keys
+    bf16x8 p;
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const bf16x2 two = {(__bf16)exp2_of(fmaf(s[kc >> 1][8 * (kc & 1) + j], c, -w.mc)),
+                          (__bf16)exp2_of(fmaf(s[kc >> 1][8 * (kc & 1) + j + 1], c, -w.mc))};
+      w.l = __builtin_amdgcn_fdot2_f32_bf16(two, ones, w.l, false);
+      p[j] = two[0], p[j + 1] = two[1];
+    }
+#pragma unroll
+    for (int b = 0; b < DB; ++b) {
+      bf16x8 v;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = 16 * kc + 8 * e + trow;
+        const s16x4 t = lds_read_tr16(lv + row * RB + 16 * ((4 * b + tu) ^ swizzle<DB>(row)) + 8 * (i16 & 1));
+        __builtin_memcpy((char*)&v + 8 * e, &t, 8);
+      }
+      w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, w.o[b], 0, 0, 0);
+    }
+  }
+}
+
+// A row by the definition, key by key: for rows whose sums met an infinity or a
+// NaN, which may be a key's that the row does not see (a tile multiplies such a
+// key's value by a weight of 0).  A whole wave takes the row; lane l has columns
+// 4 l .. 4 l + 3.
+struct Slow {
+  float o[4], mc, l;
+};
+__device__ __forceinline__ Slow slow_row(const uint16_t* q, const uint16_t* k, int64_t ldk,
+                                         const uint16_t* v, int64_t ldv, int hd, int begin, int end,
+                                         float c) {
+  const int lane = threadIdx.x & 63, d = 4 * lane;
+  const bool in = d < hd;
+  Slow r = {{0.0f, 0.0f, 0.0f, 0.0f}, NO_MAX, 0.0f};
+  float qv[4] = {};
+  if (in) {
+    for (int i = 0; i < 4; ++i) qv[i] = bf16_bits_to_float(q[d + i]);
+  }
+  for (int j = begin; j < end; ++j) {
+    float s = 0.0f, x[4] = {};
+    if (in) {
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(qv[i], bf16_bits_to_float(k[(int64_t)j * ldk + d + i]), s);
+        x[i] = bf16_bits_to_float(v[(int64_t)j * ldv + d + i]);
+      }
+    }
+    for (int o = 1; o < 64; o *= 2) s += __shfl_xor(s, o);
+    s *= c;
+    if (s > r.mc) {
+      const float f = exp2_of(r.mc - s);
+      r.mc = s, r.l *= f;
+      for (int i = 0; i < 4; ++i) r.o[i] *= f;
+    }
+    const float p = exp2_of(s - r.mc);
+    r.l += p;
+    for (int i = 0; i < 4; ++i) r.o[i] = fmaf(p, x[i], r.o[i]);
+  }
+  return r;
+}
+
+struct Grid {
+  int64_t slots;   // tiles of rows, over all sequences
+  int splits;      // of a tile's keys over workgroups
+  float* part;     // splits > 1: [splits][tq][hq][hd + 2]: O, maximum, sum
+};
+
+// Writes row (query, head): finished, or as a part.  e: columns 4 at a time.
+__device__ __forceinline__ void store4(const AttnArgs& a, const Grid& g, int split, int64_t query,
+                                       int head, int d, const float o[4], float mc, float l,
+                                       float inv) {
+  if (d >= a.hd) return;
+  if (g.splits == 1) {
+    *(bf16x4*)(a.out + query * a.ldo + head * a.hso + d) =
+        bf16x4{(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
+  } else {
+    float* p = g.part + ((split * a.tq + query) * a.hq + head) * (a.hd + 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[d + i] = o[i];
+    if (d == 0) p[a.hd] = mc, p[a.hd + 1] = l;
+  }
+}
+
+// A tile's keys as this workgroup has them: [begin, end), whole tiles of `step`.
+__device__ __forceinline__ void key_range(int kend, int step, int splits, int split, int& begin,
+                                          int& end) {
+  const int tiles = (kend + step - 1) / step, per = (tiles + splits - 1) / splits;
+  begin = min(split * per * step, kend), end = min((split + 1) * per * step, kend);
+}
+
+__device__ __forceinline__ bool finite4(const f32x16& v) {
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) t = fmaf(v[i], 0.0f, t);
+  return t == 0.0f;
+}
+
+// The wave's 32 rows leave: l is the whole row's sum, o its columns.
+template <int DB>
+__device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Place& p, int group,
+                                      int kvh, int64_t row0, int64_t rows, int split, int begin,
+                                      int end, float c, const f32x16 (&o)[DB], float mc, float l) {
+  const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
+  const int64_t row = row0 + l32;
+  const int64_t query = row / group;
+  const int head = kvh * group + (int)(row - query * group);
+  const bool live = row < rows;
+  const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays)
+  bool ok = l - l == 0.0f;
+#pragma unroll
+  for (int b = 0; b < DB; ++b) {
+    ok = ok && finite4(o[b]);
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float t[4] = {o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
+        store4(a, g, split, p.q0 + query, head, 32 * b + 2 * i + 4 * h, t, mc, l, inv);
+      }
+    }
+  }
+  if (!a.causal) return;
+  const int lim = (int)min(query + p.lk - p.lq, (int64_t)p.lk - 1);  // the last key seen
+  uint64_t bad = __ballot(live && !ok && lim < p.lk - 1);
+  uint32_t rest = (uint32_t)bad | (uint32_t)(bad >> 32);
+  while (rest) {
+    const int r = __builtin_ctz(rest);
+    rest &= rest - 1;
+    const int64_t qi = (row0 + r) / group;
+    const int hr = kvh * group + (int)(row0 + r - qi * group);
+    const int last = (int)(qi + p.lk - p.lq) + 1;
+    const Slow s = slow_row(a.q + (p.q0 + qi) * a.ldq + hr * a.hsq,
+                            a.k + p.start * a.ldk + kvh * a.hsk, a.ldk,
+                            a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd, begin, min(end, last), c);
+    store4(a, g, split, p.q0 + qi, hr, 4 * lane, s.o, s.mc, s.l, s.l > 0.0f ? 1.0f / s.l : s.l);
+  }
+}
+
+// Many rows: four waves of 32 rows, which share tiles of 64 keys in LDS.
+constexpr int BM = 128, BK = 64;
+
+template <int DB>
+__global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Grid g) {
+  constexpr int RB = 64 * DB, TILE = BK * RB;  // bytes of a row and of a tile
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  // key heads go to the XCDs in turn; of one sequence the later rows, which see
+  // more keys, first
+  const int kvh = (int)(blockIdx.x % a.hk);
+  const int64_t rest = blockIdx.x / a.hk;
+  const int split = (int)(rest / g.slots);
+  const int64_t slot = g.slots - 1 - rest % g.slots;
+  const int group = a.hq / a.hk;
+  const Place p = find(a, group, BM, slot);
+  const int64_t rows = (int64_t)p.lq * group;
+  if (p.row0 < 0 || p.row0 >= rows) return;
+  const float c = a.scale * 1.4426950408889634f;
+
+  // rows past the last are copies of it
+  const int64_t row0 = p.row0 + 32 * wave, row = min(row0 + l32, rows - 1);
+  const int query = (int)(row / group);
+  const int head = kvh * group + (int)(row - (int64_t)query * group);
+  Rows<DB> w;
+  start_rows<DB>(w, a.q + (p.q0 + query) * a.ldq + head * a.hsq, a.hd, h);
+  const int back = p.lk - p.lq;
+  auto last_key = [&](int64_t r) __attribute__((always_inline)) {  // that row r sees
+    return a.causal ? (int)min(min(r, rows - 1) / group + back, (int64_t)p.lk - 1) : p.lk - 1;
+  };
+  const int lim = last_key(row), lim_first = last_key(row0), lim_last = last_key(row0 + 31);
+  int begin, end;
+  key_range(last_key(p.row0 + BM - 1) + 1, BK, g.splits, split, begin, end);
+
+  // direct loads: this wave's DB KB of each tile, units past hd replaced
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  int trow[DB], tcol[DB];
+#pragma unroll
+  for (int j = 0; j < DB; ++j) {
+    const int i = (DB * wave + j) * 64 + lane;
+    trow[j] = i / (4 * DB);
+    tcol[j] = 16 * min((i % (4 * DB)) ^ swizzle<DB>(trow[j]), a.hd / 8 - 1);
+  }
+  const char* const kb = (const char*)(a.k + p.start * a.ldk + kvh * a.hsk);
+  const char* const vb = (const char*)(a.v + p.start * a.ldv + kvh * a.hsv);
+  auto issue = [&](int key0, int buf) __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + buf * 2 * TILE + DB * wave * 1024;
+    const int most = p.lk - 1 - key0;  // rows past the last key are copies of it
+    const char* const ks = kb + 2 * (int64_t)key0 * a.ldk;
+    const char* const vs = vb + 2 * (int64_t)key0 * a.ldv;
+#pragma unroll
+    for (int j = 0; j < DB; ++j)
+      dma16(ks, (uint32_t)min(trow[j], most) * (uint32_t)(2 * a.ldk) + tcol[j], dst + 1024 * j);
+#pragma unroll
+    for (int j = 0; j < DB; ++j)
+      dma16(vs, (uint32_t)min(trow[j], most) * (uint32_t)(2 * a.ldv) + tcol[j], dst + TILE + 1024 * j);
+  };
+  if (begin < end) issue(begin, 0);
+  for (int key0 = begin, buf = 0; key0 < end; key0 += BK, buf ^= 1) {
+    // this tile has landed, and the other buffer is read
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (key0 + BK < end) issue(key0 + BK, buf ^ 1);
+    if (key0 > lim_last) continue;
+    const char* const t = lds + buf * 2 * TILE;
+    tile_step<DB, BK / 32>(w, t, t + TILE, c, lim - key0, lim_first < key0 + BK - 1);
+  }
+  const float l = w.l + other_half(w.l);
+  leave<DB>(a, g, p, group, kvh, row0, rows, split, begin, end, c, w.o, w.mc, l);
+}
+
+// Few rows: one tile of 32 rows, the keys in tiles of 32 that four waves (two,
+// where LDS holds no more) take in turn, each with two buffers of its own, so that
+// none waits for another; their sums meet at the end.
+constexpr int FM = 32, FK = 32;
+constexpr int few_waves(int DB) { return DB <= 4 ? 4 : 2; }
+
+template <int DB>
+__global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(AttnArgs a, Grid g) {
+  constexpr int RB = 64 * DB, TILE = FK * RB, PIECES = 2 * DB, FW = few_waves(DB);
+  extern __shared__ __attribute__((aligned(1024))) char lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l32 = lane & 31, h = lane >> 5;
+  const int kvh = (int)(blockIdx.x % a.hk);
+  const int64_t rest = blockIdx.x / a.hk;
+  const int split = (int)(rest % g.splits);
+  const int64_t slot = rest / g.splits;
+  const int group = a.hq / a.hk;
+  const Place p = find(a, group, FM, slot);
+  const int64_t rows = (int64_t)p.lq * group;
+  if (p.row0 < 0 || p.row0 >= rows) return;
+  const float c = a.scale * 1.4426950408889634f;
+  const int64_t row = min(p.row0 + l32, rows - 1);
+  const int query = (int)(row / group);
+  const int head = kvh * group + (int)(row - (int64_t)query * group);
+  Rows<DB> w;
+  start_rows<DB>(w, a.q + (p.q0 + query) * a.ldq + head * a.hsq, a.hd, h);
+  const int back = p.lk - p.lq;
+  auto last_key = [&](int64_t r) __attribute__((always_inline)) {
+    return a.causal ? (int)min(min(r, rows - 1) / group + back, (int64_t)p.lk - 1) : p.lk - 1;
+  };
+  const int lim = last_key(row), lim_first = last_key(p.row0);
+  int begin, end;
+  key_range(last_key(p.row0 + FM - 1) + 1, FK * FW, g.splits, split, begin, end);
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 4 * TILE;
+  const char* const mine = lds + wave * 4 * TILE;
+  int trow[PIECES], tcol[PIECES];
+#pragma unroll
+  for (int j = 0; j < PIECES; ++j) {
+    const int i = j * 64 + lane;
+    trow[j] = i / (4 * DB);
+    tcol[j] = 16 * min((i % (4 * DB)) ^ swizzle<DB>(trow[j]), a.hd / 8 - 1);
+  }
+  const char* const kb = (const char*)(a.k + p.start * a.ldk + kvh * a.hsk);
+  const char* const vb = (const char*)(a.v + p.start * a.ldv + kvh * a.hsv);
+  auto issue = [&](int key0, int buf) __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + buf * 2 * TILE;
+    const int most = p.lk - 1 - key0;
+    const char* const ks = kb + 2 * (int64_t)key0 * a.ldk;
+    const char* const vs = vb + 2 * (int64_t)key0 * a.ldv;
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j)
+      dma16(ks, (uint32_t)min(trow[j], most) * (uint32_t)(2 * a.ldk) + tcol[j], dst + 1024 * j);
+#pragma unroll
+    for (int j = 0; j < PIECES; ++j)
+      dma16(vs, (uint32_t)min(trow[j], most) * (uint32_t)(2 * a.ldv) + tcol[j], dst + TILE + 1024 * j);
+  };
+  const int first = begin + FK * wave;
+  if (first < end) issue(first, 0);
+  for (int key0 = first, buf = 0; key0 < end; key0 += FK * FW, buf ^= 1) {
+    // every read of the other buffer has returned before it is written again
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (key0 + FK * FW < end) {
+      issue(key0 + FK * FW, buf ^ 1);
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PIECES) : "memory");
+    } else {
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+    const char* const t = mine + buf * 2 * TILE;
+    tile_step<DB, FK / 32>(w, t, t + TILE, c, lim - key0, lim_first < key0 + FK - 1);
+  }
+  float l = w.l + other_half(w.l);
+  // the waves' sums, brought to one maximum, by way of LDS
+  __syncthreads();
+  float* const stat = (float*)lds;  // [FW][2][32]
+  if (h == 0) stat[wave * 64 + l32] = w.mc, stat[wave * 64 + 32 + l32] = l;
+  __syncthreads();
+  float mc = NO_MAX, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < FW; ++i) mc = fmaxf(mc, stat[i * 64 + l32]);
+#pragma unroll
+  for (int i = 0; i < FW; ++i) sum += stat[i * 64 + 32 + l32] * exp2_of(stat[i * 64 + l32] - mc);
+  const float f = exp2_of(w.mc - mc);
+  float* const parts = (float*)lds + FW * 64;
+  constexpr int PER = DB * 16 * 64;
+#pragma unroll
+  for (int from = 1; from < FW; ++from) {
+    if (wave == from) {
+#pragma unroll
+      for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) parts[(from - 1) * PER + (16 * b + i) * 64 + lane] = w.o[b][i] * f;
+    }
+  }
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int b = 0; b < DB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = w.o[b][i] * f;
+#pragma unroll
+      for (int from = 1; from < FW; ++from) v += parts[(from - 1) * PER + (16 * b + i) * 64 + lane];
+      w.o[b][i] = v;
+    }
+  leave<DB>(a, g, p, group, kvh, p.row0, rows, split, begin, end, c, w.o, mc, sum);
+}
+
+// The splits' parts of each row, in split order.
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, Grid g) {
+  const int per = a.hd / 4;  // threads per row
+  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = t / per;
+  if (row >= a.tq * a.hq) return;
+  const int64_t query = row / a.hq;
+  const int d = 4 * (int)(t - row * per), head = (int)(row - query * a.hq);
+  // rows before the first and behind the last sequence are not anyone's
+  const int64_t first = a.cu_q[0], last = a.cu_q[a.batch];
+  if (query < first || query >= last) return;
+  const float* p = g.part + row * (a.hd + 2);
+  const int64_t next = a.tq * a.hq * (a.hd + 2);
+  float mc = NO_MAX;
+  for (int s = 0; s < g.splits; ++s) mc = fmaxf(mc, p[s * next + a.hd]);
+  float l = 0.0f, o[4] = {};
+  for (int s = 0; s < g.splits; ++s) {
+    const float f = exp2_of(p[s * next + a.hd] - mc);
+    l = fmaf(p[s * next + a.hd + 1], f, l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = fmaf(p[s * next + d + i], f, o[i]);
+  }
+  const float inv = l > 0.0f ? 1.0f / l : l;
+  *(bf16x4*)(a.out + query * a.ldo + head * a.hso + d) =
+      bf16x4{(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
+}
+
+struct Plan {
+  bool few;  // rows: the kernel whose waves share the keys
+  Grid g;
+  size_t bytes;
+};
+
+Plan plan_for(int64_t tq, int64_t batch, int hq, int hk, int hd, int64_t max_kv_len) {
+  Plan p;
+  const int group = hq / hk;
+  p.few = tq * group <= batch * FM;
+  const int rows = p.few ? FM : BM;
+  p.g.slots = tq * group / rows + batch;
+  p.g.splits = 1;
+  p.g.part = nullptr;
+  const int64_t groups = p.g.slots * hk, tiles = ceil_div(max_kv_len, p.few ? 128 : BK);
+  if (groups < 256) p.g.splits = (int)std::max<int64_t>(1, std::min(std::min<int64_t>(ceil_div(256, groups), 32), tiles / 2));
+  p.bytes = p.g.splits > 1 ? (size_t)p.g.splits * tq * hq * (hd + 2) * 4 : 0;
+  return p;
+}
+
+template <int DB>
+hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.g.slots * a.hk * p.g.splits));
+  if (p.few) {
+    constexpr int FW = few_waves(DB);
+    const size_t bytes = std::max<size_t>((size_t)FW * 4 * FK * 64 * DB,
+                                          FW * 256 + (FW - 1) * DB * 16 * 64 * 4);
+    hipLaunchKernelGGL((attention_keys_kernel<DB>), grid, dim3(64 * FW), bytes, stream, a, p.g);
+  } else {
+    hipLaunchKernelGGL((attention_rows_kernel<DB>), grid, dim3(256), (size_t)4 * BK * 64 * DB, stream,
+                       a, p.g);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t attention_workspace(int64_t tq, int64_t batch, int hq, int hk, int hd, int64_t max_kv_len) {
+  return plan_for(tq, batch, hq, hk, hd, max_kv_len).bytes;
+}
+
+hipError_t attention_launch(const AttnArgs& a, int64_t max_kv_len, void* ws, hipStream_t stream) {
+  Plan p = plan_for(a.tq, a.batch, a.hq, a.hk, a.hd, max_kv_len);
+  p.g.part = (float*)ws;
+  hipError_t e = a.hd <= 64    ? launch<2>(a, p, stream)
+                 : a.hd <= 96  ? launch<3>(a, p, stream)
+                 : a.hd <= 128 ? launch<4>(a, p, stream)
+                 : a.hd <= 192 ? launch<6>(a, p, stream)
+                               : launch<8>(a, p, stream);
+  if (e != hipSuccess || p.g.splits == 1) return e;
+  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)ceil_div(a.tq * a.hq * (a.hd / 4), 256)),
+                     dim3(256), 0, stream, a, p.g);
+  return hipGetLastError();
+}
+
+}  // namespace gptq

@@ -97,6 +97,68 @@ hipError_t w4a8_launch(const int8_t* X, const float* x_scales, int64_t m, int64_
                        const uint16_t* zeros_f16, int64_t d_out, int64_t d_in, int group_size,
                        float* Y, void* ws, hipStream_t stream);
 
+// ---- W4A16 product with bias, activation, gate and residual ----------------
+enum Activation { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3, ACT_GELU_TANH = 4 };
+
+struct Epilogue {
+  const void* bias;  // [d_out], null: none
+  const void* res;   // [m][ldr], null: none
+  void* y;           // [m][ldy]
+  int64_t ldr, ldy;
+  int F;             // columns of Y
+  int act;
+  bool bias_f32, res_f32, y_f32;
+  bool vec4;         // four neighbouring values of Y at a multiple of 4 are one aligned store
+};
+
+size_t linear_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size, bool gated);
+hipError_t linear_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
+                         const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
+                         int64_t d_in, int group_size, bool gated, const Epilogue& e, void* ws,
+                         hipStream_t stream);
+// for few tokens
+size_t linear_vec_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size, bool gated);
+hipError_t linear_vec_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* qweight,
+                             const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
+                             int64_t d_in, int group_size, bool gated, const Epilogue& e, void* ws,
+                             hipStream_t stream);
+
+// ---- norms of queries and keys, rotation, rows of a cache ------------------
+// Strides in elements: ld* between tokens (rows), hs* between heads.
+struct RopeArgs {
+  const void *q, *k, *v;  // v null: none
+  int64_t ldq, hsq, ldk, hsk, ldv, hsv;
+  int64_t m;
+  int hq, hk, hd, rot;
+  const int32_t* positions;
+  const double* inv_freq;
+  const void *q_weight, *k_weight;  // null: no norm
+  bool w_f32, interleaved;
+  float eps;
+  const int64_t* slots;  // null: row t
+  int64_t kv_rows;       // rows of k_out and v_out
+  uint16_t *q_out, *k_out, *v_out;
+  int64_t ldqo, hsqo, ldko, hsko, ldvo, hsvo;
+};
+hipError_t qk_norm_rope_launch(const RopeArgs& a, bool f32, hipStream_t stream);
+
+// ---- attention over packed queries and runs of keys ------------------------
+struct AttnArgs {
+  const uint16_t *q, *k, *v;
+  int64_t ldq, hsq, ldk, hsk, ldv, hsv;  // elements, as above
+  int64_t tq, kv_rows;
+  int batch, hq, hk, hd;
+  const int32_t* cu_q;
+  const int64_t* kv_start;  // null, with kv_len: the keys are packed as the queries
+  const int32_t* kv_len;
+  int causal;
+  float scale;
+  uint16_t* out;
+  int64_t ldo, hso;
+};
+size_t attention_workspace(int64_t tq, int64_t batch, int hq, int hk, int hd, int64_t max_kv_len);
+hipError_t attention_launch(const AttnArgs& a, int64_t max_kv_len, void* ws, hipStream_t stream);
+
 // Polls a bounded wait between workgroups may take before it gives up
 // (environment GPTQ_SYNC_SPIN_LIMIT, default 2^20), read once per process.
 int64_t sync_spin_limit();

@@ -60,12 +60,19 @@ __device__ __forceinline__ float wave_sum4(const float v[4]) {
 
 // ks: waves that share a row (runs per row); rpw: rows per wave, a
 // multiple of 4.
-template <bool I8>
-__global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, int rpw) {
+template <bool I8, class E>
+__global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, int rpw, E epi) {
   extern __shared__ float red[];  // [rows of the workgroup][ks]
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int seg = wave % ks, rg = wave / ks, rows = (int)(blockDim.x >> 6) / ks * rpw;
   const int64_t n0 = (int64_t)blockIdx.x * rows + rg * rpw;
+  // gated: even rows are gate rows, odd ones the up rows that go with them
+  auto valid_row = [&](int64_t n) __attribute__((always_inline)) {
+    if constexpr (E::gated)
+      return min(n >> 1, (int64_t)epi.e.F - 1) + (n & 1) * epi.e.F;
+    else
+      return min(n, (int64_t)a.n - 1);
+  };
   const int row_bytes = a.k / 2;
   const int k0 = seg * RUN + 32 * lane;
   const bool in = k0 < a.k;
@@ -79,7 +86,7 @@ __global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, 
   auto load = [&](int r, Rows& v) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int64_t n = min(n0 + r + u, (int64_t)a.n - 1);
+      const int64_t n = valid_row(n0 + r + u);
       v.w[u] = *(const uint4*)((const char*)a.q + n * row_bytes + kc / 2);
       v.s[u] = a.s16[n * a.ng + g];
       v.z[u] = a.z16 ? a.z16[n * a.ng + g] : (uint16_t)0x4800;  // 8
@@ -155,12 +162,28 @@ __global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, 
     cur = nxt;
   }
   __syncthreads();
-  for (int row = threadIdx.x; row < rows; row += blockDim.x) {
-    const int64_t n = (int64_t)blockIdx.x * rows + row;
+  auto summed = [&](int row) __attribute__((always_inline)) {
     float v = 0.0f;
     for (int s = 0; s < ks; ++s) v += red[row * ks + s];
+    return v;
+  };
+  if constexpr (E::gated) {
+    for (int p = threadIdx.x; p < rows / 2; p += blockDim.x) {
+      const int64_t u = (int64_t)blockIdx.x * (rows / 2) + p;
+      if (u < epi.e.F) finish<true>(epi.e, 0, u, summed(2 * p), summed(2 * p + 1));
+    }
+    return;
+  }
+  for (int row = threadIdx.x; row < rows; row += blockDim.x) {
+    const int64_t n = (int64_t)blockIdx.x * rows + row;
+    float v = summed(row);
     if constexpr (I8) v *= a.sx[0];
-    if (n < a.n) a.y[n] = v;
+    if (n < a.n) {
+      if constexpr (E::linear)
+        finish<false>(epi.e, 0, n, v, 0.0f);
+      else
+        a.y[n] = v;
+    }
   }
 }
 
@@ -169,14 +192,14 @@ __global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, 
 inline bool dot_takes(int64_t m, int64_t k) { return m == 1 && k <= 16 * RUN; }
 
 // Rows per wave: few enough that the launch has some 8192 waves' rows at once.
-template <bool I8>
-hipError_t dot_launch(const VecArgs& a, int G, hipStream_t stream) {
+template <bool I8, class E = Plain>
+hipError_t dot_launch(const VecArgs& a, int G, hipStream_t stream, const E& e = E{}) {
   const int ks = (int)ceil_div(a.k, RUN), rgs = ks >= 8 ? 1 : 8 / ks;
   int rpw = 4;
   while (rpw < 32 && (int64_t)a.n * ks / rpw > 8192) rpw *= 2;
   const int rows = rgs * rpw;
-  hipLaunchKernelGGL((w4_dot_kernel<I8>), dim3((unsigned)ceil_div(a.n, rows)), dim3(64 * ks * rgs),
-                     (size_t)rows * ks * sizeof(float), stream, a, G == 0 ? a.k : G, ks, rpw);
+  hipLaunchKernelGGL((w4_dot_kernel<I8, E>), dim3((unsigned)ceil_div(a.n, rows)), dim3(64 * ks * rgs),
+                     (size_t)rows * ks * sizeof(float), stream, a, G == 0 ? a.k : G, ks, rpw, e);
   return hipGetLastError();
 }
 

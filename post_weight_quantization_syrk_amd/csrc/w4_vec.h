@@ -35,6 +35,7 @@
 #pragma once
 
 #include "common.h"
+#include "linear_epi.h"
 
 #include <hip/hip_fp16.h>
 #include <algorithm>
@@ -59,6 +60,18 @@ struct VecArgs {
   int m, n, k, ng;
   int vec;              // scales (and zeros) that one aligned load may take: 1, 2, 4 or 8
   int splits, per_split;  // of the row's blocks of 512 k over workgroups
+};
+
+// How the sums leave: as they are (times sx), or finished by an epilogue.  Gated,
+// weight rows u and F + u belong together: a workgroup's row tiles are pairs of
+// tiles, first of gate rows, then of the up rows that go with them.
+struct Plain {
+  static constexpr bool linear = false, gated = false;
+};
+template <bool GATED>
+struct Finished {
+  static constexpr bool linear = true, gated = GATED;
+  Epilogue e;
 };
 
 // The most that divides a row of scales and its addresses.
@@ -169,8 +182,8 @@ struct Shape {
 
 // I8: int8 X; NT: tiles of 16 tokens; R: tiles of 16 weight rows; G: group
 // size, 0 for one group per row; RS: waves that share the tokens' buffers.
-template <bool I8, int NT, int R, int G, int RS>
-__global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4_vec_kernel(VecArgs a) {
+template <bool I8, int NT, int R, int G, int RS, class E>
+__global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4_vec_kernel(VecArgs a, E epi) {
   typedef typename Types<I8>::acc_t acc_t;
   typedef Shape<I8, NT, R, G, RS> S;
   constexpr bool TR = G == 32 || G == 64;
@@ -182,6 +195,20 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
   const int wave = w0 / RS, waves = (int)(blockDim.x >> 6) / RS, rs = w0 % RS;  // k slot; rows
   const int l16 = lane & 15, h = lane >> 4;
   const int n0 = (blockIdx.x * RS + rs) * 16 * R;
+  // the weight row of this wave's row lr, which may lie past the end; and the
+  // nearest that does not
+  auto row_at = [&](int lr) __attribute__((always_inline)) {
+    if constexpr (E::gated)
+      return n0 / 2 + 16 * (lr >> 5) + (lr & 15) + ((lr >> 4) & 1) * epi.e.F;
+    else
+      return n0 + lr;
+  };
+  auto valid_row_at = [&](int lr) __attribute__((always_inline)) {
+    if constexpr (E::gated)
+      return min(n0 / 2 + 16 * (lr >> 5) + (lr & 15), epi.e.F - 1) + ((lr >> 4) & 1) * epi.e.F;
+    else
+      return min(n0 + lr, a.n - 1);
+  };
   const int row_bytes = a.k / 2;
   char* const words = smem + wave * S::SLOT + rs * S::WORDS;
   char* const tokens = smem + wave * S::SLOT + RS * S::WORDS;
@@ -207,7 +234,7 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
   const char* qrow[R];
 #pragma unroll
   for (int r = 0; r < R; ++r)
-    qrow[r] = (const char*)a.q + (int64_t)min(n0 + 16 * r + (lane >> 2), a.n - 1) * row_bytes;
+    qrow[r] = (const char*)a.q + (int64_t)valid_row_at(16 * r + (lane >> 2)) * row_bytes;
   const int qu = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
   const char* xrow[XD];
   int xu[XD];
@@ -259,7 +286,7 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
       const int e = min(64 * i + lane, 16 * R * P - 1);
-      const int64_t o = (int64_t)min(n0 + e / P, a.n - 1) * a.ng + min(b * S::GPB + (e % P) * V, a.ng - V);
+      const int64_t o = (int64_t)valid_row_at(e / P) * a.ng + min(b * S::GPB + (e % P) * V, a.ng - V);
       s[i] = *(const Piece*)(a.s16 + o);
       if (a.z16) z[i] = *(const Piece*)(a.z16 + o);
     }
@@ -289,7 +316,7 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
   if constexpr (G == 0) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int64_t n = min(n0 + 16 * r + l16, a.n - 1);
+      const int64_t n = valid_row_at(16 * r + l16);
       row_sz[r] = a.s16[n] | zero_bits(a.z16 ? a.z16[n] : (uint16_t)0x4800) << 16;
     }
   }
@@ -490,13 +517,36 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
 #pragma unroll
       for (int e = 0; e < 4; ++e) out[((r * NT + t) * 4 + e) * 64 + lane] = tot[r][t][e];
   __syncthreads();
-  for (int e = wave; e < PER; e += waves) {
+  auto summed = [&](int e) __attribute__((always_inline)) {
     float v = 0.0f;
     for (int w = 0; w < waves; ++w) v += ((const float*)smem)[(rs * waves + w) * OUT + e * 64 + lane];
+    return v;
+  };
+  if constexpr (E::gated) {
+    if (a.splits == 1) {
+      for (int q = wave; q < PER / 2; q += waves) {
+        const int i = q & 3, t = (q >> 2) % NT, r = (q >> 2) / NT * 2;
+        const int token = 16 * t + 4 * h + i, u = row_at(16 * r + l16);
+        const float v0 = summed((r * NT + t) * 4 + i), v1 = summed(((r + 1) * NT + t) * 4 + i);
+        if (token < a.m && u < epi.e.F) finish<true>(epi.e, token, u, v0, v1);
+      }
+      return;
+    }
+  }
+  for (int e = wave; e < PER; e += waves) {
+    float v = summed(e);
     const int i = e & 3, t = (e >> 2) % NT, r = (e >> 2) / NT;
-    const int token = 16 * t + 4 * h + i, n = n0 + 16 * r + l16;
-    if (token < a.m && n < a.n) {
+    const int token = 16 * t + 4 * h + i, n = row_at(16 * r + l16);
+    bool in = token < a.m && n < a.n;
+    if constexpr (E::gated) in = in && n - (r & 1) * epi.e.F < epi.e.F;
+    if (in) {
       if (I8 && a.splits == 1) v *= a.sx[token];
+      if constexpr (E::linear && !E::gated) {
+        if (a.splits == 1) {
+          finish<false>(epi.e, token, n, v, 0.0f);
+          continue;
+        }
+      }
       a.y[((int64_t)blockIdx.y * a.m + token) * a.n + n] = v;
     }
   }
@@ -522,23 +572,23 @@ inline hipError_t join_launch(const float* part, const float* sx, int64_t m, int
   return hipGetLastError();
 }
 
-template <bool I8, int NT, int R, int G, int RS>
-hipError_t vec_launch_one(const VecArgs& a, hipStream_t stream) {
+template <bool I8, int NT, int R, int G, int RS, class E>
+hipError_t vec_launch_one(const VecArgs& a, const E& e, hipStream_t stream) {
   typedef Shape<I8, NT, R, G, RS> S;
   const int slots = std::min(S::SLOTS, a.per_split);  // no more than there are blocks
-  hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G, RS>),
+  hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G, RS, E>),
                      dim3((unsigned)ceil_div(a.n, 16 * R * RS), a.splits), dim3(64 * RS * slots),
-                     group_bytes(I8, NT, R, G, RS, slots), stream, a);
+                     group_bytes(I8, NT, R, G, RS, slots), stream, a, e);
   return hipGetLastError();
 }
 
-template <bool I8, int NT, int R, int RS>
-hipError_t vec_launch_g(const VecArgs& a, int G, hipStream_t stream) {
+template <bool I8, int NT, int R, int RS, class E>
+hipError_t vec_launch_g(const VecArgs& a, int G, const E& e, hipStream_t stream) {
   switch (G) {
-    case 32: return vec_launch_one<I8, NT, R, 32, RS>(a, stream);
-    case 64: return vec_launch_one<I8, NT, R, 64, RS>(a, stream);
-    case 128: return vec_launch_one<I8, NT, R, 128, RS>(a, stream);
-    default: return vec_launch_one<I8, NT, R, 0, RS>(a, stream);
+    case 32: return vec_launch_one<I8, NT, R, 32, RS>(a, e, stream);
+    case 64: return vec_launch_one<I8, NT, R, 64, RS>(a, e, stream);
+    case 128: return vec_launch_one<I8, NT, R, 128, RS>(a, e, stream);
+    default: return vec_launch_one<I8, NT, R, 0, RS>(a, e, stream);
   }
 }
 
@@ -567,14 +617,16 @@ struct VecPlan {
 // 1024 x 8192 12.1 us in four splits and 24.5 in one; through 11008 x 4096 23 us
 // and 25 with sharing waves, through 8192 x 8192 32 and 29.5, through 16384 x
 // 12288 98 and 67.
-inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
-  VecPlan p = {1, 1, 1, 1, 0};
+// (A gated product's row tiles come in pairs: r is even.)
+inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G, bool gated = false) {
+  VecPlan p = {gated ? 2 : 1, 1, 1, 1, 0};
   const int nt = (int)ceil_div(m, 16), nblk = (int)ceil_div(k, KBLK);
   double least = 0.0;
   for (int rs = 1; rs <= SHARE; rs += SHARE - 1)
     for (int r = rs == 1 ? 1 : 2; r <= 4; ++r)
       for (int s = 1; s <= 8 && s <= nblk; ++s) {
         if (rs > 1 && !may_share(i8, nt)) continue;
+        if (gated && r % 2 != 0) continue;
         const int per = (int)ceil_div(nblk, s), waves = std::min(per, most_slots(i8, nt, r, G, rs));
         const int64_t groups = ceil_div(n, 16 * r * rs) * s;
         const bool several = 2 * group_bytes(i8, nt, r, G, rs, waves) <= LDS_BYTES;  // per CU
@@ -595,33 +647,53 @@ inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G) {
   return p;
 }
 
-template <bool I8, int NT>
-hipError_t vec_launch_t(const VecArgs& a, int r, int rs, int G, hipStream_t stream) {
+template <bool I8, int NT, class E>
+hipError_t vec_launch_t(const VecArgs& a, int r, int rs, int G, const E& e, hipStream_t stream) {
   if constexpr (may_share(I8, NT)) {
     if (rs > 1) {
-      if (r == 4) return vec_launch_g<I8, NT, 4, SHARE>(a, G, stream);
-      if (r == 3) return vec_launch_g<I8, NT, 3, SHARE>(a, G, stream);
-      return vec_launch_g<I8, NT, 2, SHARE>(a, G, stream);
+      if (r == 4) return vec_launch_g<I8, NT, 4, SHARE>(a, G, e, stream);
+      if constexpr (!E::gated) {
+        if (r == 3) return vec_launch_g<I8, NT, 3, SHARE>(a, G, e, stream);
+      }
+      return vec_launch_g<I8, NT, 2, SHARE>(a, G, e, stream);
     }
   }
-  if (r == 4) return vec_launch_g<I8, NT, 4, 1>(a, G, stream);
-  if (r == 3) return vec_launch_g<I8, NT, 3, 1>(a, G, stream);
-  if (r == 2) return vec_launch_g<I8, NT, 2, 1>(a, G, stream);
-  return vec_launch_g<I8, NT, 1, 1>(a, G, stream);
+  if (r == 4) return vec_launch_g<I8, NT, 4, 1>(a, G, e, stream);
+  if constexpr (!E::gated) {
+    if (r == 3) return vec_launch_g<I8, NT, 3, 1>(a, G, e, stream);
+    if (r == 1) return vec_launch_g<I8, NT, 1, 1>(a, G, e, stream);
+  }
+  return vec_launch_g<I8, NT, 2, 1>(a, G, e, stream);
+}
+
+// The product; with splits their sums are left in ws, for the caller to join.
+template <bool I8, class E>
+hipError_t vec_launch_parts(VecArgs a, const VecPlan& p, int G, void* ws, const E& e,
+                            hipStream_t stream) {
+  if (p.splits > 1) a.y = (float*)ws;
+  a.splits = p.splits, a.per_split = p.per_split;
+  return a.m <= 16   ? vec_launch_t<I8, 1>(a, p.r, p.rs, G, e, stream)
+         : a.m <= 32 ? vec_launch_t<I8, 2>(a, p.r, p.rs, G, e, stream)
+         : a.m <= 48 ? vec_launch_t<I8, 3>(a, p.r, p.rs, G, e, stream)
+                     : vec_launch_t<I8, 4>(a, p.r, p.rs, G, e, stream);
 }
 
 template <bool I8>
-hipError_t vec_launch(VecArgs a, int G, void* ws, hipStream_t stream) {
+hipError_t vec_launch(const VecArgs& a, int G, void* ws, hipStream_t stream) {
   const VecPlan p = vec_plan(I8, a.m, a.n, a.k, G);
-  float* const y = a.y;
-  if (p.splits > 1) a.y = (float*)ws;
-  a.splits = p.splits, a.per_split = p.per_split;
-  hipError_t e = a.m <= 16   ? vec_launch_t<I8, 1>(a, p.r, p.rs, G, stream)
-                 : a.m <= 32 ? vec_launch_t<I8, 2>(a, p.r, p.rs, G, stream)
-                 : a.m <= 48 ? vec_launch_t<I8, 3>(a, p.r, p.rs, G, stream)
-                             : vec_launch_t<I8, 4>(a, p.r, p.rs, G, stream);
+  const hipError_t e = vec_launch_parts<I8>(a, p, G, ws, Plain{}, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  return join_launch(a.y, I8 ? a.sx : nullptr, a.m, a.n, p.splits, y, stream);
+  return join_launch((const float*)ws, I8 ? a.sx : nullptr, a.m, a.n, p.splits, a.y, stream);
+}
+
+// The same with an epilogue.
+template <bool I8, bool GATED>
+hipError_t vec_finish_launch(const VecArgs& a, int G, void* ws, const Epilogue& epi,
+                             hipStream_t stream) {
+  const VecPlan p = vec_plan(I8, a.m, a.n, a.k, G, GATED);
+  const hipError_t e = vec_launch_parts<I8>(a, p, G, ws, Finished<GATED>{epi}, stream);
+  if (e != hipSuccess || p.splits == 1) return e;
+  return join_finish_launch<GATED>((const float*)ws, a.m, a.n, p.splits, epi, stream);
 }
 
 }  // namespace w4vec

@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgptq_mi3
 GPTQ_OK, GPTQ_EINVAL, GPTQ_EUNSUPPORTED, GPTQ_EHIP, GPTQ_ENOTSPD = range(5)
 GPTQ_BF16, GPTQ_F32, GPTQ_I8 = 0, 1, 2
 GPTQ_MATVEC_MAX_M = 64
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}  # gptq_activation
 
 _lib = None
 
@@ -78,6 +79,15 @@ def lib() -> ctypes.CDLL:
         "gptq_w4a8_workspace": (SZ, [I64, I64, I64, I]),
         "gptq_add_rmsnorm": (I, [P, I, I64, P, I, I64, P, I64, P, I, D, I64, I64, P, I, I64, P,
                                  P]),
+        "gptq_w4a16_linear": (I, [P, I64, I64, P, P, P, I64, I64, I, I, P, I, I, I, P, I, I64, P,
+                                  I, I64, P, SZ, P]),
+        "gptq_w4a16_linear_workspace": (SZ, [I64, I64, I64, I, I]),
+        "gptq_qk_norm_rope": (I, [P, I64, I64, P, I64, I64, P, I64, I64, I, I64, I, I, I, P, P, I,
+                                  I, P, P, I, D, P, I64, P, I64, I64, P, I64, I64, P, I64, I64,
+                                  P]),
+        "gptq_attention": (I, [P, I64, I64, P, I64, I64, P, I64, I64, I64, I64, I64, I, I, I, P, P,
+                               P, I64, I, D, P, I64, I64, P, SZ, P]),
+        "gptq_attention_workspace": (SZ, [I64, I64, I, I, I, I64]),
         "gptq_quantize_layers": (I, [P, P, I, I, I64, P, P, I, I, I, I, P, P, P, P, P, SZ, P]),
         "gptq_act_order": (I, [P, I, I64, I64, I64, P, P, P, SZ, P]),
         "gptq_act_order_workspace": (SZ, [I64, I64]),
@@ -504,8 +514,8 @@ def _span(ws):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
-def _w4_checks(where, X, x_dtype, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream):
-    """The packed weights' shapes against X's; returns (index, m, d_in, d_out, ldx, Y).  A group
+def _w4_inputs(where, X, x_dtype, qweight, scales_f16, zeros_f16, group_size, sym):
+    """The packed weights' shapes against X's; returns (index, m, d_in, d_out, ldx).  A group
     size that the library refuses is left to it: it reads nothing then."""
     index = _index(where, X, (x_dtype,))
     m, d_in = X.shape
@@ -532,12 +542,19 @@ def _w4_checks(where, X, x_dtype, qweight, scales_f16, zeros_f16, group_size, sy
                 raise ValueError(f"{where}: zeros_f16 is needed unless sym")
             _flat(where, "zeros_f16", zeros_f16, meta, _W16_TYPES, index)
         raise ValueError(f"{where}: X must be row-major, got strides {X.stride()}")
+    return index, m, d_in, d_out, ldx if m > 1 else d_in
+
+
+def _w4_checks(where, X, x_dtype, qweight, scales_f16, zeros_f16, group_size, sym, Y, stream):
+    """The same with the product's fp32 Y; returns (index, m, d_in, d_out, ldx, Y)."""
+    index, m, d_in, d_out, ldx = _w4_inputs(where, X, x_dtype, qweight, scales_f16, zeros_f16,
+                                            group_size, sym)
     if Y is None:
         Y = _empty(stream, (m, d_out), dtype=torch.float32, device=X.device)
     elif not (Y.shape == (m, d_out) and Y.dtype is torch.float32 and Y.is_contiguous()
               and Y.get_device() == index):
         _flat(where, "Y", Y, (m, d_out), (torch.float32,), index)
-    return index, m, d_in, d_out, ldx if m > 1 else d_in, Y
+    return index, m, d_in, d_out, ldx, Y
 
 
 @functools.lru_cache(maxsize=1024)
@@ -628,3 +645,183 @@ def gptq_add_rmsnorm(X: torch.Tensor, weight: torch.Tensor, *,
           _dtype_code(weight), float(eps), m, d, out.data_ptr(), GPTQ_I8 if i8 else GPTQ_BF16, ldo,
           out_scales.data_ptr() if i8 else None, _raw_stream(where, index, stream))
     return out, out_scales, residual_out
+
+
+# ------------------------------------------------ completing a decoder block
+@functools.lru_cache(maxsize=1024)
+def gptq_w4a16_linear_workspace(m: int, d_out: int, d_in: int, group_size: int,
+                                gated: bool = False) -> int:
+    return int(lib().gptq_w4a16_linear_workspace(m, d_out, d_in, group_size, int(bool(gated))))
+
+
+def gptq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.Tensor,
+                      zeros_f16: torch.Tensor | None, *, group_size: int, sym: bool,
+                      bias: torch.Tensor | None = None, activation: str = "none",
+                      gated: bool = False, residual: torch.Tensor | None = None,
+                      out_dtype: torch.dtype = torch.bfloat16, Y: torch.Tensor | None = None,
+                      ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y = act(X W^T + bias) + residual for X [m, d_in] bf16 and the packed 4-bit weights, any m;
+    gated: act(gate) * up + residual [m, d_out / 2], the gate's weight rows (and bias) stacked
+    before the up projection's.  activation: a key of ACTIVATIONS.  Y = residual updates it in
+    place."""
+    where = "gptq_w4a16_linear"
+    index, m, d_in, d_out, ldx = _w4_inputs(where, X, torch.bfloat16, qweight, scales_f16,
+                                            zeros_f16, group_size, sym)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"{where}: activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    if gated and d_out % 2:
+        raise ValueError(f"{where}: gated weights have an even number of rows, got {d_out}")
+    shape = (m, d_out // 2 if gated else d_out)
+    if Y is None:
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"{where}: out_dtype must be one of {_FLOATS}")
+        Y = _empty(stream, shape, dtype=out_dtype, device=X.device)
+    ldy = _rows(where, "Y", Y, shape, (out_dtype,) if out_dtype in _FLOATS else _FLOATS, index)
+    b_ptr = b_code = r_ptr = r_code = ldr = 0
+    if bias is not None:
+        _flat(where, "bias", bias, (d_out,), _FLOATS, index)
+        b_ptr, b_code = bias.data_ptr(), _dtype_code(bias)
+    if residual is not None:
+        ldr = _rows(where, "residual", residual, shape, _FLOATS, index)
+        r_ptr, r_code = residual.data_ptr(), _dtype_code(residual)
+    ws = _scratch(where, ws, gptq_w4a16_linear_workspace(m, d_out, d_in, group_size, bool(gated)), X,
+                  stream)
+    _call(where, index, lib().gptq_w4a16_linear, X.data_ptr(), m, ldx, qweight.data_ptr(),
+          scales_f16.data_ptr(), None if sym else zeros_f16.data_ptr(), d_out, d_in, group_size,
+          1 if sym else 0, b_ptr, b_code, act, 1 if gated else 0, r_ptr, r_code, ldr, Y.data_ptr(),
+          _dtype_code(Y), ldy, *_span(ws), _raw_stream(where, index, stream))
+    return Y
+
+
+def _heads(where: str, name: str, t: torch.Tensor, shape, dtypes, index: int):
+    """Checks an array of heads [rows, heads, hd] (None: any number) and returns its strides
+    between rows and heads, those that no second row or head uses as if it were dense."""
+    rows, heads, hd = t.shape if t.dim() == 3 else (-1, -1, -1)
+    if not (t.dim() == 3 and t.dtype in dtypes and t.get_device() == index
+            and all(b is None or a == b for a, b in zip((rows, heads, hd), shape))
+            and (t.stride(2) == 1 or hd == 1)):
+        raise ValueError(f"{where}: {name} must be {list(shape)} of {dtypes} on GPU {index} with "
+                         f"neighbouring columns, got {list(t.shape)} {t.dtype} of strides "
+                         f"{t.stride()} on {t.device}")
+    return (t.stride(0) if rows > 1 else heads * hd), (t.stride(1) if heads > 1 else hd)
+
+
+def gptq_qk_norm_rope(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor | None = None, *,
+                      positions: torch.Tensor | None, inv_freq: torch.Tensor | None,
+                      q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                      eps: float = 1e-6, interleaved: bool = False,
+                      slots: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                      k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
+                      stream=None):
+    """Q [m, hq, hd], K and V [m, hk, hd] (bf16 or fp32): queries and keys normalized over each
+    head (with a weight), their first 2 len(inv_freq) columns turned by positions[t] inv_freq[i]
+    (float64), all rounded to bf16.  slots [m] int64: the rows of k_out and v_out (a cache) that
+    the tokens' keys and values go to; one outside writes nothing.  Returns (q_out, k_out, v_out
+    or None)."""
+    where = "gptq_qk_norm_rope"
+    if Q.dim() != 3 or not Q.is_cuda:
+        raise ValueError(f"{where}: Q must be [m, hq, hd] on a GPU")
+    index = Q.get_device()
+    m, hq, hd = Q.shape
+    ldq, hsq = _heads(where, "Q", Q, (m, None, hd), _FLOATS, index)
+    ldk, hsk = _heads(where, "K", K, (m, None, hd), (Q.dtype,), index)
+    hk = K.shape[1]
+    ldv = hsv = ldvo = hsvo = 0
+    if V is not None:
+        ldv, hsv = _heads(where, "V", V, (m, hk, hd), (Q.dtype,), index)
+    elif v_out is not None:
+        raise ValueError(f"{where}: v_out without V")
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _flat(where, "inv_freq", inv_freq, (rot // 2,), (torch.float64,), index)
+        if positions is None:
+            raise ValueError(f"{where}: inv_freq without positions")
+    if positions is not None:
+        _flat(where, "positions", positions, (m,), (torch.int32,), index)
+    w_code = 0
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _flat(where, name, w, (hd,), _FLOATS, index)
+            w_code = _dtype_code(w)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError(f"{where}: q_weight and k_weight must have one type")
+    bf16 = (torch.bfloat16,)
+    rows = m
+    if slots is not None:
+        _flat(where, "slots", slots, (m,), (torch.int64,), index)
+        if k_out is None or (V is not None and v_out is None):
+            raise ValueError(f"{where}: slots need k_out (and v_out with V)")
+        rows = k_out.shape[0]
+    if q_out is None:
+        q_out = _empty(stream, (m, hq, hd), dtype=torch.bfloat16, device=Q.device)
+    if k_out is None:
+        k_out = _empty(stream, (m, hk, hd), dtype=torch.bfloat16, device=Q.device)
+    if V is not None and v_out is None:
+        v_out = _empty(stream, (m, hk, hd), dtype=torch.bfloat16, device=Q.device)
+    ldqo, hsqo = _heads(where, "q_out", q_out, (m, hq, hd), bf16, index)
+    ldko, hsko = _heads(where, "k_out", k_out, (rows, hk, hd), bf16, index)
+    if V is not None:
+        ldvo, hsvo = _heads(where, "v_out", v_out, (rows, hk, hd), bf16, index)
+    _call(where, index, lib().gptq_qk_norm_rope, Q.data_ptr(), ldq, hsq, K.data_ptr(), ldk, hsk,
+          None if V is None else V.data_ptr(), ldv, hsv, _dtype_code(Q), m, hq, hk, hd,
+          positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None, rot,
+          1 if interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
+          None if k_weight is None else k_weight.data_ptr(), w_code, float(eps),
+          None if slots is None else slots.data_ptr(), rows, q_out.data_ptr(), ldqo, hsqo,
+          k_out.data_ptr(), ldko, hsko, None if V is None else v_out.data_ptr(), ldvo, hsvo,
+          _raw_stream(where, index, stream))
+    return q_out, k_out, v_out
+
+
+@functools.lru_cache(maxsize=1024)
+def gptq_attention_workspace(total_q: int, batch: int, hq: int, hk: int, hd: int,
+                             max_kv_len: int) -> int:
+    return int(lib().gptq_attention_workspace(total_q, batch, hq, hk, hd, max_kv_len))
+
+
+def gptq_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, *, cu_q: torch.Tensor,
+                   kv_start: torch.Tensor | None = None, kv_len: torch.Tensor | None = None,
+                   causal: bool = True, scale: float | None = None,
+                   max_kv_len: int | None = None, out: torch.Tensor | None = None,
+                   ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of Q [total_q, hq, hd] over K and V [kv_rows, hk, hd], bf16.  Sequence s has the
+    queries cu_q[s] .. cu_q[s + 1] - 1 (int32 [batch + 1]) and the kv_len[s] (int32) rows of K and
+    V from kv_start[s] (int64) on, or, without these, its queries' own rows.  causal: the last
+    query sees every key, each one before it one fewer.  scale: 1 / sqrt(hd) by default.
+    max_kv_len: the longest kv_len where the caller knows it (only for speed; by default the rows
+    of K).  Rows of out outside all sequences are left as they were."""
+    where = "gptq_attention"
+    if Q.dim() != 3 or not Q.is_cuda:
+        raise ValueError(f"{where}: Q must be [total_q, hq, hd] on a GPU")
+    index = Q.get_device()
+    tq, hq, hd = Q.shape
+    bf16 = (torch.bfloat16,)
+    ldq, hsq = _heads(where, "Q", Q, (tq, hq, hd), bf16, index)
+    ldk, hsk = _heads(where, "K", K, (None, None, hd), bf16, index)
+    rows, hk, _ = K.shape
+    ldv, hsv = _heads(where, "V", V, (rows, hk, hd), bf16, index)
+    batch = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
+    if batch < 0:
+        raise ValueError(f"{where}: cu_q must be [batch + 1]")
+    _flat(where, "cu_q", cu_q, (batch + 1,), (torch.int32,), index)
+    if (kv_start is None) != (kv_len is None):
+        raise ValueError(f"{where}: kv_start and kv_len belong together")
+    if kv_start is not None:
+        _flat(where, "kv_start", kv_start, (batch,), (torch.int64,), index)
+        _flat(where, "kv_len", kv_len, (batch,), (torch.int32,), index)
+    elif rows != tq:
+        raise ValueError(f"{where}: without kv_start K and V have the queries' rows, {tq}, got {rows}")
+    if out is None:
+        out = _empty(stream, (tq, hq, hd), dtype=torch.bfloat16, device=Q.device)
+    ldo, hso = _heads(where, "out", out, (tq, hq, hd), bf16, index)
+    longest = rows if max_kv_len is None else min(int(max_kv_len), rows)
+    ws = _scratch(where, ws, gptq_attention_workspace(tq, batch, hq, hk, hd, longest), Q, stream)
+    _call(where, index, lib().gptq_attention, Q.data_ptr(), ldq, hsq, K.data_ptr(), ldk, hsk,
+          V.data_ptr(), ldv, hsv, tq, rows, batch, hq, hk, hd, cu_q.data_ptr(),
+          None if kv_start is None else kv_start.data_ptr(),
+          None if kv_len is None else kv_len.data_ptr(), longest, 1 if causal else 0,
+          hd ** -0.5 if scale is None else float(scale), out.data_ptr(), ldo, hso, *_span(ws),
+          _raw_stream(where, index, stream))
+    return out
