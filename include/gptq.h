@@ -412,7 +412,8 @@ size_t gptq_w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_siz
  *               F..2F-1 the up projection's, stacked as gptq_quantize_layers
  *               leaves them.
  *
- * X           [m x ldx] bf16, row-major; 16-byte aligned, ldx a multiple of 8.
+ * X           [m x ldx] bf16, row-major; 16-byte aligned, ldx a multiple of 8, at
+ *             most 2^23 (GPTQ_EUNSUPPORTED past it).
  * qweight, scales_f16, zeros_f16, group_size, sym: as gptq_w4a16_matvec.  Zeros
  *             are whole numbers, as gptq_pack writes them.
  * bias        [d_out] of bias_dtype (bf16 or float32), or NULL: none.
@@ -424,9 +425,8 @@ size_t gptq_w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_siz
  * Y           [m x ldy] out of y_dtype (bf16 or float32); columns past the used
  *             ones are left as they were.
  * m           0 (no-op) .. 2^30; d_in a multiple of 32, <= 65536.
- * ws          gptq_w4a16_linear_workspace(...) bytes: 0 for most shapes of a few
- *             tokens (m <= 64); for more, the scales laid out by groups, and parts
- *             of the sums where k is split.  Its contents on entry do not matter;
+ * ws          gptq_w4a16_linear_workspace(...) bytes: parts of the sums where k is
+ *             split over workgroups, else 0.  Its contents on entry do not matter;
  *             calls in flight together need one each.
  * Products are exact; sums, the group scaling and everything behind them are
  * float32, rounded once to Y's type.  The order of every sum is fixed: the same

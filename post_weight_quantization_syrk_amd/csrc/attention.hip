@@ -32,14 +32,19 @@ constexpr float NO_MAX = -3.0e38f;  // of a row that has seen no key yet
 // rounding, and sums stay far inside float32.
 constexpr float GROWTH = 8.0f;
 
-// Unit (16 bytes) u of row r of a tile in LDS stands at u ^ swizzle(r): eight rows
-// read at one unit, and four rows read at two, fall on different banks.
+// Unit (16 bytes) u of row r of a tile in LDS stands at u ^ swizzle(r).  A cycle
+// serves 256 bytes: sixteen rows read at one unit (keys), and four rows read at
+// four neighbouring units (values), fall on different banks, whatever a row's 64 DB
+// bytes leave over 256.  (With three bits in place of four at DB = 4 half of the
+// LDS cycles were conflicts.)
 template <int DB>
 __device__ __forceinline__ int swizzle(int r) {
-  if constexpr (DB % 2 == 0)
-    return ((r & 3) << 1) | ((r >> 2) & 1);
-  else  // rows of 64 bytes more or less than a multiple of 128
-    return (r & 2) | ((r >> 2) & 1);
+  if constexpr (DB % 4 == 0)
+    return ((r & 3) << 2) | ((r >> 2) & 3);
+  else if constexpr (DB % 2 == 0)
+    return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  else
+    return (r >> 2) & 3;
 }
 
 // Direct global -> LDS load of 16 bytes per lane at a uniform base and a lane's

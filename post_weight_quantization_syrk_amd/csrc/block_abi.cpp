@@ -89,6 +89,7 @@ int gptq_w4a16_linear(const void* X, int64_t m, int64_t ldx, const uint32_t* qwe
   if (m == 0) return GPTQ_OK;
   const int64_t F = gated ? d_out / 2 : d_out;
   if (ldx < d_in || ldx % 8 != 0 || !X || !aligned(X, 16)) return GPTQ_EINVAL;
+  if (ldx > 1 << 23) return GPTQ_EUNSUPPORTED;
   if (!qweight || !scales_f16 || (!sym && !zeros_f16) || !aligned(qweight, 16) ||
       !aligned(scales_f16, 2) || !aligned(zeros_f16, 2))
     return GPTQ_EINVAL;

@@ -97,27 +97,54 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t row, int64_t 
   }
 }
 
-// The splits' sums [splits][m][n] added in split order, then finished.
+// The splits' sums [splits][m][n] added in split order, then finished: four
+// neighbouring columns per thread, four splits' loads at a time.
 template <bool GATED>
 __global__ __launch_bounds__(256) void join_finish_kernel(const float* __restrict__ part, int64_t m,
                                                           int n, int splits, Epilogue e) {
+  const int per = (e.F + 3) / 4;
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= m * e.F) return;
-  const int64_t row = t / e.F, u = t - row * e.F;
+  if (t >= m * per) return;
+  const int64_t row = t / per;
+  const int u = 4 * (int)(t - row * per), cols = min(4, e.F - u);
   const float* p = part + row * n + u;
-  float v0 = 0.0f, v1 = 0.0f;
-  for (int s = 0; s < splits; ++s, p += m * n) {
-    v0 += p[0];
-    if constexpr (GATED) v1 += p[e.F];
+  const int64_t next = m * n;
+  const bool whole = cols == 4 && n % 4 == 0 && e.F % 4 == 0;  // aligned
+  float v0[4] = {}, v1[4] = {};
+  for (int s = 0; s < splits; s += 4) {
+    float a[4][4], b[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* q = p + min(s + i, splits - 1) * next;
+      if (whole) {
+        *(float4*)a[i] = *(const float4*)q;
+        if constexpr (GATED) *(float4*)b[i] = *(const float4*)(q + e.F);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          a[i][k] = q[min(k, cols - 1)];
+          if constexpr (GATED) b[i][k] = q[e.F + min(k, cols - 1)];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s + i >= splits) break;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v0[k] += a[i][k];
+        if constexpr (GATED) v1[k] += b[i][k];
+      }
+    }
   }
-  finish<GATED>(e, row, u, v0, v1);
+  finish4<GATED>(e, row, u, cols, v0, v1);
 }
 
 template <bool GATED>
 hipError_t join_finish_launch(const float* part, int64_t m, int n, int splits, const Epilogue& e,
                               hipStream_t stream) {
-  hipLaunchKernelGGL((join_finish_kernel<GATED>), dim3((unsigned)ceil_div(m * e.F, 256)), dim3(256),
-                     0, stream, part, m, n, splits, e);
+  hipLaunchKernelGGL((join_finish_kernel<GATED>), dim3((unsigned)ceil_div(m * ((e.F + 3) / 4), 256)),
+                     dim3(256), 0, stream, part, m, n, splits, e);
   return hipGetLastError();
 }
 

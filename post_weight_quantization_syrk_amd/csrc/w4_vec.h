@@ -144,6 +144,19 @@ __device__ __forceinline__ void dma16_at(const void* p, uint32_t lds) {
                    : "memory", "m0");
 }
 
+// The same at a uniform base and a lane's offset.
+__device__ __forceinline__ void dma16_from(const void* base, uint32_t voff, uint32_t lds) {
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  const uint32_t blo = __builtin_amdgcn_readfirstlane((uint32_t)b);
+  const uint32_t bhi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  const void* sbase = (const void*)(uintptr_t)(((uint64_t)bhi << 32) | blo);
+  const uint32_t lbase = __builtin_amdgcn_readfirstlane(lds);
+  __asm__ volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                   :
+                   : "v"(voff), "s"(sbase), "s"(lbase)
+                   : "memory", "m0");
+}
+
 constexpr int LDS_BYTES = 160 * 1024;
 
 // LDS of a wave: two steps' words, and a word with the scale and zero of each

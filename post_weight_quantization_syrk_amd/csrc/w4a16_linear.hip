@@ -16,15 +16,8 @@ namespace {
 
 constexpr int KCH = 64;  // k per chunk: 128 bytes of a row of X, 32 of a weight row
 
-// Per group and weight row a word with the scale's binary16 bits below and the
-// zero's above.  Columns stand in the order in which the tiles take weight rows:
-// gated, 32 gate rows, then the 32 up rows that go with them.
-struct Layout {
-  int64_t cols;  // weight rows, padded to whole tiles
-  int ng;
-  size_t bytes;
-};
-
+// Columns of a tile in the order in which it takes weight rows: gated, 32 gate
+// rows, then the 32 up rows that go with them.
 template <bool GATED>
 __device__ __forceinline__ int64_t weight_row(int64_t c, int F) {
   return GATED ? (c >> 6) * 32 + (c & 31) + ((c >> 5) & 1) * F : c;
@@ -34,40 +27,70 @@ __device__ __forceinline__ bool weight_row_in(int64_t c, int F) {
   return GATED ? (c >> 6) * 32 + (c & 31) < F : c < F;
 }
 
+// The weights in eight bits, for calls with many rows of X: q - z as e4m3, which
+// has every whole number up to 16 in magnitude, so that two leave for bf16 with one
+// operation and no zero is taken off again.  Panels of 32 columns x 64 k (2 KB),
+// chunk after chunk, 16-byte unit u of row r at u ^ (r / 4 mod 4), as the tiles
+// have them in LDS; columns past the last and k past the row's end are zeros.
+// Scales follow as float32 [ng][cols].  (57344 x 8192: 0.15 ms.)
+struct Wide {
+  int64_t cols;  // padded to whole tiles
+  int nch, ng;
+  size_t scales;  // byte offset
+  size_t bytes;
+};
+
+Wide wide_of(int64_t d_out, int64_t d_in, int group_size, bool gated) {
+  Wide w;
+  w.cols = ceil_div(gated ? ceil_div(d_out / 2, 32) * 64 : d_out, 256) * 256;
+  w.nch = (int)ceil_div(d_in, KCH);
+  w.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
+  w.scales = (size_t)w.cols * w.nch * KCH;
+  w.bytes = w.scales + (size_t)w.cols * w.ng * 4;
+  return w;
+}
+
 template <bool GATED>
-__global__ __launch_bounds__(256) void linear_layout_kernel(Layout l, int F,
-                                                            const uint16_t* __restrict__ S16,
-                                                            const uint16_t* __restrict__ Z16,
-                                                            int vec, uint32_t* __restrict__ ws) {
+__global__ __launch_bounds__(256) void widen_kernel(Wide w, int F, int K, int G,
+                                                    const uint32_t* __restrict__ Q,
+                                                    const uint16_t* __restrict__ S16,
+                                                    const uint16_t* __restrict__ Z16,
+                                                    char* __restrict__ ws) {
+  const int64_t pieces = w.cols * w.nch * 2;  // of 32 k
   const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t params = ceil_div(l.ng, vec) * l.cols;
-  if (t >= params) return;
-  const int g = (int)(t / l.cols) * vec;
-  const int64_t c = t % l.cols;
-  const bool in = weight_row_in<GATED>(c, F);
-  uint16_t s[8] = {}, z[8];
+  if (t < pieces) {
+    const int64_t c = t / (2 * w.nch);
+    const int piece = (int)(t - c * (2 * w.nch)), k = 32 * piece;
+    const int r = (int)(c & 31);
+    uint4 o[2] = {};
+    if (k < K && weight_row_in<GATED>(c, F)) {
+      const int64_t row = weight_row<GATED>(c, F);
+      const uint4 v = *(const uint4*)((const char*)Q + row * (K / 2) + k / 2);
+      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+      const float z = Z16 ? w4vec::half_bits(Z16[row * w.ng + k / G]) : 8.0f;
+      uint32_t out[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) z[i] = 0x4800;  // 8
-  if (in) {
-    const int64_t at = weight_row<GATED>(c, F) * l.ng + g;
-    if (vec == 8) {
-      *(uint4*)s = *(const uint4*)(S16 + at);
-      if (Z16) *(uint4*)z = *(const uint4*)(Z16 + at);
-    } else if (vec == 4) {
-      *(uint2*)s = *(const uint2*)(S16 + at);
-      if (Z16) *(uint2*)z = *(const uint2*)(Z16 + at);
-    } else if (vec == 2) {
-      *(uint32_t*)s = *(const uint32_t*)(S16 + at);
-      if (Z16) *(uint32_t*)z = *(const uint32_t*)(Z16 + at);
-    } else {
-      s[0] = S16[at];
-      if (Z16) z[0] = Z16[at];
+      for (int i = 0; i < 8; ++i) {
+        float f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = (float)((in[i / 2] >> (16 * (i & 1) + 4 * j)) & 15u) - z;
+        int b = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+        out[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], b, true);
+      }
+      o[0] = make_uint4(out[0], out[1], out[2], out[3]);
+      o[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
-  }
-  uint32_t* out = ws + (int64_t)g * l.cols + c;
+    char* const panel = ws + ((c >> 5) * w.nch + (piece >> 1)) * 2048 + r * 64;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < vec) out[i * l.cols] = (uint32_t)s[i] | (uint32_t)z[i] << 16;
+    for (int j = 0; j < 2; ++j)
+      *(uint4*)(panel + 16 * ((2 * (piece & 1) + j) ^ ((r >> 2) & 3))) = o[j];
+  } else if (t - pieces < w.cols * w.ng) {
+    const int64_t i = t - pieces;
+    const int g = (int)(i / w.cols);
+    const int64_t c = i - g * w.cols;
+    ((float*)(ws + w.scales))[i] =
+        weight_row_in<GATED>(c, F) ? w4vec::half_bits(S16[weight_row<GATED>(c, F) * w.ng + g]) : 0.0f;
+  }
 }
 
 // The eight codes of a word minus the zero, as bf16 in k order: even and odd
@@ -89,39 +112,62 @@ __device__ __forceinline__ bf16x8 minus_zero(uint32_t w, float z) {
   return r;
 }
 
+// Eight of the wide weights.
+__device__ __forceinline__ bf16x8 from_wide(uint32_t a, uint32_t b) {
+  const w4vec::bf16x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+  const w4vec::bf16x2 p1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+  const w4vec::bf16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+  const w4vec::bf16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+  return bf16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
 struct Args {
   const char* x;
   int64_t ldx;    // bytes
   const uint32_t* q;
-  const uint32_t* sz;
+  const uint16_t *s16, *z16;  // z16 null: symmetric
+  const char* wide;           // the weights in eight bits, or null
+  const float* scales;        // and their scales [ng][cols]
+  int64_t cols;
   float* part;    // splits' sums [splits][M][N], null: finished here
   Epilogue e;
-  Layout l;
   int64_t M;
-  int N, K;
+  int N, K, ng;
   int tiles_m, tiles_n;
   int splits, per_split;  // of the chunks
 };
 
-template <int MI, int NI, int G>
+// A wave's tile: up to 256 rows of X by 32 weight rows, or, of the wide weights,
+// 128 by 64.
+constexpr int blocks_n(bool wide) { return wide ? 2 : 1; }
+constexpr int most_m(bool wide) { return wide ? 4 : 8; }
+constexpr int tile_n(bool wide) { return 128 * blocks_n(wide); }
+constexpr int BLOCK = 8;  // groups whose scales a wave has in LDS
+constexpr int SCALES = 4 * BLOCK * 32 * 4;
+constexpr int LDS_BYTES = 80 * 1024;  // two workgroups on a CU
+
+template <int MI, bool WIDE>
 struct Shape {
-  static constexpr int TM = 32 * MI, TN = 128 * NI;
-  static constexpr int GPC = G == 0 ? 0 : G >= KCH ? 1 : KCH / G;  // groups in a chunk
-  static constexpr int ABYTES = TM * 2 * KCH, BBYTES = TN * (KCH / 2), SZBYTES = GPC * TN * 4;
-  static constexpr int STAGE = ABYTES + BBYTES + SZBYTES;
-  static constexpr int OUT = 32 * TN * 4;  // 32 rows of sums on their way out
-  static constexpr int LDS = 2 * STAGE > OUT ? 2 * STAGE : OUT;
+  static constexpr int ABYTES = 32 * MI * 2 * KCH, BBYTES = tile_n(WIDE) * KCH / (WIDE ? 1 : 2);
+  static constexpr int STAGE = ABYTES + BBYTES;
+  static constexpr int LOADS = MI + 1;  // of a wave per chunk (4-bit weights)
+  // chunks in LDS: two of the wide weights (their scales come by ordinary loads,
+  // which the compiler waits for by waiting for all), else as many as fit, up to four
+  static constexpr int FIT = (LDS_BYTES - SCALES) / STAGE;
+  static constexpr int BUFS = WIDE ? 2 : FIT < 4 ? FIT : 4;
+  static_assert(BUFS >= 2 && BUFS * STAGE <= LDS_BYTES, "two buffers");
 };
 
-// Four waves side by side, each 32 MI rows of X by 32 NI weight rows: a wave
+// Four waves side by side, each all 32 MI rows of X by 32 weight rows: a wave
 // takes the codes of its own weight rows apart, and none twice.  G: group size,
-// 0 for one group per row.  GATED: NI is 2, gate rows and up rows.
-template <int MI, int NI, int G, bool GATED>
+// 0 for one group per row.
+template <int MI, int G, bool GATED, bool WIDE>
 __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m0, int64_t c0,
                                              int split) {
-  typedef Shape<MI, NI, G> S;
-  constexpr int TN = S::TN, GPC = S::GPC, ABYTES = S::ABYTES, BBYTES = S::BBYTES;
-  constexpr int STAGE = S::STAGE;
+  typedef Shape<MI, WIDE> S;
+  constexpr int GPC = G == 32 ? 2 : 1;  // groups in a chunk
+  constexpr int STAGE = S::STAGE, BUFS = S::BUFS, ABYTES = S::ABYTES;
+  constexpr int NI = blocks_n(WIDE), TN = tile_n(WIDE), BL = MI * NI;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, l32 = lane & 31;
@@ -131,104 +177,187 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
   const int F = a.e.F;
 
   // direct loads, 1 KB each: 8 rows of X, or 32 weight rows, at units that put
-  // 16 rows on different banks
-  const char* xrow[MI];
+  // 16 rows on different banks; bases are uniform, lanes have 32-bit offsets
+  const char* xbase = a.x + m0 * a.ldx;
+  auto xu = [&](int j) __attribute__((always_inline)) {  // of row 8 (MI wave + j) + lane / 8
+    return 16 * ((lane & 7) ^ ((4 * (MI * wave + j) + (lane >> 4)) & 7));
+  };
+  uint32_t xoff[MI];
 #pragma unroll
-  for (int j = 0; j < MI; ++j)
-    xrow[j] = a.x + min(m0 + 8 * (MI * wave + j) + (lane >> 3), a.M - 1) * a.ldx;
-  int xu[MI];
-#pragma unroll
-  for (int j = 0; j < MI; ++j)
-    xu[j] = 16 * ((lane & 7) ^ (((8 * (MI * wave + j) + (lane >> 3)) >> 1) & 7));
-  const char* qrow[NI];
-#pragma unroll
-  for (int j = 0; j < NI; ++j) {
-    const int64_t c = wcol + 32 * j + (lane >> 1);
-    qrow[j] = (const char*)a.q +
-              (weight_row_in<GATED>(c, F) ? weight_row<GATED>(c, F) : 0) * (a.K / 2);
+  for (int j = 0; j < MI; ++j) {
+    const int r = 8 * (MI * wave + j) + (lane >> 3);
+    xoff[j] = (uint32_t)min((int64_t)r, a.M - 1 - m0) * (uint32_t)a.ldx + xu(j);
   }
+  // columns past the last: copies of the last valid row of this wave, or of row 0
+  const int64_t row0 = weight_row<GATED>(wcol, F);
+  const int there = weight_row_in<GATED>(wcol, F)
+                        ? (int)min((int64_t)32, F - (GATED ? (wcol >> 6) * 32 : wcol)) : 0;
+  const char* qbase = (const char*)a.q + (there ? row0 : 0) * (a.K / 2);
+  const uint32_t qrow = (uint32_t)min(lane >> 1, max(there - 1, 0)) * (uint32_t)(a.K / 2);
   const int qu = 16 * ((lane & 1) ^ ((lane >> 4) & 1));
-  const uint32_t* sz = a.sz + wcol + 4 * lane;
+  const char* const wbase = a.wide + (wcol >> 5) * nch * 2048;
   auto issue = [&](int c, int buf) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + buf * STAGE;
+    const char* const xb = xbase + (int64_t)c * (2 * KCH);
+    const char* const qb = qbase + (int64_t)c * (KCH / 2);
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int j = 0; j < MI; ++j)
-      w4vec::dma16_at(xrow[j] + min(c * 2 * KCH + xu[j], 2 * a.K - 16),
-                      dst + (MI * wave + j) * 1024);
+      for (int j = 0; j < 2 * NI; ++j)
+        w4vec::dma16_from(wbase + ((int64_t)(j >> 1) * nch + c) * 2048 + 1024 * (j & 1), lane * 16,
+                          dst + ABYTES + (2 * NI * wave + j) * 1024);
+    }
+    if ((c + 1) * KCH <= a.K) {
 #pragma unroll
-    for (int j = 0; j < NI; ++j)
-      w4vec::dma16_at(qrow[j] + min(c * (KCH / 2) + qu, a.K / 2 - 16),
-                      dst + ABYTES + (NI * wave + j) * 1024);
-    if constexpr (G != 0) {
-      if (lane < 8 * NI) {  // this wave's 32 NI words of each group
+      for (int j = 0; j < MI; ++j) w4vec::dma16_from(xb, xoff[j], dst + (MI * wave + j) * 1024);
+      if constexpr (!WIDE) w4vec::dma16_from(qb, qrow + qu, dst + ABYTES + wave * 1024);
+    } else {
+      // a last chunk that is not whole: units past the row's end are copies
+      const int xmost = 2 * a.K - 16 - c * 2 * KCH, qmost = a.K / 2 - 16 - c * (KCH / 2);
 #pragma unroll
-        for (int g = 0; g < GPC; ++g)
-          w4vec::dma16_at(sz + (int64_t)min(G >= KCH ? c * KCH / G : c * GPC + g, a.l.ng - 1) * a.l.cols,
-                          dst + ABYTES + BBYTES + (g * TN + 32 * NI * wave) * 4);
+      for (int j = 0; j < MI; ++j)
+        w4vec::dma16_from(xb, xoff[j] - (uint32_t)max(xu(j) - xmost, 0), dst + (MI * wave + j) * 1024);
+      if constexpr (!WIDE) w4vec::dma16_from(qb, qrow + min(qu, qmost), dst + ABYTES + wave * 1024);
+    }
+  };
+  // The scales and zeros of BLOCK groups of the wave's rows, a word each in LDS:
+  // lane half 0 loads a row's scales, half 1 its zeros, one block ahead.
+  constexpr int CPB = G == 0 ? 1 : BLOCK * G / KCH;  // chunks per block
+  uint32_t* const sc = (uint32_t*)(lds + BUFS * STAGE) + wave * BLOCK * 32;
+  const int64_t mrow = there ? row0 + min(l32, there - 1) : 0;
+  const uint16_t* const meta = (h && a.z16 ? a.z16 : a.s16) + mrow * a.ng;
+  const bool eights = a.z16 == nullptr && h;  // symmetric: zeros are 8
+  uint32_t ahead[4];
+  auto fetch = [&](int b) __attribute__((always_inline)) {
+    if (a.ng >= BLOCK) {
+      // the row's last block starts earlier instead of running past its end
+      __builtin_memcpy(ahead, meta + min(b * BLOCK, a.ng - BLOCK), 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        ahead[j] = meta[min(2 * j, a.ng - 1)] | (uint32_t)meta[min(2 * j + 1, a.ng - 1)] << 16;
+    }
+    if (eights) ahead[0] = ahead[1] = ahead[2] = ahead[3] = 0x48004800u;
+  };
+  auto first_group = [&](int b) __attribute__((always_inline)) {
+    return a.ng >= BLOCK ? min(b * BLOCK, a.ng - BLOCK) : 0;
+  };
+  auto publish = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // scales of groups 2j, 2j + 1 in every lane, and zeros
+      const w4vec::u32x2 r = __builtin_amdgcn_permlane32_swap(ahead[j], ahead[j], false, false);
+      if (h == (j >> 1)) {
+        sc[2 * j * 32 + l32] = __builtin_amdgcn_perm(r[1], r[0], 0x05040100u);
+        sc[(2 * j + 1) * 32 + l32] = __builtin_amdgcn_perm(r[1], r[0], 0x07060302u);
       }
     }
   };
-  uint32_t row_sz[NI];
+  uint32_t row_sz = 0;
+  float next[NI * GPC];  // wide: the scales of the chunk to come (of the row, G = 0)
+  const float* const wscale = a.scales + wcol + l32;
+  auto fetch_wide = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
-  for (int ni = 0; ni < NI; ++ni) row_sz[ni] = G == 0 ? a.sz[wcol + 32 * ni + l32] : 0u;
+    for (int i = 0; i < NI * GPC; ++i)
+      next[i] = wscale[(G == 0 ? 0 : min(c * KCH / (G ? G : 1) + i % GPC, a.ng - 1)) * a.cols + 32 * (i / GPC)];
+  };
+  if constexpr (WIDE) {
+    fetch_wide(ch0);
+  } else if constexpr (G == 0) {
+    row_sz = a.s16[mrow] | (uint32_t)(a.z16 ? a.z16[mrow] : 0x4800) << 16;
+  } else {
+    fetch(ch0 / CPB);
+  }
 
-  constexpr int BL = MI * NI;  // 32 x 32 blocks of a wave, ni the faster index
-  f32x16 tot[BL];
+  f32x16 tot[BL];  // blocks, ni the faster index
 #pragma unroll
   for (int b = 0; b < BL; ++b)
 #pragma unroll
     for (int i = 0; i < 16; ++i) tot[b][i] = 0.0f;
-  issue(ch0, 0);
+#pragma unroll
+  for (int i = 0; i < BUFS - 1; ++i)
+    if (ch0 + i < ch1) issue(ch0 + i, i);
+  int buf = 0, fill = BUFS - 1;
   for (int c = ch0; c < ch1; ++c) {
-    const int buf = (c - ch0) & 1;
     // chunk c has landed, and chunk c - 1's buffer is read
-    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (c + BUFS - 2 < ch1)
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((BUFS - 2) * S::LOADS) : "memory");
+    else
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    float scale[NI * GPC], z[GPC];
+    if constexpr (WIDE && G != 0) {
+      // (here, so that the compiler waits for them before more loads are out)
+#pragma unroll
+      for (int g = 0; g < NI * GPC; ++g) {
+        scale[g] = next[g];
+        asm volatile("" : "+v"(scale[g]));
+      }
+    }
     __syncthreads();
-    if (c + 1 < ch1) issue(c + 1, buf ^ 1);
+    if (c + BUFS - 1 < ch1) issue(c + BUFS - 1, fill);
+    if constexpr (WIDE && G != 0) {
+      if (c + 1 < ch1) fetch_wide(c + 1);
+    }
+    fill = fill + 1 == BUFS ? 0 : fill + 1;
     const char* la = lds + buf * STAGE + l32 * 2 * KCH;
-    const char* lb = lds + buf * STAGE + ABYTES + (32 * NI * wave + l32) * (KCH / 2);
-    const uint32_t* lz =
-        (const uint32_t*)(lds + buf * STAGE + ABYTES + BBYTES) + 32 * NI * wave + l32;
+    const char* lb = lds + buf * STAGE + ABYTES + (32 * NI * wave + l32) * (WIDE ? KCH : KCH / 2);
+    int sc_at[GPC] = {};  // of the chunk's groups; past the row's end, of its last
+    if constexpr (G != 0 && !WIDE) {
+      const int b = c / CPB;
+      if (c == ch0 || c % CPB == 0) {
+        publish();
+        if ((b + 1) * CPB < ch1) fetch(b + 1);
+      }
+#pragma unroll
+      for (int g = 0; g < GPC; ++g)
+        sc_at[g] = (min(c * KCH / G + g, a.ng - 1) - first_group(b)) * 32 + l32;
+    }
+    buf = buf + 1 == BUFS ? 0 : buf + 1;
     const int sw = (l32 >> 3) & 1;
     // MFMA q of a chunk takes, in lane half h, unit u of X: with groups of 32
     // the two halves share 32 consecutive k, otherwise 64
     auto unit = [&](int q) __attribute__((always_inline)) {
       return G == 32 ? 4 * (q >> 1) + 2 * h + (q & 1) : 4 * h + q;
     };
+    auto xfrag = [&](int mi, int q) __attribute__((always_inline)) {
+      return *(const bf16x8*)(la + mi * 32 * 2 * KCH + 16 * (unit(q) ^ ((l32 >> 1) & 7)));
+    };
     const bool tail = (c + 1) * KCH > a.K;  // past the row's end: zeros
-    float scale[NI][GPC ? GPC : 1];
-    bf16x8 bf[NI][4];
+    bf16x8 bf[NI * 4];
+    if constexpr (WIDE) {
 #pragma unroll
-    for (int ni = 0; ni < NI; ++ni) {
-      float z[GPC ? GPC : 1];
-#pragma unroll
-      for (int g = 0; g < (GPC ? GPC : 1); ++g) {
-        const uint32_t v = G == 0 ? row_sz[ni] : lz[g * TN + 32 * ni];
-        scale[ni][g] = w4vec::half_bits((uint16_t)v);
-        z[g] = w4vec::half_bits((uint16_t)(v >> 16));
-        asm("" : "+v"(scale[ni][g]), "+v"(z[g]));  // or every product converts it again
+      for (int i = 0; i < 2 * NI; ++i) {
+        const int j = i & 1, u = G == 32 ? 2 * j + h : 2 * h + j;
+        const uint4 v = *(const uint4*)(lb + (i >> 1) * 32 * KCH + 16 * (u ^ ((l32 >> 2) & 3)));
+        bf[2 * i] = from_wide(v.x, v.y);
+        bf[2 * i + 1] = from_wide(v.z, v.w);
       }
-      const char* lw = lb + 32 * ni * (KCH / 2);
+    } else {
+#pragma unroll
+      for (int g = 0; g < GPC; ++g) {
+        const uint32_t v = G == 0 ? row_sz : sc[sc_at[g]];
+        scale[g] = w4vec::half_bits((uint16_t)v);
+        z[g] = w4vec::half_bits((uint16_t)(v >> 16));
+        asm("" : "+v"(scale[g]), "+v"(z[g]));  // or every product converts it again
+      }
       uint32_t w[4];
       if constexpr (G == 32) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint2 v = *(const uint2*)(lw + 16 * (j ^ sw) + 8 * h);
+          const uint2 v = *(const uint2*)(lb + 16 * (j ^ sw) + 8 * h);
           w[2 * j] = v.x, w[2 * j + 1] = v.y;
         }
       } else {
-        const uint4 v = *(const uint4*)(lw + 16 * (h ^ sw));
+        const uint4 v = *(const uint4*)(lb + 16 * (h ^ sw));
         w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        bf[ni][q] = minus_zero(w[q], z[G == 32 ? q >> 1 : 0]);
-        if (tail && c * KCH + 8 * unit(q) >= a.K) bf[ni][q] = bf16x8{};
+      for (int q = 0; q < 4; ++q) bf[q] = minus_zero(w[q], z[G == 32 ? q >> 1 : 0]);
+      if (tail) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c * KCH + 8 * unit(q) >= a.K) bf[q] = bf16x8{};
       }
     }
-    auto xfrag = [&](int mi, int q) __attribute__((always_inline)) {
-      return *(const bf16x8*)(la + mi * 32 * 2 * KCH + 16 * (unit(q) ^ ((l32 >> 1) & 7)));
-    };
     if constexpr (G == 0) {
 #pragma unroll
       for (int mi = 0; mi < MI; ++mi)
@@ -237,12 +366,13 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
           const bf16x8 x = xfrag(mi, q);
 #pragma unroll
           for (int ni = 0; ni < NI; ++ni)
-            tot[mi * NI + ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, bf[ni][q],
+            tot[mi * NI + ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, bf[4 * ni + q],
                                                                         tot[mi * NI + ni], 0, 0, 0);
         }
     } else {
-      // step s multiplies for one block and one group while the step before it
-      // is scaled into its total; the steps of 32 rows follow one another
+      // step s multiplies for one block and one group while the step before it is
+      // scaled into its total, behind half of the step's products: the sum has
+      // left the matrix cores by then
       constexpr int PER = NI * GPC, STEPS = MI * PER, QPS = 4 / GPC;
       bf16x8 af[2][4];
       f32x16 acc[2];
@@ -263,19 +393,20 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
 #pragma unroll
           for (int q = 0; q < QPS; ++q)
             acc[s & 1] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                af[mi & 1][g * QPS + q], bf[ni][g * QPS + q], acc[s & 1], 0, 0, 0);
+                af[mi & 1][g * QPS + q], bf[4 * ni + g * QPS + q], acc[s & 1], 0, 0, 0);
         }
         if (s > 0) {
           const int p = s - 1;
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            tot[p / GPC][i] = fmaf(scale[p % PER / GPC][p % GPC], acc[p & 1][i], tot[p / GPC][i]);
+            tot[p / GPC][i] = fmaf(scale[p % PER], acc[p & 1][i], tot[p / GPC][i]);
         }
 #pragma unroll
         for (int q = 0; q < QPS; ++q) {
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);        // an LDS read
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);        // a product
-          __builtin_amdgcn_sched_group_barrier(0x002, 16 / QPS, 0); // its share of the scaling
+          if (2 * q >= QPS)
+            __builtin_amdgcn_sched_group_barrier(0x002, 32 / QPS, 0); // its share of the scaling
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -285,7 +416,8 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
 #pragma unroll
     for (int b = 0; b < BL; ++b)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) tot[b][i] *= w4vec::half_bits((uint16_t)row_sz[b % NI]);
+      for (int i = 0; i < 16; ++i)
+        tot[b][i] *= WIDE ? next[b % NI] : w4vec::half_bits((uint16_t)row_sz);
   }
   // Out by way of LDS, 32 rows at a time, four columns to a thread: whole rows of
   // Y are stored, and the epilogue's code is there once.
@@ -335,10 +467,9 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
   }
 }
 
-template <int MI, int NI, int G, bool GATED>
+template <int G, bool GATED, bool WIDE>
 __global__ __launch_bounds__(256, 2) void linear_kernel(Args a) {
-  constexpr int TM = 32 * MI, TN = 128 * NI;
-  __shared__ __attribute__((aligned(1024))) char lds[Shape<MI, NI, G>::LDS];
+  __shared__ __attribute__((aligned(1024))) char lds[LDS_BYTES];
   // consecutive workgroups go to the eight XCDs in turn: each XCD takes a run
   // of tiles, eight tiles of weight rows wide, so that its L2 holds what they
   // share
@@ -349,84 +480,93 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(Args a) {
   const int sup = t / (8 * a.tiles_m), rest = t - sup * 8 * a.tiles_m;
   const int wide = min(8, a.tiles_n - 8 * sup);
   const int tm = rest / wide, tn = 8 * sup + rest - tm * wide;
-  const int64_t m0 = (int64_t)tm * TM, c0 = (int64_t)tn * TN;
-  // the last rows' tile does the work of the rows that are there
-  const int64_t left = a.M - m0;
-  if constexpr (MI >= 2) {
-    if (left <= 32) return tile_product<1, NI, G, GATED>(a, lds, m0, c0, split);
+  // blocks of 32 rows of X, spread over the tiles evenly
+  const int blocks = (int)((a.M + 31) / 32), each = blocks / a.tiles_m, more = blocks % a.tiles_m;
+  const int64_t m0 = 32 * ((int64_t)tm * each + min(tm, more)), c0 = (int64_t)tn * tile_n(WIDE);
+  const int n = each + (tm < more ? 1 : 0);
+  if constexpr (!WIDE) {
+    if (n == 8) return tile_product<8, G, GATED, WIDE>(a, lds, m0, c0, split);
+    if (n == 7) return tile_product<7, G, GATED, WIDE>(a, lds, m0, c0, split);
+    if (n == 6) return tile_product<6, G, GATED, WIDE>(a, lds, m0, c0, split);
+    if (n == 5) return tile_product<5, G, GATED, WIDE>(a, lds, m0, c0, split);
   }
-  if constexpr (MI >= 4) {
-    if (left <= 64) return tile_product<2, NI, G, GATED>(a, lds, m0, c0, split);
-  }
-  tile_product<MI, NI, G, GATED>(a, lds, m0, c0, split);
+  if (n == 4) return tile_product<4, G, GATED, WIDE>(a, lds, m0, c0, split);
+  if (n == 3) return tile_product<3, G, GATED, WIDE>(a, lds, m0, c0, split);
+  if (n == 2) return tile_product<2, G, GATED, WIDE>(a, lds, m0, c0, split);
+  tile_product<1, G, GATED, WIDE>(a, lds, m0, c0, split);
 }
 
 // Few tokens: the kernels that read the weights once for all of them.
 bool few_tokens(int64_t m) { return m <= 64; }
 
 struct Plan {
-  int mi, ni;  // tile: 32 mi rows of X by 128 ni weight rows
+  bool wide;  // weights in eight bits first
+  int tiles_m, tiles_n;
   int splits, per_split;
-  Layout l;
   size_t part_off, bytes;
 };
 
+// Tiles, splits of k and the form of the weights by the least of a time in us,
+// fitted to some 300 launches of 128 to 4096 tokens through seven layers.  A chunk
+// takes a tile of b blocks of 32 rows `alone` where it has a CU to itself (up to
+// 256 workgroups) and `shared` where the CU has two (past 256 some have, with more
+// to wait for than the mean); where the chip is full its power is the bound, and
+// taking four bits apart in every tile costs a tenth more.  Making the weights wide
+// costs a launch and their bytes, splits their sums' bytes.
+// 515 tokens through 4099 x 11008, groups of 32: 92 us with three tiles of rows and
+// k in five (98 with five and three; 106 wide); 2048 tokens through 8192 x 8192: 333
+// us wide, 349 from four bits; 8192 tokens through 57344 x 8192: 7.0 and 7.6 ms.
 Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size, bool gated) {
-  Plan p;
   const int nch = (int)ceil_div(d_in, KCH);
-  p.mi = 4, p.ni = gated || ceil_div(m, 128) * ceil_div(d_out, 256) >= 256 ? 2 : 1;
-  while (p.mi > 1 && ceil_div(m, 32 * p.mi) * ceil_div(d_out, 128 * p.ni) < 256) p.mi /= 2;
-  int64_t splits = 1;
-  while (splits < 8 && splits * 8 <= nch &&
-         ceil_div(m, 32 * p.mi) * ceil_div(d_out, 128 * p.ni) * splits < 256)
-    splits *= 2;
-  p.per_split = (int)ceil_div(nch, splits);
+  const int64_t blocks = ceil_div(m, 32), cols = gated ? ceil_div(d_out / 2, 32) * 64 : d_out;
+  const bool g32 = group_size == 32;
+  Plan p = {};
+  double best = 0.0;
+  for (int wide = 0; wide < 2; ++wide) {
+    const int64_t tiles_n = ceil_div(cols, tile_n(wide));
+    int64_t before = 0;
+    for (int b = most_m(wide); b >= 1; --b) {
+      const int64_t tiles_m = ceil_div(blocks, b);
+      if (tiles_m == before) continue;  // the larger b gave the same tiles
+      before = tiles_m;
+      const int most = (int)ceil_div(blocks, tiles_m);
+      const double alone = wide ? 0.26 + 0.276 * most : 0.32 + (g32 ? 0.173 : 0.146) * most;
+      const double two = wide ? 0.31 + 0.511 * most : g32 ? 0.57 + 0.233 * most : 0.47 + 0.224 * most;
+      for (int splits = 1; splits <= 8 && (splits == 1 || splits * 4 <= nch); ++splits) {
+        const int64_t groups = tiles_m * tiles_n * splits, last = groups % 512;
+        const double shared = std::max(alone, !wide && groups >= 512 ? 1.1 * two : two);
+        const double end = last == 0 ? 0.0
+                           : last <= 256 ? alone
+                                         : alone + (shared - alone) * (0.55 + 0.45 * (double)(last - 256) / 256);
+        double us = (double)ceil_div(nch, splits) * ((double)(groups / 512) * shared + end);
+        if (splits > 1) us += 4.0e-6 * (double)(m * d_out) * (splits + 1) / 3.0;
+        if (wide) us += 4.0 + 1.5e-6 * (double)(cols * d_in) / 5.0;
+        if (best == 0.0 || us < best) {
+          best = us;
+          p.wide = wide, p.tiles_m = (int)tiles_m, p.tiles_n = (int)tiles_n, p.splits = splits;
+        }
+      }
+    }
+  }
+  p.per_split = (int)ceil_div(nch, p.splits);
   p.splits = (int)ceil_div(nch, p.per_split);
-  p.l.cols = ceil_div(gated ? d_out / 2 : d_out, (gated ? 64 : 128) * p.ni) * 128 * p.ni;
-  p.l.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
-  p.l.bytes = (size_t)p.l.ng * p.l.cols * 4;
-  p.part_off = (p.l.bytes + 255) / 256 * 256;
-  p.bytes = p.splits > 1 ? p.part_off + (size_t)p.splits * m * d_out * 4 : p.l.bytes;
+  p.part_off = p.wide ? ceil_div(wide_of(d_out, d_in, group_size, gated).bytes, 256) * 256 : 0;
+  p.bytes = p.part_off + (p.splits > 1 ? (size_t)p.splits * m * d_out * 4 : 0);
   return p;
 }
 
-template <int MI, int NI, bool GATED>
-void launch(const Args& a, int G, hipStream_t stream) {
+template <bool GATED, bool WIDE>
+hipError_t tiles_launch(const Args& a, int G, hipStream_t stream) {
   const dim3 grid((unsigned)(8 * ceil_div((int64_t)a.tiles_m * a.tiles_n * a.splits, 8)));
   switch (G) {
-    case 32: hipLaunchKernelGGL((linear_kernel<MI, NI, 32, GATED>), grid, dim3(256), 0, stream, a); break;
-    case 64: hipLaunchKernelGGL((linear_kernel<MI, NI, 64, GATED>), grid, dim3(256), 0, stream, a); break;
-    case 128: hipLaunchKernelGGL((linear_kernel<MI, NI, 128, GATED>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((linear_kernel<MI, NI, 0, GATED>), grid, dim3(256), 0, stream, a);
+    case 32: hipLaunchKernelGGL((linear_kernel<32, GATED, WIDE>), grid, dim3(256), 0, stream, a); break;
+    case 64: hipLaunchKernelGGL((linear_kernel<64, GATED, WIDE>), grid, dim3(256), 0, stream, a); break;
+    case 128: hipLaunchKernelGGL((linear_kernel<128, GATED, WIDE>), grid, dim3(256), 0, stream, a); break;
+    default: hipLaunchKernelGGL((linear_kernel<0, GATED, WIDE>), grid, dim3(256), 0, stream, a);
   }
-}
-
-template <bool GATED>
-hipError_t tiles_launch(Args a, const Plan& p, int group_size, const uint16_t* scales_f16,
-                        const uint16_t* zeros_f16, void* ws, hipStream_t stream) {
-  const int vec = w4vec::scale_vec(scales_f16, zeros_f16, p.l.ng);
-  const int64_t items = ceil_div(p.l.ng, vec) * p.l.cols;
-  hipLaunchKernelGGL((linear_layout_kernel<GATED>), dim3((unsigned)ceil_div(items, 256)), dim3(256),
-                     0, stream, p.l, a.e.F, scales_f16, zeros_f16, vec, (uint32_t*)ws);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int G = group_size == -1 ? 0 : group_size;
-  if constexpr (GATED) {
-    switch (p.mi) {
-      case 4: launch<4, 2, true>(a, G, stream); break;
-      case 2: launch<2, 2, true>(a, G, stream); break;
-      default: launch<1, 2, true>(a, G, stream);
-    }
-  } else {
-    switch (p.mi) {
-      case 4: p.ni == 2 ? launch<4, 2, false>(a, G, stream) : launch<4, 1, false>(a, G, stream); break;
-      case 2: launch<2, 1, false>(a, G, stream); break;
-      default: launch<1, 1, false>(a, G, stream);
-    }
-  }
-  e = hipGetLastError();
-  if (e != hipSuccess || p.splits == 1) return e;
-  return join_finish_launch<GATED>(a.part, a.M, a.N, p.splits, a.e, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  return join_finish_launch<GATED>(a.part, a.M, a.N, a.splits, a.e, stream);
 }
 
 }  // namespace
@@ -445,13 +585,24 @@ hipError_t linear_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* 
                              gated, e, ws, stream);
   const Plan p = plan_for(m, d_out, d_in, group_size, gated);
   Args a;
-  a.x = (const char*)X, a.ldx = 2 * ldx, a.q = qweight, a.sz = (const uint32_t*)ws;
+  a.x = (const char*)X, a.ldx = 2 * ldx, a.q = qweight, a.s16 = scales_f16, a.z16 = zeros_f16;
   a.part = p.splits > 1 ? (float*)((char*)ws + p.part_off) : nullptr;
-  a.e = e, a.l = p.l, a.M = m, a.N = (int)d_out, a.K = (int)d_in;
-  a.tiles_m = (int)ceil_div(m, 32 * p.mi), a.tiles_n = (int)(p.l.cols / (128 * p.ni));
-  a.splits = p.splits, a.per_split = p.per_split;
-  return gated ? tiles_launch<true>(a, p, group_size, scales_f16, zeros_f16, ws, stream)
-               : tiles_launch<false>(a, p, group_size, scales_f16, zeros_f16, ws, stream);
+  a.e = e, a.M = m, a.N = (int)d_out, a.K = (int)d_in;
+  a.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
+  a.tiles_m = p.tiles_m, a.tiles_n = p.tiles_n, a.splits = p.splits, a.per_split = p.per_split;
+  a.wide = nullptr, a.scales = nullptr, a.cols = 0;
+  const int G = group_size == -1 ? 0 : group_size;
+  if (!p.wide)
+    return gated ? tiles_launch<true, false>(a, G, stream) : tiles_launch<false, false>(a, G, stream);
+  const Wide w = wide_of(d_out, d_in, group_size, gated);
+  a.wide = (const char*)ws, a.scales = (const float*)((char*)ws + w.scales), a.cols = w.cols;
+  const dim3 grid((unsigned)ceil_div(w.cols * (2 * w.nch + w.ng), 256));
+  const auto widen = gated ? widen_kernel<true> : widen_kernel<false>;
+  hipLaunchKernelGGL(widen, grid, dim3(256), 0, stream, w, e.F, (int)d_in,
+                     G == 0 ? (int)d_in : G, qweight, scales_f16, a.z16, (char*)ws);
+  const hipError_t st = hipGetLastError();
+  if (st != hipSuccess) return st;
+  return gated ? tiles_launch<true, true>(a, G, stream) : tiles_launch<false, true>(a, G, stream);
 }
 
 }  // namespace gptq

@@ -232,8 +232,10 @@ def test_refuses(case):
     elif case == "X":
         X = X.float()
     elif case == "workspace":
-        X = c.X[:1].expand(100, 256).contiguous()
-        kw["ws"] = torch.zeros(16, dtype=torch.uint8, device=DEV)
+        c = Case(100, 8192, 64, 128, False)
+        X, dev = c.X, list(c.dev)
+        assert gptq.gptq_w4a16_linear_workspace(100, 64, 8192, 128) > 16
+        kw.update(ws=torch.zeros(16, dtype=torch.uint8, device=DEV), bias=None)
     elif case == "host bias":
         kw["bias"] = torch.zeros(64)
     elif case == "in place, two types":
