@@ -72,12 +72,13 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 
 // The sequence that a tile of rows belongs to, and its place.  Sequence s has
 // its tiles from slot floor(cu[s] group / rows) + s on, which leaves room for
-// them all: no prefix sum over the sequences is needed, only a search.
+// them all: no prefix sum over the sequences is needed, only a search.  (Rows,
+// queries times group, are below 2^31: the front end sees to that.)
 struct Place {
   int64_t q0;     // first query of the sequence
   int64_t start;  // first row of its keys
   int lq, lk;     // queries and keys
-  int64_t row0;   // first row of the tile within the sequence
+  int row0, rows; // first row of the tile within the sequence; rows of the sequence
 };
 
 __device__ __forceinline__ int64_t uniform(int64_t v) {
@@ -86,31 +87,36 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
 }
 
 // Offsets and lengths that do not fit the arrays are brought inside them.
-__device__ __forceinline__ Place find(const AttnArgs& a, int group, int tile_rows, int64_t slot) {
-  const int lane = threadIdx.x & 63;
-  auto cu = [&](int s) __attribute__((always_inline)) {
-    return min(max((int64_t)a.cu_q[s], (int64_t)0), a.tq);
-  };
+template <int TILE_ROWS>
+__device__ __forceinline__ Place find(const AttnArgs& a, int group, int slot) {
+  const int lane = threadIdx.x & 63, tq = (int)a.tq;
   int lo = 0, n = a.batch;
   while (n > 1) {
     const int step = (n + 63) / 64, at = lane * step;
-    const bool le = at < n && cu(lo + min(at, n - 1)) * group / tile_rows + lo + at <= slot;
+    const int c = min(max(a.cu_q[lo + min(at, n - 1)], 0), tq);
+    const bool le = at < n && c * group / TILE_ROWS + lo + at <= slot;
     const int i = max(__builtin_popcountll(__ballot(le)) - 1, 0);
     lo += i * step;
     n = min(step, n - i * step);
   }
   lo = __builtin_amdgcn_readfirstlane(lo);
-  Place p;
-  p.q0 = uniform(cu(lo));
-  p.lq = (int)max(uniform(cu(lo + 1)) - p.q0, (int64_t)0);
-  p.row0 = (slot - (p.q0 * group / tile_rows + lo)) * tile_rows;
+  const int c0 = __builtin_amdgcn_readfirstlane(a.cu_q[lo]);
+  const int c1 = __builtin_amdgcn_readfirstlane(a.cu_q[lo + 1]);
+  int64_t start = 0;
+  int len = 0;
   if (a.kv_start) {
-    p.start = min(max(uniform(a.kv_start[lo]), (int64_t)0), a.kv_rows);
-    p.lk = (int)min((int64_t)max(__builtin_amdgcn_readfirstlane(a.kv_len[lo]), 0), a.kv_rows - p.start);
-  } else {
-    p.start = min(p.q0, a.kv_rows);
-    p.lk = (int)min((int64_t)p.lq, a.kv_rows - p.start);
+    start = uniform(a.kv_start[lo]);
+    len = __builtin_amdgcn_readfirstlane(a.kv_len[lo]);
   }
+  Place p;
+  const int q0 = min(max(c0, 0), tq);
+  p.q0 = q0;
+  p.lq = max(min(max(c1, 0), tq) - q0, 0);
+  p.rows = p.lq * group;
+  p.row0 = (slot - (q0 * group / TILE_ROWS + lo)) * TILE_ROWS;
+  if (!a.kv_start) start = q0, len = p.lq;
+  p.start = min(max(start, (int64_t)0), a.kv_rows);
+  p.lk = (int)min((int64_t)max(len, 0), a.kv_rows - p.start);
   return p;
 }
 
@@ -131,6 +137,10 @@ __device__ __forceinline__ void start_rows(Rows<DB>& w, const uint16_t* qrow, in
     if (d < hd) v = *(const uint4*)(qrow + d);
     __builtin_memcpy(&w.q[i], &v, 16);
   }
+  // used here, so that the compiler waits for them here and not, with all direct
+  // loads in flight, in every step
+#pragma unroll
+  for (int i = 0; i < 2 * DB; ++i) asm volatile("" : "+v"(w.q[i]));
 #pragma unroll
   for (int b = 0; b < DB; ++b) w.o[b] = f32x16{};
   w.mc = NO_MAX, w.l = 0.0f;
@@ -155,6 +165,7 @@ __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const cha
     }
   }
   if (masked) {
+    asm volatile("");
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
@@ -168,6 +179,7 @@ __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const cha
     for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[kb][i]);
   mx = fmaxf(mx, other_half(mx)) * c;
   if (__any(mx > w.mc + GROWTH)) {
+    asm volatile("");  // (stays a branch: it is hardly ever taken)
     const float mc = fmaxf(w.mc, mx), f = exp2_of(w.mc - mc);
     w.mc = mc, w.l *= f;
 #pragma unroll
@@ -241,12 +253,13 @@ __device__ __forceinline__ Slow slow_row(const uint16_t* q, const uint16_t* k, i
 }
 
 struct Grid {
-  int64_t slots;   // tiles of rows, over all sequences
-  int splits;      // of a tile's keys over workgroups
-  float* part;     // splits > 1: [splits][tq][hq][hd + 2]: O, maximum, sum
+  int slots;     // tiles of rows, over all sequences
+  int splits;    // of a tile's keys over workgroups
+  float* part;   // splits > 1: O [splits][tq][hq][hd], then
+  float2* stat;  // maximum and sum [tq][hq][splits]
 };
 
-// Writes row (query, head): finished, or as a part.  e: columns 4 at a time.
+// Four columns of a row (query, head), finished or as a part.
 __device__ __forceinline__ void store4(const AttnArgs& a, const Grid& g, int split, int64_t query,
                                        int head, int d, const float o[4], float mc, float l,
                                        float inv) {
@@ -255,10 +268,9 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Grid& g, int spl
     *(bf16x4*)(a.out + query * a.ldo + head * a.hso + d) =
         bf16x4{(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
   } else {
-    float* p = g.part + ((split * a.tq + query) * a.hq + head) * (a.hd + 2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[d + i] = o[i];
-    if (d == 0) p[a.hd] = mc, p[a.hd + 1] = l;
+    const int64_t row = query * a.hq + head;
+    *(float4*)(g.part + (split * a.tq * a.hq + row) * a.hd + d) = make_float4(o[0], o[1], o[2], o[3]);
+    if (d == 0) g.stat[row * g.splits + split] = make_float2(mc, l);
   }
 }
 
@@ -276,43 +288,63 @@ __device__ __forceinline__ bool finite4(const f32x16& v) {
   return t == 0.0f;
 }
 
-// The wave's 32 rows leave: l is the whole row's sum, o its columns.
+// The wave's 32 rows leave: lane l's is `row` of the sequence (query, head), with
+// l the whole row's sum and o its columns; lim: the last key that it sees.
 template <int DB>
 __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Place& p, int group,
-                                      int kvh, int64_t row0, int64_t rows, int split, int begin,
-                                      int end, float c, const f32x16 (&o)[DB], float mc, float l) {
+                                      int kvh, bool live, int query, int head, int lim, int split,
+                                      int begin, int end, float c, const f32x16 (&o)[DB], float mc,
+                                      float l, char* room) {
+  constexpr int RB = 64 * DB;
   const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
-  const int64_t row = row0 + l32;
-  const int64_t query = row / group;
-  const int head = kvh * group + (int)(row - query * group);
-  const bool live = row < rows;
   const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays)
   bool ok = l - l == 0.0f;
 #pragma unroll
-  for (int b = 0; b < DB; ++b) {
-    ok = ok && finite4(o[b]);
+  for (int b = 0; b < DB; ++b) ok = ok && finite4(o[b]);
+  if (g.splits > 1) {
     if (live) {
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float t[4] = {o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
-        store4(a, g, split, p.q0 + query, head, 32 * b + 2 * i + 4 * h, t, mc, l, inv);
-      }
+      for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float t[4] = {o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
+          store4(a, g, split, p.q0 + query, head, 32 * b + 2 * i + 4 * h, t, mc, l, inv);
+        }
+    }
+  } else {
+    // by way of LDS (the wave's own 32 RB bytes), so that whole rows are stored: in
+    // pieces of 8 bytes a row apart the stores took 4 us of a workgroup's time
+    constexpr int SW = DB % 2 == 0 ? 7 : 3;  // units change places inside their eight, or four
+    __asm__ volatile("" ::: "memory");
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4)
+        *(bf16x4*)(room + l32 * RB + 16 * ((4 * b + (i >> 2)) ^ (l32 & SW)) + 8 * h) =
+            bf16x4{(__bf16)(o[b][i] * inv), (__bf16)(o[b][i + 1] * inv), (__bf16)(o[b][i + 2] * inv),
+                   (__bf16)(o[b][i + 3] * inv)};
+    const int64_t at = live ? (p.q0 + query) * a.ldo + head * a.hso : -1;
+    __asm__ volatile("" ::: "memory");  // the wave's LDS accesses keep their order
+#pragma unroll
+    for (int j = 0; j < 2 * DB; ++j) {
+      const int i = 64 * j + lane, r = i / (4 * DB), u = (i - r * 4 * DB) ^ (r & SW);
+      const uint4 v = *(const uint4*)(room + 16 * i);
+      const int64_t to = __shfl(at, r);
+      if (to >= 0 && 8 * u < a.hd) *(uint4*)(a.out + to + 8 * u) = v;
     }
   }
   if (!a.causal) return;
-  const int lim = (int)min(query + p.lk - p.lq, (int64_t)p.lk - 1);  // the last key seen
   uint64_t bad = __ballot(live && !ok && lim < p.lk - 1);
   uint32_t rest = (uint32_t)bad | (uint32_t)(bad >> 32);
   while (rest) {
     const int r = __builtin_ctz(rest);
     rest &= rest - 1;
-    const int64_t qi = (row0 + r) / group;
-    const int hr = kvh * group + (int)(row0 + r - qi * group);
-    const int last = (int)(qi + p.lk - p.lq) + 1;
-    const Slow s = slow_row(a.q + (p.q0 + qi) * a.ldq + hr * a.hsq,
+    const int64_t qi = p.q0 + __builtin_amdgcn_readlane(query, r);
+    const int hr = __builtin_amdgcn_readlane(head, r), last = __builtin_amdgcn_readlane(lim, r) + 1;
+    const Slow s = slow_row(a.q + qi * a.ldq + hr * a.hsq,
                             a.k + p.start * a.ldk + kvh * a.hsk, a.ldk,
                             a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd, begin, min(end, last), c);
-    store4(a, g, split, p.q0 + qi, hr, 4 * lane, s.o, s.mc, s.l, s.l > 0.0f ? 1.0f / s.l : s.l);
+    store4(a, g, split, qi, hr, 4 * lane, s.o, s.mc, s.l, s.l > 0.0f ? 1.0f / s.l : s.l);
   }
 }
 
@@ -327,29 +359,19 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
   const int l32 = lane & 31, h = lane >> 5;
   // key heads go to the XCDs in turn; of one sequence the later rows, which see
   // more keys, first
-  const int kvh = (int)(blockIdx.x % a.hk);
-  const int64_t rest = blockIdx.x / a.hk;
-  const int split = (int)(rest / g.slots);
-  const int64_t slot = g.slots - 1 - rest % g.slots;
-  const int group = a.hq / a.hk;
-  const Place p = find(a, group, BM, slot);
-  const int64_t rows = (int64_t)p.lq * group;
-  if (p.row0 < 0 || p.row0 >= rows) return;
+  const int kvh = (int)(blockIdx.x % (uint32_t)a.hk), rest = (int)(blockIdx.x / (uint32_t)a.hk);
+  const int split = (int)((uint32_t)rest / (uint32_t)g.slots);
+  const int slot = g.slots - 1 - (rest - split * g.slots);
+  const int group = (int)((uint32_t)a.hq / (uint32_t)a.hk);
+  const Place p = find<BM>(a, group, slot);
+  if (p.row0 < 0 || p.row0 >= p.rows) return;
   const float c = a.scale * 1.4426950408889634f;
 
-  // rows past the last are copies of it
-  const int64_t row0 = p.row0 + 32 * wave, row = min(row0 + l32, rows - 1);
-  const int query = (int)(row / group);
-  const int head = kvh * group + (int)(row - (int64_t)query * group);
-  Rows<DB> w;
-  start_rows<DB>(w, a.q + (p.q0 + query) * a.ldq + head * a.hsq, a.hd, h);
+  // the last key that any row of the tile sees
   const int back = p.lk - p.lq;
-  auto last_key = [&](int64_t r) __attribute__((always_inline)) {  // that row r sees
-    return a.causal ? (int)min(min(r, rows - 1) / group + back, (int64_t)p.lk - 1) : p.lk - 1;
-  };
-  const int lim = last_key(row), lim_first = last_key(row0), lim_last = last_key(row0 + 31);
+  const int tile_last = (int)((uint32_t)min(p.row0 + BM - 1, p.rows - 1) / (uint32_t)group);
   int begin, end;
-  key_range(last_key(p.row0 + BM - 1) + 1, BK, g.splits, split, begin, end);
+  key_range(a.causal ? min(tile_last + back, p.lk - 1) + 1 : p.lk, BK, g.splits, split, begin, end);
 
   // direct loads: this wave's DB KB of each tile, units past hd replaced
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
@@ -375,6 +397,15 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
       dma16(vs, (uint32_t)min(trow[j], most) * (uint32_t)(2 * a.ldv) + tcol[j], dst + TILE + 1024 * j);
   };
   if (begin < end) issue(begin, 0);
+
+  // rows past the last are copies of it
+  const int row0 = p.row0 + 32 * wave, row = min(row0 + l32, p.rows - 1);
+  const int query = (int)((uint32_t)row / (uint32_t)group), head = kvh * group + row - query * group;
+  Rows<DB> w;
+  start_rows<DB>(w, a.q + (p.q0 + query) * a.ldq + head * a.hsq, a.hd, h);
+  // the last key that a row sees: the lane's, the wave's first and last
+  const int lim = a.causal ? min(query + back, p.lk - 1) : p.lk - 1;
+  const int lim_first = __builtin_amdgcn_readlane(lim, 0), lim_last = __builtin_amdgcn_readlane(lim, 31);
   for (int key0 = begin, buf = 0; key0 < end; key0 += BK, buf ^= 1) {
     // this tile has landed, and the other buffer is read
     __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -385,7 +416,9 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
     tile_step<DB, BK / 32>(w, t, t + TILE, c, lim - key0, lim_first < key0 + BK - 1);
   }
   const float l = w.l + other_half(w.l);
-  leave<DB>(a, g, p, group, kvh, row0, rows, split, begin, end, c, w.o, w.mc, l);
+  __syncthreads();  // the tiles are read
+  leave<DB>(a, g, p, group, kvh, row0 + l32 < p.rows, query, head, lim, split, begin, end, c, w.o, w.mc, l,
+            lds + wave * 32 * RB);
 }
 
 // Few rows: one tile of 32 rows, the keys in tiles of 32 that four waves (two,
@@ -400,27 +433,16 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l32 = lane & 31, h = lane >> 5;
-  const int kvh = (int)(blockIdx.x % a.hk);
-  const int64_t rest = blockIdx.x / a.hk;
-  const int split = (int)(rest % g.splits);
-  const int64_t slot = rest / g.splits;
-  const int group = a.hq / a.hk;
-  const Place p = find(a, group, FM, slot);
-  const int64_t rows = (int64_t)p.lq * group;
-  if (p.row0 < 0 || p.row0 >= rows) return;
+  const int kvh = (int)(blockIdx.x % (uint32_t)a.hk), rest = (int)(blockIdx.x / (uint32_t)a.hk);
+  const int slot = (int)((uint32_t)rest / (uint32_t)g.splits), split = rest - slot * g.splits;
+  const int group = (int)((uint32_t)a.hq / (uint32_t)a.hk);
+  const Place p = find<FM>(a, group, slot);
+  if (p.row0 < 0 || p.row0 >= p.rows) return;
   const float c = a.scale * 1.4426950408889634f;
-  const int64_t row = min(p.row0 + l32, rows - 1);
-  const int query = (int)(row / group);
-  const int head = kvh * group + (int)(row - (int64_t)query * group);
-  Rows<DB> w;
-  start_rows<DB>(w, a.q + (p.q0 + query) * a.ldq + head * a.hsq, a.hd, h);
   const int back = p.lk - p.lq;
-  auto last_key = [&](int64_t r) __attribute__((always_inline)) {
-    return a.causal ? (int)min(min(r, rows - 1) / group + back, (int64_t)p.lk - 1) : p.lk - 1;
-  };
-  const int lim = last_key(row), lim_first = last_key(p.row0);
+  const int tile_last = (int)((uint32_t)min(p.row0 + FM - 1, p.rows - 1) / (uint32_t)group);
   int begin, end;
-  key_range(last_key(p.row0 + FM - 1) + 1, FK * FW, g.splits, split, begin, end);
+  key_range(a.causal ? min(tile_last + back, p.lk - 1) + 1 : p.lk, FK * FW, g.splits, split, begin, end);
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 4 * TILE;
   const char* const mine = lds + wave * 4 * TILE;
@@ -447,6 +469,13 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
   };
   const int first = begin + FK * wave;
   if (first < end) issue(first, 0);
+
+  const int row = min(p.row0 + l32, p.rows - 1);
+  const int query = (int)((uint32_t)row / (uint32_t)group), head = kvh * group + row - query * group;
+  Rows<DB> w;
+  start_rows<DB>(w, a.q + (p.q0 + query) * a.ldq + head * a.hsq, a.hd, h);
+  const int lim = a.causal ? min(query + back, p.lk - 1) : p.lk - 1;
+  const int lim_first = __builtin_amdgcn_readlane(lim, 0);
   for (int key0 = first, buf = 0; key0 < end; key0 += FK * FW, buf ^= 1) {
     // every read of the other buffer has returned before it is written again
     __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -493,34 +522,54 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
       for (int from = 1; from < FW; ++from) v += parts[(from - 1) * PER + (16 * b + i) * 64 + lane];
       w.o[b][i] = v;
     }
-  leave<DB>(a, g, p, group, kvh, p.row0, rows, split, begin, end, c, w.o, mc, sum);
+  leave<DB>(a, g, p, group, kvh, p.row0 + l32 < p.rows, query, head, lim, split, begin, end, c, w.o, mc, sum,
+            lds);
 }
 
-// The splits' parts of each row, in split order.
+// The splits' parts of a row, joined by a wave: lane s has split s's maximum and
+// sum, and four columns to a lane of every `subs`-th split's O.
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, Grid g) {
-  const int per = a.hd / 4;  // threads per row
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = t / per;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (row >= a.tq * a.hq) return;
   const int64_t query = row / a.hq;
-  const int d = 4 * (int)(t - row * per), head = (int)(row - query * a.hq);
+  const int head = (int)(row - query * a.hq);
+  const int per = a.hd / 4, subs = max(64 / per, 1), sub = lane / per, d = 4 * (lane - sub * per);
+  const float2 st = g.stat[row * g.splits + min(lane, g.splits - 1)];
   // rows before the first and behind the last sequence are not anyone's
-  const int64_t first = a.cu_q[0], last = a.cu_q[a.batch];
-  if (query < first || query >= last) return;
-  const float* p = g.part + row * (a.hd + 2);
-  const int64_t next = a.tq * a.hq * (a.hd + 2);
-  float mc = NO_MAX;
-  for (int s = 0; s < g.splits; ++s) mc = fmaxf(mc, p[s * next + a.hd]);
-  float l = 0.0f, o[4] = {};
-  for (int s = 0; s < g.splits; ++s) {
-    const float f = exp2_of(p[s * next + a.hd] - mc);
-    l = fmaf(p[s * next + a.hd + 1], f, l);
+  const int first = a.cu_q[0], last = a.cu_q[a.batch];
+  float o[4] = {};
+  float mc = lane < g.splits ? st.x : NO_MAX;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fmaf(p[s * next + d + i], f, o[i]);
+  for (int i = 1; i < 64; i *= 2) mc = fmaxf(mc, __shfl_xor(mc, i));
+  const float f = lane < g.splits ? exp2_of(st.x - mc) : 0.0f;
+  float l = st.y * f;
+#pragma unroll
+  for (int i = 1; i < 64; i *= 2) l += __shfl_xor(l, i);
+  const float* p = g.part + row * a.hd + d;
+  const int64_t next = a.tq * a.hq * a.hd;
+  for (int s = sub; s - sub < g.splits; s += 4 * subs) {  // the same trips for every lane
+    float4 t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) t[i] = *(const float4*)(p + min(s + i * subs, g.splits - 1) * next);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = s + i * subs;
+      const float w = __shfl(f, min(at, 63));
+      if (at < g.splits && sub < subs) {
+        o[0] = fmaf(w, t[i].x, o[0]), o[1] = fmaf(w, t[i].y, o[1]);
+        o[2] = fmaf(w, t[i].z, o[2]), o[3] = fmaf(w, t[i].w, o[3]);
+      }
+    }
   }
+  float sum[4] = {o[0], o[1], o[2], o[3]};
+  for (int i = 1; i < subs; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) sum[k] += __shfl(o[k], (lane + i * per) & 63);
+  if (sub != 0 || query < first || query >= last) return;
   const float inv = l > 0.0f ? 1.0f / l : l;
   *(bf16x4*)(a.out + query * a.ldo + head * a.hso + d) =
-      bf16x4{(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
+      bf16x4{(__bf16)(sum[0] * inv), (__bf16)(sum[1] * inv), (__bf16)(sum[2] * inv), (__bf16)(sum[3] * inv)};
 }
 
 struct Plan {
@@ -529,23 +578,44 @@ struct Plan {
   size_t bytes;
 };
 
+// Few rows (up to 32 to a sequence): the kernel whose waves share the keys; its
+// splits by the least of a time in us.  One workgroup to a CU reads keys and values
+// at up to 35 GB/s, all together at 5.4 TB/s, and takes 4 us besides: 16 sequences
+// of 8192 keys, 8 key heads: 135 us in one piece, 105 in two, 112 in four; 24: 157
+// in one, 162 in four; one sequence of 4096: 44 us in one piece, 11.9 in 16.
+// More rows: two workgroups on every CU where the keys allow pieces of 256 (the
+// queries' own keys count half): 256 queries over 4096 keys: 95 us in one piece, 40
+// in eight; a prompt of 512: 17 us in one, 23 in two.
 Plan plan_for(int64_t tq, int64_t batch, int hq, int hk, int hd, int64_t max_kv_len) {
   Plan p;
   const int group = hq / hk;
   p.few = tq * group <= batch * FM;
   const int rows = p.few ? FM : BM;
-  p.g.slots = tq * group / rows + batch;
+  p.g.slots = (int)(tq * group / rows + batch);
   p.g.splits = 1;
-  p.g.part = nullptr;
-  const int64_t groups = p.g.slots * hk, tiles = ceil_div(max_kv_len, p.few ? 128 : BK);
-  if (groups < 256) p.g.splits = (int)std::max<int64_t>(1, std::min(std::min<int64_t>(ceil_div(256, groups), 32), tiles / 2));
-  p.bytes = p.g.splits > 1 ? (size_t)p.g.splits * tq * hq * (hd + 2) * 4 : 0;
+  p.g.part = nullptr, p.g.stat = nullptr;
+  const int64_t tiles = std::max(batch, ceil_div(tq * group, rows)) * hk;
+  if (p.few) {
+    const double bytes = 4.0 * (double)max_kv_len * hd;  // of a sequence and key head
+    double least = 0.0;
+    for (int s = 1; s <= 32 && (s == 1 || s * 128 <= max_kv_len); ++s) {
+      const int64_t n = tiles * s, full = n / 256, last = n % 256;
+      double us = (double)full * 256 * (bytes / s) / 5.4e6 + 4.0 * (double)ceil_div(n, 256);
+      if (last) us += std::max((double)last * (bytes / s) / 5.4e6, bytes / s / 35e3);
+      if (s > 1) us += 3.0;
+      if (least == 0.0 || us < least) least = us, p.g.splits = s;
+    }
+  } else {
+    const int64_t keys = max_kv_len - std::min(max_kv_len, tq / batch) / 2;
+    p.g.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(512 / tiles, keys / 256), 32));
+  }
+  p.bytes = p.g.splits > 1 ? (size_t)p.g.splits * tq * hq * (hd * 4 + 8) : 0;
   return p;
 }
 
 template <int DB>
 hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.g.slots * a.hk * p.g.splits));
+  const dim3 grid((unsigned)((int64_t)p.g.slots * a.hk * p.g.splits));
   if (p.few) {
     constexpr int FW = few_waves(DB);
     const size_t bytes = std::max<size_t>((size_t)FW * 4 * FK * 64 * DB,
@@ -567,13 +637,14 @@ size_t attention_workspace(int64_t tq, int64_t batch, int hq, int hk, int hd, in
 hipError_t attention_launch(const AttnArgs& a, int64_t max_kv_len, void* ws, hipStream_t stream) {
   Plan p = plan_for(a.tq, a.batch, a.hq, a.hk, a.hd, max_kv_len);
   p.g.part = (float*)ws;
+  p.g.stat = (float2*)((float*)ws + (size_t)p.g.splits * a.tq * a.hq * a.hd);
   hipError_t e = a.hd <= 64    ? launch<2>(a, p, stream)
                  : a.hd <= 96  ? launch<3>(a, p, stream)
                  : a.hd <= 128 ? launch<4>(a, p, stream)
                  : a.hd <= 192 ? launch<6>(a, p, stream)
                                : launch<8>(a, p, stream);
   if (e != hipSuccess || p.g.splits == 1) return e;
-  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)ceil_div(a.tq * a.hq * (a.hd / 4), 256)),
+  hipLaunchKernelGGL(attention_join_kernel, dim3((unsigned)ceil_div(a.tq * a.hq, 4)),
                      dim3(256), 0, stream, a, p.g);
   return hipGetLastError();
 }
