@@ -695,16 +695,16 @@ def gptq_w4a16_linear(X: torch.Tensor, qweight: torch.Tensor, scales_f16: torch.
 
 
 def _heads(where: str, name: str, t: torch.Tensor, shape, dtypes, index: int):
-    """Checks an array of heads [rows, heads, hd] (None: any number) and returns its strides
-    between rows and heads, those that no second row or head uses as if it were dense."""
-    rows, heads, hd = t.shape if t.dim() == 3 else (-1, -1, -1)
-    if not (t.dim() == 3 and t.dtype in dtypes and t.get_device() == index
-            and all(b is None or a == b for a, b in zip((rows, heads, hd), shape))
-            and (t.stride(2) == 1 or hd == 1)):
+    """Checks an array of heads [rows, heads, hd] and returns its strides between rows and heads,
+    those that no second row or head uses as if it were dense."""
+    ld, hs, one = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if not (t.shape == shape and t.dtype in dtypes and t.get_device() == index
+            and (one == 1 or shape[2] == 1)):
         raise ValueError(f"{where}: {name} must be {list(shape)} of {dtypes} on GPU {index} with "
                          f"neighbouring columns, got {list(t.shape)} {t.dtype} of strides "
                          f"{t.stride()} on {t.device}")
-    return (t.stride(0) if rows > 1 else heads * hd), (t.stride(1) if heads > 1 else hd)
+    rows, heads, hd = shape
+    return ld if rows > 1 else heads * hd, hs if heads > 1 else hd
 
 
 def gptq_qk_norm_rope(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor | None = None, *,
@@ -720,57 +720,61 @@ def gptq_qk_norm_rope(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor | None =
     the tokens' keys and values go to; one outside writes nothing.  Returns (q_out, k_out, v_out
     or None)."""
     where = "gptq_qk_norm_rope"
-    if Q.dim() != 3 or not Q.is_cuda:
-        raise ValueError(f"{where}: Q must be [m, hq, hd] on a GPU")
+    if Q.dim() != 3 or not Q.is_cuda or Q.dtype not in _FLOATS or K.dim() != 3:
+        raise ValueError(f"{where}: Q and K must be [m, heads, hd] of {_FLOATS} on a GPU, got "
+                         f"{list(Q.shape)} {Q.dtype} on {Q.device} and {list(K.shape)}")
     index = Q.get_device()
     m, hq, hd = Q.shape
-    ldq, hsq = _heads(where, "Q", Q, (m, None, hd), _FLOATS, index)
-    ldk, hsk = _heads(where, "K", K, (m, None, hd), (Q.dtype,), index)
     hk = K.shape[1]
-    ldv = hsv = ldvo = hsvo = 0
+    x_type, out_type, like_k = (Q.dtype,), (torch.bfloat16,), (m, hk, hd)
+    ldq, hsq = _heads(where, "Q", Q, (m, hq, hd), x_type, index)
+    ldk, hsk = _heads(where, "K", K, like_k, x_type, index)
+    v_ptr = ldv = hsv = vo_ptr = ldvo = hsvo = 0
     if V is not None:
-        ldv, hsv = _heads(where, "V", V, (m, hk, hd), (Q.dtype,), index)
+        ldv, hsv = _heads(where, "V", V, like_k, x_type, index)
+        v_ptr = V.data_ptr()
     elif v_out is not None:
         raise ValueError(f"{where}: v_out without V")
-    rot = 0
+    rot = pos_ptr = freq_ptr = 0
+    if positions is not None:
+        _flat(where, "positions", positions, (m,), (torch.int32,), index)
+        pos_ptr = positions.data_ptr()
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         _flat(where, "inv_freq", inv_freq, (rot // 2,), (torch.float64,), index)
         if positions is None:
             raise ValueError(f"{where}: inv_freq without positions")
-    if positions is not None:
-        _flat(where, "positions", positions, (m,), (torch.int32,), index)
-    w_code = 0
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _flat(where, name, w, (hd,), _FLOATS, index)
-            w_code = _dtype_code(w)
-    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
-        raise ValueError(f"{where}: q_weight and k_weight must have one type")
-    bf16 = (torch.bfloat16,)
-    rows = m
+        freq_ptr = inv_freq.data_ptr()
+    qw_ptr = kw_ptr = w_code = 0
+    if q_weight is not None:
+        _flat(where, "q_weight", q_weight, (hd,), _FLOATS, index)
+        qw_ptr, w_code = q_weight.data_ptr(), _dtype_code(q_weight)
+    if k_weight is not None:
+        _flat(where, "k_weight", k_weight, (hd,), _FLOATS, index)
+        kw_ptr, w_code = k_weight.data_ptr(), _dtype_code(k_weight)
+        if qw_ptr and q_weight.dtype is not k_weight.dtype:
+            raise ValueError(f"{where}: q_weight and k_weight must have one type")
+    rows, slot_ptr = m, 0
     if slots is not None:
         _flat(where, "slots", slots, (m,), (torch.int64,), index)
-        if k_out is None or (V is not None and v_out is None):
+        if k_out is None or (v_ptr and v_out is None):
             raise ValueError(f"{where}: slots need k_out (and v_out with V)")
-        rows = k_out.shape[0]
+        rows, slot_ptr = k_out.shape[0], slots.data_ptr()
     if q_out is None:
         q_out = _empty(stream, (m, hq, hd), dtype=torch.bfloat16, device=Q.device)
     if k_out is None:
-        k_out = _empty(stream, (m, hk, hd), dtype=torch.bfloat16, device=Q.device)
-    if V is not None and v_out is None:
-        v_out = _empty(stream, (m, hk, hd), dtype=torch.bfloat16, device=Q.device)
-    ldqo, hsqo = _heads(where, "q_out", q_out, (m, hq, hd), bf16, index)
-    ldko, hsko = _heads(where, "k_out", k_out, (rows, hk, hd), bf16, index)
+        k_out = _empty(stream, like_k, dtype=torch.bfloat16, device=Q.device)
+    ldqo, hsqo = _heads(where, "q_out", q_out, (m, hq, hd), out_type, index)
+    ldko, hsko = _heads(where, "k_out", k_out, (rows, hk, hd), out_type, index)
     if V is not None:
-        ldvo, hsvo = _heads(where, "v_out", v_out, (rows, hk, hd), bf16, index)
+        if v_out is None:
+            v_out = _empty(stream, like_k, dtype=torch.bfloat16, device=Q.device)
+        ldvo, hsvo = _heads(where, "v_out", v_out, (rows, hk, hd), out_type, index)
+        vo_ptr = v_out.data_ptr()
     _call(where, index, lib().gptq_qk_norm_rope, Q.data_ptr(), ldq, hsq, K.data_ptr(), ldk, hsk,
-          None if V is None else V.data_ptr(), ldv, hsv, _dtype_code(Q), m, hq, hk, hd,
-          positions.data_ptr() if rot else None, inv_freq.data_ptr() if rot else None, rot,
-          1 if interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
-          None if k_weight is None else k_weight.data_ptr(), w_code, float(eps),
-          None if slots is None else slots.data_ptr(), rows, q_out.data_ptr(), ldqo, hsqo,
-          k_out.data_ptr(), ldko, hsko, None if V is None else v_out.data_ptr(), ldvo, hsvo,
+          v_ptr, ldv, hsv, _dtype_code(Q), m, hq, hk, hd, pos_ptr, freq_ptr, rot,
+          1 if interleaved else 0, qw_ptr, kw_ptr, w_code, float(eps), slot_ptr, rows,
+          q_out.data_ptr(), ldqo, hsqo, k_out.data_ptr(), ldko, hsko, vo_ptr, ldvo, hsvo,
           _raw_stream(where, index, stream))
     return q_out, k_out, v_out
 
@@ -793,35 +797,37 @@ def gptq_attention(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, *, cu_q: t
     max_kv_len: the longest kv_len where the caller knows it (only for speed; by default the rows
     of K).  Rows of out outside all sequences are left as they were."""
     where = "gptq_attention"
-    if Q.dim() != 3 or not Q.is_cuda:
-        raise ValueError(f"{where}: Q must be [total_q, hq, hd] on a GPU")
+    if Q.dim() != 3 or not Q.is_cuda or K.dim() != 3:
+        raise ValueError(f"{where}: Q and K must be [rows, heads, hd] on a GPU, got {list(Q.shape)} "
+                         f"on {Q.device} and {list(K.shape)}")
     index = Q.get_device()
-    tq, hq, hd = Q.shape
-    bf16 = (torch.bfloat16,)
-    ldq, hsq = _heads(where, "Q", Q, (tq, hq, hd), bf16, index)
-    ldk, hsk = _heads(where, "K", K, (None, None, hd), bf16, index)
+    like_q = tq, hq, hd = Q.shape
     rows, hk, _ = K.shape
-    ldv, hsv = _heads(where, "V", V, (rows, hk, hd), bf16, index)
-    batch = cu_q.shape[0] - 1 if cu_q.dim() == 1 else -1
+    bf16, like_k = (torch.bfloat16,), (rows, hk, hd)
+    ldq, hsq = _heads(where, "Q", Q, like_q, bf16, index)
+    ldk, hsk = _heads(where, "K", K, like_k, bf16, index)
+    ldv, hsv = _heads(where, "V", V, like_k, bf16, index)
+    batch = cu_q.numel() - 1
     if batch < 0:
         raise ValueError(f"{where}: cu_q must be [batch + 1]")
     _flat(where, "cu_q", cu_q, (batch + 1,), (torch.int32,), index)
+    start_ptr = len_ptr = 0
     if (kv_start is None) != (kv_len is None):
         raise ValueError(f"{where}: kv_start and kv_len belong together")
     if kv_start is not None:
         _flat(where, "kv_start", kv_start, (batch,), (torch.int64,), index)
         _flat(where, "kv_len", kv_len, (batch,), (torch.int32,), index)
+        start_ptr, len_ptr = kv_start.data_ptr(), kv_len.data_ptr()
     elif rows != tq:
         raise ValueError(f"{where}: without kv_start K and V have the queries' rows, {tq}, got {rows}")
     if out is None:
         out = _empty(stream, (tq, hq, hd), dtype=torch.bfloat16, device=Q.device)
-    ldo, hso = _heads(where, "out", out, (tq, hq, hd), bf16, index)
+    ldo, hso = _heads(where, "out", out, like_q, bf16, index)
     longest = rows if max_kv_len is None else min(int(max_kv_len), rows)
     ws = _scratch(where, ws, gptq_attention_workspace(tq, batch, hq, hk, hd, longest), Q, stream)
     _call(where, index, lib().gptq_attention, Q.data_ptr(), ldq, hsq, K.data_ptr(), ldk, hsk,
-          V.data_ptr(), ldv, hsv, tq, rows, batch, hq, hk, hd, cu_q.data_ptr(),
-          None if kv_start is None else kv_start.data_ptr(),
-          None if kv_len is None else kv_len.data_ptr(), longest, 1 if causal else 0,
+          V.data_ptr(), ldv, hsv, tq, rows, batch, hq, hk, hd, cu_q.data_ptr(), start_ptr, len_ptr,
+          longest, 1 if causal else 0,
           hd ** -0.5 if scale is None else float(scale), out.data_ptr(), ldo, hso, *_span(ws),
           _raw_stream(where, index, stream))
     return out
