@@ -60,6 +60,7 @@ struct VecArgs {
   int m, n, k, ng;
   int vec;              // scales (and zeros) that one aligned load may take: 1, 2, 4 or 8
   int splits, per_split;  // of the row's blocks of 512 k over workgroups
+  int slots;              // k slots of a workgroup, at most
 };
 
 // How the sums leave: as they are (times sx), or finished by an epilogue.  Gated,
@@ -588,7 +589,8 @@ inline hipError_t join_launch(const float* part, const float* sx, int64_t m, int
 template <bool I8, int NT, int R, int G, int RS, class E>
 hipError_t vec_launch_one(const VecArgs& a, const E& e, hipStream_t stream) {
   typedef Shape<I8, NT, R, G, RS> S;
-  const int slots = std::min(S::SLOTS, a.per_split);  // no more than there are blocks
+  // no more waves than there are blocks
+  const int slots = std::min(std::min(S::SLOTS, a.per_split), a.slots);
   hipLaunchKernelGGL((w4_vec_kernel<I8, NT, R, G, RS, E>),
                      dim3((unsigned)ceil_div(a.n, 16 * R * RS), a.splits), dim3(64 * RS * slots),
                      group_bytes(I8, NT, R, G, RS, slots), stream, a, e);
@@ -614,6 +616,7 @@ struct VecPlan {
   int r;   // tiles of 16 weight rows per wave
   int rs;  // waves that share the tokens' buffers
   int splits, per_split;
+  int slots;
   size_t ws_bytes;
 };
 
@@ -630,9 +633,15 @@ struct VecPlan {
 // 1024 x 8192 12.1 us in four splits and 24.5 in one; through 11008 x 4096 23 us
 // and 25 with sharing waves, through 8192 x 8192 32 and 29.5, through 16384 x
 // 12288 98 and 67.
-// (A gated product's row tiles come in pairs: r is even.)
-inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G, bool gated = false) {
-  VecPlan p = {gated ? 2 : 1, 1, 1, 1, 0};
+// With an epilogue (`finished`; gated, row tiles come in pairs and r is even) joining
+// splits costs more, and up to 16 tokens of layers past one round of workgroups take
+// 32 rows and four k slots each, so that several share a CU and one loads while
+// another multiplies: 16 tokens through 22016 x 4096, groups of 64: 17.8 us, with 64
+// rows and eight slots 21; 8 tokens 16.2 and 18.9; 57344 x 8192 64 and 71 us (12288 x
+// 4096, one round of 48 rows and eight slots: 8.2 us, in 32 and four 11.1).
+inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G, bool finished = false,
+                        bool gated = false) {
+  VecPlan p = {gated ? 2 : 1, 1, 1, 1, 8, 0};
   const int nt = (int)ceil_div(m, 16), nblk = (int)ceil_div(k, KBLK);
   double least = 0.0;
   for (int rs = 1; rs <= SHARE; rs += SHARE - 1)
@@ -649,13 +658,15 @@ inline VecPlan vec_plan(bool i8, int64_t m, int64_t n, int64_t k, int G, bool ga
         double us = rounds * 0.27 * (2 + r) * (1.0 + 0.35 * (nt - 1)) * steps;
         if (rs > 1) us = 6.0 + us * (G == 32 ? 1.4 : G == 64 ? 1.25 : 1.0);
         if (!several) us += 2.0 * (rounds - 1.0);  // a round's start and end
-        if (s > 1) us += 2.5 + 1e-6 * (double)(m * n) * (s + 1);
+        if (s > 1) us += (finished ? 6.5 : 2.5) + 1e-6 * (double)(m * n) * (s + 1);
         if (least == 0.0 || us < least) {
           least = us;
           p.r = r, p.rs = rs, p.per_split = per, p.splits = (int)ceil_div(nblk, per);
         }
         if (per <= waves) break;  // a wave has one block: no fewer steps
       }
+  if (finished && nt == 1 && n > 12288)
+    p.r = 2, p.rs = 1, p.splits = 1, p.per_split = nblk, p.slots = 4;
   p.ws_bytes = p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0;
   return p;
 }
@@ -684,7 +695,7 @@ template <bool I8, class E>
 hipError_t vec_launch_parts(VecArgs a, const VecPlan& p, int G, void* ws, const E& e,
                             hipStream_t stream) {
   if (p.splits > 1) a.y = (float*)ws;
-  a.splits = p.splits, a.per_split = p.per_split;
+  a.splits = p.splits, a.per_split = p.per_split, a.slots = p.slots;
   return a.m <= 16   ? vec_launch_t<I8, 1>(a, p.r, p.rs, G, e, stream)
          : a.m <= 32 ? vec_launch_t<I8, 2>(a, p.r, p.rs, G, e, stream)
          : a.m <= 48 ? vec_launch_t<I8, 3>(a, p.r, p.rs, G, e, stream)
@@ -703,7 +714,7 @@ hipError_t vec_launch(const VecArgs& a, int G, void* ws, hipStream_t stream) {
 template <bool I8, bool GATED>
 hipError_t vec_finish_launch(const VecArgs& a, int G, void* ws, const Epilogue& epi,
                              hipStream_t stream) {
-  const VecPlan p = vec_plan(I8, a.m, a.n, a.k, G, GATED);
+  const VecPlan p = vec_plan(I8, a.m, a.n, a.k, G, true, GATED);
   const hipError_t e = vec_launch_parts<I8>(a, p, G, ws, Finished<GATED>{epi}, stream);
   if (e != hipSuccess || p.splits == 1) return e;
   return join_finish_launch<GATED>((const float*)ws, a.m, a.n, p.splits, epi, stream);
