@@ -46,14 +46,14 @@ __device__ __forceinline__ void finish(const Epilogue& e, int64_t row, int64_t u
     ((__bf16*)e.y)[row * e.ldy + u] = (__bf16)y;
 }
 
-// Up to four neighbouring outputs of a row, n of which are there.
-template <bool GATED>
+// Up to four outputs of a row, STEP columns apart, n of which are there.
+template <bool GATED, int STEP = 1>
 __device__ __forceinline__ void finish4(const Epilogue& e, int64_t row, int64_t u, int n, float v0[4],
                                         float v1[4]) {
   if (e.bias) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t c = u + min(i, n - 1);
+      const int64_t c = u + STEP * min(i, n - 1);
       v0[i] += load_as_float(e.bias, c, e.bias_f32);
       if constexpr (GATED) v1[i] += load_as_float(e.bias, e.F + c, e.bias_f32);
     }
@@ -62,7 +62,7 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t row, int64_t 
   if (e.res) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      res[i] = load_as_float(e.res, row * e.ldr + u + min(i, n - 1), e.res_f32);
+      res[i] = load_as_float(e.res, row * e.ldr + u + STEP * min(i, n - 1), e.res_f32);
   }
   if (e.act != ACT_NONE) {
 #pragma unroll 1
@@ -77,7 +77,7 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t row, int64_t 
     v0[i] += res[i];
   }
   const int64_t at = row * e.ldy + u;
-  if (e.vec4 && n == 4) {
+  if (STEP == 1 && e.vec4 && n == 4) {
     if (e.y_f32) {
       *(float4*)((float*)e.y + at) = make_float4(v0[0], v0[1], v0[2], v0[3]);
     } else {
@@ -91,40 +91,35 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t row, int64_t 
   for (int i = 0; i < 4; ++i) {
     if (i >= n) break;
     if (e.y_f32)
-      ((float*)e.y)[at + i] = v0[i];
+      ((float*)e.y)[at + STEP * i] = v0[i];
     else
-      ((__bf16*)e.y)[at + i] = (__bf16)v0[i];
+      ((__bf16*)e.y)[at + STEP * i] = (__bf16)v0[i];
   }
 }
 
-// The splits' sums [splits][m][n] added in split order, then finished: four
-// neighbouring columns per thread, four splits' loads at a time.
+// The splits' sums [splits][m][n] added in split order, then finished: a wave takes
+// 256 columns of a row, a lane four of them 64 apart, so that every load and store
+// is of neighbours whatever n's alignment; four splits' loads are in flight at a time.
 template <bool GATED>
 __global__ __launch_bounds__(256) void join_finish_kernel(const float* __restrict__ part, int64_t m,
                                                           int n, int splits, Epilogue e) {
-  const int per = (e.F + 3) / 4;
-  const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (t >= m * per) return;
-  const int64_t row = t / per;
-  const int u = 4 * (int)(t - row * per), cols = min(4, e.F - u);
+  const int chunks = (e.F + 255) / 256;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), row = t / chunks;
+  const int u = 256 * (int)(t - row * chunks) + (threadIdx.x & 63);
+  const int cols = min(4, (e.F - u + 63) / 64);
+  if (row >= m || cols <= 0) return;
   const float* p = part + row * n + u;
   const int64_t next = m * n;
-  const bool whole = cols == 4 && n % 4 == 0 && e.F % 4 == 0;  // aligned
   float v0[4] = {}, v1[4] = {};
   for (int s = 0; s < splits; s += 4) {
     float a[4][4], b[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float* q = p + min(s + i, splits - 1) * next;
-      if (whole) {
-        *(float4*)a[i] = *(const float4*)q;
-        if constexpr (GATED) *(float4*)b[i] = *(const float4*)(q + e.F);
-      } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          a[i][k] = q[min(k, cols - 1)];
-          if constexpr (GATED) b[i][k] = q[e.F + min(k, cols - 1)];
-        }
+      for (int k = 0; k < 4; ++k) {
+        a[i][k] = q[64 * min(k, cols - 1)];
+        if constexpr (GATED) b[i][k] = q[e.F + 64 * min(k, cols - 1)];
       }
     }
 #pragma unroll
@@ -137,13 +132,13 @@ __global__ __launch_bounds__(256) void join_finish_kernel(const float* __restric
       }
     }
   }
-  finish4<GATED>(e, row, u, cols, v0, v1);
+  finish4<GATED, 64>(e, row, u, cols, v0, v1);
 }
 
 template <bool GATED>
 hipError_t join_finish_launch(const float* part, int64_t m, int n, int splits, const Epilogue& e,
                               hipStream_t stream) {
-  hipLaunchKernelGGL((join_finish_kernel<GATED>), dim3((unsigned)ceil_div(m * ((e.F + 3) / 4), 256)),
+  hipLaunchKernelGGL((join_finish_kernel<GATED>), dim3((unsigned)ceil_div(m * ((e.F + 255) / 256), 4)),
                      dim3(256), 0, stream, part, m, n, splits, e);
   return hipGetLastError();
 }

@@ -158,6 +158,12 @@ struct Shape {
   static_assert(BUFS >= 2 && BUFS * STAGE <= LDS_BYTES, "two buffers");
 };
 
+// A barrier for LDS alone: __syncthreads() also waits for the stores that are out,
+// 1 us for every 32 rows that leave.
+__device__ __forceinline__ void lds_barrier() {
+  __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
 // Four waves side by side, each all 32 MI rows of X by 32 weight rows: a wave
 // takes the codes of its own weight rows apart, and none twice.  G: group size,
 // 0 for one group per row.
@@ -428,9 +434,9 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
   const int col = 4 * (threadIdx.x % TPR);
   const int lcol = GATED ? 64 * (col >> 5) + (col & 31) : col;
   const int ncol = (int)min((int64_t)4, F - (u0 + col));  // of these columns, those that are there
+  __syncthreads();
 #pragma unroll 1
   for (int mi = 0; mi < MI; ++mi) {
-    __syncthreads();
 #pragma unroll
     for (int j = 0; j < MI; ++j) {
       if (j != mi) continue;
@@ -441,7 +447,25 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
           sums[(8 * (i >> 2) + 4 * h + (i & 3)) * TN + 32 * (NI * wave + ni) + l32] =
               tot[j * NI + ni][i];
     }
-    __syncthreads();
+    lds_barrier();
+    if (a.part) {
+      // columns a thread apart, so that stores are of neighbours whatever N's alignment
+#pragma unroll
+      for (int r = 0; r < 32; r += 256 / TPR) {
+        const int rt = r + (int)threadIdx.x / TPR;
+        const int64_t row = m0 + 32 * mi + rt;
+        float* const o = a.part + ((int64_t)split * a.M + row) * a.N + u0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = (int)(threadIdx.x % TPR) + TPR * i, l = GATED ? 64 * (k >> 5) + (k & 31) : k;
+          if (row >= a.M || k >= F - u0) continue;
+          o[k] = sums[rt * TN + l];
+          if constexpr (GATED) o[F + k] = sums[rt * TN + l + 32];
+        }
+      }
+      lds_barrier();
+      continue;
+    }
 #pragma unroll 1
     for (int r = threadIdx.x / TPR; r < 32; r += 256 / TPR) {
       const int64_t row = m0 + 32 * mi + r;
@@ -452,18 +476,9 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
         const float4 q = *(const float4*)(sums + r * TN + lcol + 32);
         v1[0] = q.x, v1[1] = q.y, v1[2] = q.z, v1[3] = q.w;
       }
-      if (a.part) {
-        float* o = a.part + ((int64_t)split * a.M + row) * a.N + u0 + col;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < ncol) {
-            o[i] = v0[i];
-            if constexpr (GATED) o[F + i] = v1[i];
-          }
-      } else {
-        finish4<GATED>(a.e, row, u0 + col, ncol, v0, v1);
-      }
+      finish4<GATED>(a.e, row, u0 + col, ncol, v0, v1);
     }
+    lds_barrier();
   }
 }
 
