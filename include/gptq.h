@@ -415,7 +415,7 @@ size_t gptq_w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_siz
  * X           [m x ldx] bf16, row-major; 16-byte aligned, ldx a multiple of 8, at
  *             most 2^23 (GPTQ_EUNSUPPORTED past it).
  * qweight, scales_f16, zeros_f16, group_size, sym: as gptq_w4a16_matvec.  Zeros
- *             are whole numbers, as gptq_pack writes them.
+ *             are whole numbers 0 .. 15, as gptq_pack writes them.
  * bias        [d_out] of bias_dtype (bf16 or float32), or NULL: none.
  * activation  a gptq_activation; GELU is v/2 (1 + erf(v / sqrt 2)),
  *             GELU_TANH v/2 (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))).
@@ -467,6 +467,8 @@ size_t gptq_w4a16_linear_workspace(int64_t m, int64_t d_out, int64_t d_in, int g
  *             t ld + h hs + d, for all arrays here: ld* between tokens and hs*
  *             between heads, in elements, both multiples of 16 bytes, ld < 2^23.
  *             hq heads of Q, hk of K and V.  V (with V_out) may be NULL.
+ * m           0 (no-op) .. 2^30, and m (16 (hq + 2 hk) + 64) below 2^32
+ *             (GPTQ_EUNSUPPORTED past it).
  * hd          a multiple of 8, <= 256; rot_dim a multiple of 16, 0 .. hd
  *             (0: positions and inv_freq may be NULL).
  * positions   [m] int32, any value.
@@ -476,8 +478,8 @@ size_t gptq_w4a16_linear_workspace(int64_t m, int64_t d_out, int64_t d_in, int g
  *             and V_out; a slot outside 0 .. kv_rows-1 writes nothing (padding).
  *             Two tokens of one call with the same slot leave either's values,
  *             not always one token's whole row.  NULL: row t.
- * kv_rows     rows of K_out and V_out.  Rows that no slot names are left as they
- *             were.
+ * kv_rows     rows of K_out and V_out, at most 2^38 (for attention's K and V too).
+ *             Rows that no slot names are left as they were.
  * Q_out, K_out, V_out  bf16 out; no two of an output's values may share a place.
  *             Q_out may be Q, and without slots K_out may be K and V_out V (bf16,
  *             the same strides); no other overlap is allowed.
@@ -515,7 +517,7 @@ int gptq_qk_norm_rope(const void* Q, int64_t ldq, int64_t hsq, const void* K, in
  * max_kv_len  the longest kv_len as the caller knows it: it decides how keys are
  *             split over workgroups, and with it only speed and the order of sums;
  *             longer sequences are computed all the same.
- * hd          a multiple of 8, <= 256.  scale > 0.
+ * hd          a multiple of 8, <= 256.  1e-30 <= scale < 1e30.
  * ws          gptq_attention_workspace(...) bytes (0 where keys are not split);
  *             its contents on entry do not matter; calls in flight together need
  *             one each.
@@ -523,7 +525,7 @@ int gptq_qk_norm_rope(const void* Q, int64_t ldq, int64_t hsq, const void* K, in
  * to a maximum that the row's own exceeds by less than a factor of 2^8, and their
  * sum is that of the rounded values.  The order of every sum is fixed.  Keys and
  * values that a query does not see do not reach it, whatever they hold.
- * total_q * hq / 32 + batch * hk is bounded by 2^25 (GPTQ_EUNSUPPORTED past it).
+ * total_q * hq / 32 + batch * hk is bounded by 2^23 (GPTQ_EUNSUPPORTED past it).
  * ------------------------------------------------------------------------- */
 int gptq_attention(const void* Q, int64_t ldq, int64_t hsq, const void* K, int64_t ldk, int64_t hsk,
                    const void* V, int64_t ldv, int64_t hsv, int64_t total_q, int64_t kv_rows,

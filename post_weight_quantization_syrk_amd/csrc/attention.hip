@@ -598,7 +598,7 @@ Plan plan_for(int64_t tq, int64_t batch, int hq, int hk, int hd, int64_t max_kv_
   if (p.few) {
     const double bytes = 4.0 * (double)max_kv_len * hd;  // of a sequence and key head
     double least = 0.0;
-    for (int s = 1; s <= 32 && (s == 1 || s * 128 <= max_kv_len); ++s) {
+    for (int s = 1; s <= 32 && (s == 1 || (s * 128 <= max_kv_len && tiles * s <= 1 << 16)); ++s) {
       const int64_t n = tiles * s, full = n / 256, last = n % 256;
       double us = (double)full * 256 * (bytes / s) / 5.4e6 + 4.0 * (double)ceil_div(n, 256);
       if (last) us += std::max((double)last * (bytes / s) / 5.4e6, bytes / s / 35e3);

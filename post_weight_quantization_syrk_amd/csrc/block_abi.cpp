@@ -22,6 +22,7 @@ bool float_type(int t) { return t == GPTQ_BF16 || t == GPTQ_F32; }
 size_t type_size(int t) { return t == GPTQ_F32 ? 4 : 2; }
 
 constexpr int64_t MOST = 1 << 30;
+constexpr int64_t MOST_ROWS = (int64_t)1 << 38;  // of a cache: places fit 64 bits
 
 int check_linear(int64_t m, int64_t d_out, int64_t d_in, int group_size, int gated) {
   if (m < 0 || m > MOST || d_out <= 0 || d_out > MOST || d_in <= 0 || d_in > 65536)
@@ -58,8 +59,8 @@ int check_attention(int64_t tq, int64_t batch, int64_t hq, int64_t hk, int64_t h
     return GPTQ_EINVAL;
   if (hq % hk != 0) return GPTQ_EINVAL;
   if (hq > 65536 || hd % 8 != 0 || hd > 256) return GPTQ_EUNSUPPORTED;
-  // workgroups of one launch
-  if ((tq * (hq / hk) / 32 + batch) * hk > (MOST >> 5)) return GPTQ_EUNSUPPORTED;
+  // threads of one launch are below 2^32
+  if ((tq * (hq / hk) / 32 + batch) * hk > 1 << 23) return GPTQ_EUNSUPPORTED;
   return GPTQ_OK;
 }
 
@@ -118,15 +119,17 @@ int gptq_qk_norm_rope(const void* Q, int64_t ldq, int64_t hsq, const void* K, in
                       int64_t ldqo, int64_t hsqo, void* K_out, int64_t ldko, int64_t hsko,
                       void* V_out, int64_t ldvo, int64_t hsvo, gptq_stream stream) {
   if (m < 0 || m > MOST || hq <= 0 || hk <= 0 || hd <= 0 || rot_dim < 0 || rot_dim > hd ||
-      rot_dim % 2 != 0 || kv_rows < 0)
+      rot_dim % 2 != 0 || kv_rows < 0 || kv_rows > MOST_ROWS)
     return GPTQ_EINVAL;
   if (!float_type(x_dtype) || (interleaved != 0 && interleaved != 1)) return GPTQ_EINVAL;
   if ((q_weight || k_weight) && (!float_type(w_dtype) || !(eps >= 0.0) || !(eps < 1e30)))
     return GPTQ_EINVAL;
   if (hd % 8 != 0 || hd > 256 || rot_dim % 16 != 0 || hq > 65536 || hk > 65536)
     return GPTQ_EUNSUPPORTED;
-  if (!V != !V_out) return GPTQ_EINVAL;
+  // threads of one launch are below 2^32
+  if (m * (16 * ((int64_t)hq + 2 * hk) + 64) >> 32) return GPTQ_EUNSUPPORTED;
   if (m == 0) return GPTQ_OK;
+  if (!V != !V_out) return GPTQ_EINVAL;
   if (!Q || !K || !Q_out || !K_out) return GPTQ_EINVAL;
   if (rot_dim && (!positions || !inv_freq || !aligned(positions, 4) || !aligned(inv_freq, 8)))
     return GPTQ_EINVAL;
@@ -174,8 +177,9 @@ int gptq_attention(const void* Q, int64_t ldq, int64_t hsq, const void* K, int64
                    gptq_stream stream) {
   int st = check_attention(total_q, batch, hq, hk, hd);
   if (st != GPTQ_OK) return st;
-  if (kv_rows < 0 || max_kv_len < 0 || (causal != 0 && causal != 1)) return GPTQ_EINVAL;
-  if (!(scale > 0.0) || !(scale < 1e30)) return GPTQ_EINVAL;
+  if (kv_rows < 0 || kv_rows > MOST_ROWS || max_kv_len < 0 || (causal != 0 && causal != 1)) return GPTQ_EINVAL;
+  // (a scale that is 0 in float32 would turn the masked scores' infinities into NaN)
+  if (!(scale >= 1e-30) || !(scale < 1e30)) return GPTQ_EINVAL;
   if (!kv_start != !kv_len) return GPTQ_EINVAL;
   if (total_q == 0 || batch == 0) return GPTQ_OK;
   if (!Q || !out || !cu_q || (kv_rows > 0 && (!K || !V))) return GPTQ_EINVAL;

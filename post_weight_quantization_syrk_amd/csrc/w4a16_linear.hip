@@ -537,7 +537,9 @@ Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size, bool gated
   const bool g32 = group_size == 32;
   Plan p = {};
   double best = 0.0;
-  for (int wide = 0; wide < 2; ++wide) {
+  // (a launch's threads are below 2^32)
+  const bool may_widen = ceil_div(cols, 256) * 256 * (4 * nch) < (int64_t)1 << 31;
+  for (int wide = 0; wide < 1 + may_widen; ++wide) {
     const int64_t tiles_n = ceil_div(cols, tile_n(wide));
     int64_t before = 0;
     for (int b = most_m(wide); b >= 1; --b) {

@@ -97,6 +97,8 @@ ROPE = [
     (dict(ldqo=504), EINVAL), (dict(hsqo=56), EINVAL), (dict(ldko=0), EINVAL), (dict(hsvo=0), EINVAL),
     (dict(ldqo=64, hsqo=248), EINVAL), (dict(slots=A, rows=9, ldko=64, hsko=256), EINVAL),
     (dict(m=0), OK), (dict(m=0, Q=None, Ko=None), OK),
+    (dict(m=0, V=None), OK),                          # no tokens, with a cache to write to
+    (dict(slots=A, rows=(1 << 38) + 1), EINVAL), (dict(m=1 << 29, rows=1 << 29), EUNSUP),
 ]
 
 
@@ -119,7 +121,8 @@ ATTENTION = [
     (dict(hq=65540), EUNSUP), (dict(hd=60), EUNSUP), (dict(hd=264), EUNSUP),
     (dict(batch=1 << 24), EUNSUP), (dict(tq=1 << 29), EUNSUP),
     (dict(causal=2), EINVAL), (dict(scale=0.0), EINVAL), (dict(scale=-1.0), EINVAL),
-    (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL),
+    (dict(scale=float("nan")), EINVAL), (dict(scale=float("inf")), EINVAL), (dict(scale=1e-46), EINVAL),
+    (dict(rows=(1 << 38) + 1), EINVAL), (dict(batch=1 << 21), EUNSUP), (dict(tq=1 << 26, hq=64), EUNSUP),
     (dict(start=None), EINVAL), (dict(len=None), EINVAL),
     (dict(Q=None), EINVAL), (dict(K=None), EINVAL), (dict(V=None), EINVAL), (dict(out=None), EINVAL),
     (dict(cu=None), EINVAL), (dict(Q=A + 8), EINVAL), (dict(K=A + 2), EINVAL), (dict(V=A + 4), EINVAL),

@@ -166,6 +166,15 @@ def test_empty_rows_and_zero_heads():
     assert torch.equal(q, good)
 
 
+def test_no_tokens_leave_the_cache():
+    c = Case(2, 2, 1, 64, 64, seed=11)
+    cache = torch.full((2, 5, 1, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    none = torch.zeros(0, dtype=torch.int64, device=DEV)
+    e = gptq.gptq_qk_norm_rope(c.q[:0].clone(), c.k[:0].clone(), c.v[:0].clone(), positions=none.int(),
+                               inv_freq=c.freq_d, slots=none, k_out=cache[0], v_out=cache[1])
+    assert e[0].shape == (0, 2, 64) and bool((cache == 5.0).all())
+
+
 @pytest.mark.parametrize("m", [1, 300])
 def test_captured_and_replayed(m):
     c = Case(m, 8, 2, 128, 128, x="f32", seed=8)
