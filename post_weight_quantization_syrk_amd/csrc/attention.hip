@@ -488,42 +488,60 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
     const char* const t = mine + buf * 2 * TILE;
     tile_step<DB, FK / 32>(w, t, t + TILE, c, lim - key0, lim_first < key0 + FK - 1);
   }
-  float l = w.l + other_half(w.l);
-  // the waves' sums, brought to one maximum, by way of LDS
-  __syncthreads();
-  float* const stat = (float*)lds;  // [FW][2][32]
-  if (h == 0) stat[wave * 64 + l32] = w.mc, stat[wave * 64 + 32 + l32] = l;
-  __syncthreads();
-  float mc = NO_MAX, sum = 0.0f;
+  const float l = w.l + other_half(w.l);
+  // The waves' sums meet in LDS, where a thread takes four columns of a row: rows
+  // that are not there (28 of 32 for a token of four heads) cost nothing.
+  constexpr int PITCH = 32 * DB + 4;
+  static_assert(FW * 256 + 128 + FW * FM * PITCH * 4 <= FW * 4 * TILE, "in the tiles' place");
+  float2* const stat = (float2*)lds;                             // [FW][32]
+  int* const bad = (int*)(lds + FW * 256);                       // [32]
+  float* const parts = (float*)(lds + FW * 256 + 128);           // [FW][32][PITCH]
+  const int live = min(FM, p.rows - p.row0);
+  __syncthreads();  // the tiles are read
+  if (l32 < live) {
+    if (h == 0) stat[wave * FM + l32] = make_float2(w.mc, l);
+    float* const mine = parts + (wave * FM + l32) * PITCH + 4 * h;
 #pragma unroll
-  for (int i = 0; i < FW; ++i) mc = fmaxf(mc, stat[i * 64 + l32]);
+    for (int b = 0; b < DB; ++b)
 #pragma unroll
-  for (int i = 0; i < FW; ++i) sum += stat[i * 64 + 32 + l32] * exp2_of(stat[i * 64 + l32] - mc);
-  const float f = exp2_of(w.mc - mc);
-  float* const parts = (float*)lds + FW * 64;
-  constexpr int PER = DB * 16 * 64;
-#pragma unroll
-  for (int from = 1; from < FW; ++from) {
-    if (wave == from) {
-#pragma unroll
-      for (int b = 0; b < DB; ++b)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) parts[(from - 1) * PER + (16 * b + i) * 64 + lane] = w.o[b][i] * f;
-    }
+      for (int i = 0; i < 16; i += 4)
+        *(float4*)(mine + 32 * b + 2 * i) = make_float4(w.o[b][i], w.o[b][i + 1], w.o[b][i + 2], w.o[b][i + 3]);
   }
+  if (threadIdx.x < FM) bad[threadIdx.x] = 0;
   __syncthreads();
-  if (wave != 0) return;
+  const int per = a.hd / 4;
+  for (int at = threadIdx.x; at < live * per; at += 64 * FW) {
+    const int r = (int)((uint32_t)at / (uint32_t)per), d = 4 * (at - r * per);
+    float mc = NO_MAX, sum = 0.0f, o[4] = {};
 #pragma unroll
-  for (int b = 0; b < DB; ++b)
+    for (int i = 0; i < FW; ++i) mc = fmaxf(mc, stat[i * FM + r].x);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = w.o[b][i] * f;
-#pragma unroll
-      for (int from = 1; from < FW; ++from) v += parts[(from - 1) * PER + (16 * b + i) * 64 + lane];
-      w.o[b][i] = v;
+    for (int i = 0; i < FW; ++i) {
+      const float2 st = stat[i * FM + r];
+      const float4 v = *(const float4*)(parts + (i * FM + r) * PITCH + d);
+      const float f = exp2_of(st.x - mc);
+      sum = fmaf(st.y, f, sum);
+      o[0] = fmaf(v.x, f, o[0]), o[1] = fmaf(v.y, f, o[1]);
+      o[2] = fmaf(v.z, f, o[2]), o[3] = fmaf(v.w, f, o[3]);
     }
-  leave<DB>(a, g, p, group, kvh, p.row0 + l32 < p.rows, query, head, lim, split, begin, end, c, w.o, mc, sum,
-            lds);
+    const float odd = fmaf(o[0], 0.0f, fmaf(o[1], 0.0f, fmaf(o[2], 0.0f, fmaf(o[3], 0.0f, sum * 0.0f))));
+    if (odd != 0.0f) bad[r] = 1;
+    const int at_row = p.row0 + r, at_query = (int)((uint32_t)at_row / (uint32_t)group);
+    store4(a, g, split, p.q0 + at_query, kvh * group + at_row - at_query * group, d, o, mc, sum,
+           sum > 0.0f ? 1.0f / sum : sum);
+  }
+  if (!a.causal) return;
+  __syncthreads();
+  for (int r = wave; r < live; r += FW) {
+    const int at_row = p.row0 + r, at_query = (int)((uint32_t)at_row / (uint32_t)group);
+    const int last = min(at_query + back, p.lk - 1);
+    if (!bad[r] || last >= p.lk - 1) continue;
+    const int64_t qi = p.q0 + at_query;
+    const int hr = kvh * group + at_row - at_query * group;
+    const Slow t = slow_row(a.q + qi * a.ldq + hr * a.hsq, a.k + p.start * a.ldk + kvh * a.hsk, a.ldk,
+                            a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd, begin, min(end, last + 1), c);
+    store4(a, g, split, qi, hr, 4 * lane, t.o, t.mc, t.l, t.l > 0.0f ? 1.0f / t.l : t.l);
+  }
 }
 
 // The splits' parts of a row, joined by a wave: lane s has split s's maximum and
@@ -618,9 +636,8 @@ hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.g.slots * a.hk * p.g.splits));
   if (p.few) {
     constexpr int FW = few_waves(DB);
-    const size_t bytes = std::max<size_t>((size_t)FW * 4 * FK * 64 * DB,
-                                          FW * 256 + (FW - 1) * DB * 16 * 64 * 4);
-    hipLaunchKernelGGL((attention_keys_kernel<DB>), grid, dim3(64 * FW), bytes, stream, a, p.g);
+    hipLaunchKernelGGL((attention_keys_kernel<DB>), grid, dim3(64 * FW), (size_t)FW * 4 * FK * 64 * DB,
+                       stream, a, p.g);
   } else {
     hipLaunchKernelGGL((attention_rows_kernel<DB>), grid, dim3(256), (size_t)4 * BK * 64 * DB, stream,
                        a, p.g);
