@@ -58,7 +58,7 @@ struct VecArgs {
   float* y;
   int64_t ldx;          // bytes
   int m, n, k, ng;
-  int vec;              // scales (and zeros) that one aligned load may take: 1, 2, 4 or 8
+  int vec;              // scales (and zeros) that one aligned load may take: 1, 4 or 8
   int splits, per_split;  // of the row's blocks of 512 k over workgroups
   int slots;              // k slots of a workgroup, at most
 };
@@ -75,10 +75,10 @@ struct Finished {
   Epilogue e;
 };
 
-// The most that divides a row of scales and its addresses.
+// Of 8, 4 and 1, the most that divides a row of scales and its addresses.
 inline int scale_vec(const uint16_t* s16, const uint16_t* z16, int ng) {
   const uintptr_t bits = (uintptr_t)s16 | (uintptr_t)z16 | (uintptr_t)(2 * ng);
-  return bits % 16 == 0 ? 8 : bits % 8 == 0 ? 4 : bits % 4 == 0 ? 2 : 1;
+  return bits % 16 == 0 ? 8 : bits % 8 == 0 ? 4 : 1;
 }
 
 template <bool I8>
@@ -287,20 +287,28 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
   auto zero_bits = [](uint16_t z) __attribute__((always_inline)) {
     return (uint32_t)(I8 ? 128 - whole_zero(z) : z);
   };
-  // The scales and zeros of a block, side by side in LDS, V at a time per lane
-  // (a.vec: what their rows' alignment allows); neighbouring lanes take
-  // neighbouring pieces of a row.
-  auto scales_by = [&](int b, auto vec) __attribute__((always_inline)) {
+  // The scales and zeros of a block, side by side in LDS, V at a time per lane;
+  // neighbouring lanes take neighbouring pieces of a row.  ANY: pieces at any
+  // address, that may run into the next row; the matrix's last start earlier instead,
+  // and their values go round to their places.
+  auto scales_by = [&](int b, auto vec, auto any) __attribute__((always_inline)) {
     constexpr int V = decltype(vec)::value, P = S::GPB / V;  // pieces per row
+    constexpr bool ANY = decltype(any)::value;
     constexpr int LD = (16 * R * P + 63) / 64;
-    struct alignas(2 * V) Piece {
+    struct alignas(ANY ? 2 : 2 * V) Piece {
       uint16_t v[V];
     };
     Piece s[LD], z[LD];
+    int early[LD];
 #pragma unroll
     for (int i = 0; i < LD; ++i) {
-      const int e = min(64 * i + lane, 16 * R * P - 1);
-      const int64_t o = (int64_t)valid_row_at(e / P) * a.ng + min(b * S::GPB + (e % P) * V, a.ng - V);
+      const int e = min(64 * i + lane, 16 * R * P - 1), j = b * S::GPB + (e % P) * V;
+      int64_t o = (int64_t)valid_row_at(e / P) * a.ng + min(j, a.ng - (ANY ? 1 : V));
+      early[i] = 0;
+      if constexpr (ANY) {
+        early[i] = (int)max(o + V - (int64_t)a.n * a.ng, (int64_t)0);
+        o -= early[i];
+      }
       s[i] = *(const Piece*)(a.s16 + o);
       if (a.z16) z[i] = *(const Piece*)(a.z16 + o);
     }
@@ -308,21 +316,27 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
     for (int i = 0; i < LD; ++i) {
       const int e = min(64 * i + lane, 16 * R * P - 1);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        sc[((e % P) * V + v) * 16 * R + e / P] =
-            s[i].v[v] | zero_bits(a.z16 ? z[i].v[v] : (uint16_t)0x4800) << 16;  // 8
+      for (int v = 0; v < V; ++v) {
+        const int at = (e % P) * V + (ANY ? (v - early[i]) & (V - 1) : v);
+        const uint32_t both = s[i].v[v] | zero_bits(a.z16 ? z[i].v[v] : (uint16_t)0x4800) << 16;  // 8
+        sc[at * 16 * R + e / P] = ANY && b * S::GPB + at >= a.ng ? 0 : both;  // (another row's)
+      }
     }
   };
+  // Aligned where the rows are; else at any address (31 tokens through 25020 x 5216,
+  // groups of 32, gated, 58 us, with 2 bytes a load 85; 16 through 8192 x 11040 20.8
+  // and 26.5), one by one where the matrix has fewer than a piece.
   auto scales = [&](int b) __attribute__((always_inline)) {
+    constexpr std::false_type aligned{};
     if constexpr (G != 0) {
       if (S::GPB >= 8 && a.vec >= 8)
-        scales_by(b, std::integral_constant<int, S::GPB >= 8 ? 8 : 1>());
+        scales_by(b, std::integral_constant<int, S::GPB >= 8 ? 8 : 1>(), aligned);
       else if (a.vec >= 4)
-        scales_by(b, std::integral_constant<int, 4>());
-      else if (a.vec >= 2)
-        scales_by(b, std::integral_constant<int, 2>());
+        scales_by(b, std::integral_constant<int, 4>(), aligned);
+      else if ((int64_t)a.n * a.ng >= 8)
+        scales_by(b, std::integral_constant<int, S::GPB >= 8 ? 8 : 4>(), std::true_type());
       else
-        scales_by(b, std::integral_constant<int, 1>());
+        scales_by(b, std::integral_constant<int, 1>(), aligned);
     }
   };
 

@@ -168,6 +168,23 @@ def test_scales_at_any_address(off):
         c.check(gptq.gptq_w4a16_linear(c.X, Q, s, z, group_size=32, sym=False, out_dtype=torch.float32))
 
 
+@pytest.mark.parametrize("m", [1, 5, 40, 100])
+@pytest.mark.parametrize("g,d_in", [(32, 672), (64, 1088), (128, 1664), (32, 1120)])
+def test_weight_rows_are_their_own(m, g, d_in):
+    """A row of weights whose scales are NaN spoils its own column alone, whatever the number of
+    groups to a row divides by; the last rows' scales end where the array ends."""
+    c = Case(m, d_in, 37, g, False)
+    want = c.call()
+    Q, S, Z = c.dev
+    for row in (0, 17, 36):
+        bad = S.clone()
+        bad.view(torch.float16)[row] = float("nan")
+        got = gptq.gptq_w4a16_linear(c.X, Q, bad, Z, group_size=g, sym=False)
+        assert bool(torch.isnan(got[:, row]).all())
+        keep = [n for n in range(37) if n != row]
+        assert torch.equal(got[:, keep], want[:, keep])
+
+
 @pytest.mark.parametrize("m", [1, 33, 65, 333])
 def test_captured_and_replayed(m):
     c = Case(m, 4096, 264, 128, False, act="silu", gated=True, res="bf16", bias="bf16")
