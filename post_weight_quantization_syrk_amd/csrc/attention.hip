@@ -348,7 +348,24 @@ __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Pl
   }
 }
 
-// Many rows: four waves of 32 rows, which share tiles of 64 keys in LDS.
+// Many rows: four waves of 32 rows, which share tiles of 64 keys in LDS, two buffers
+// of them; two workgroups on a CU (heads up to 128), so that one's products run while
+// the other forms its weights.
+//
+// 16384 tokens, 64 heads of 128 over 8: 4.0 to 4.2 ms, 1.05 to 1.10 PF/s, where a
+// library bf16 product of 8192^3 reaches 1.29: under it the chip's clock falls to some
+// 1.6 GHz, at which the matrix cores are busy 56% of the cycles and the other vector
+// instructions (maxima, exponentials, rounding: 5 to a product) 36%.  Heads of 192: 0.74 PF/s, of 256: 0.67 (256 to 512 registers: one wave per
+// SIMD).  Seven prompts of 8197 tokens in all, 32 heads: 131 us, 0.66 PF/s: a fifth of
+// the products fall on tiles that are partly masked, and starting and ending take 8 us
+// of some 30 that a workgroup lives.
+//
+// Tried and slower (16384 tokens, against 1.05 PF/s on the same card, unless said): the
+// next tile's scores formed between this one's weights, whole tiles (0.87, spills) or
+// halves (0.94; heads of 256 0.75 against 0.67, of 192 0.70 against 0.74: not worth the
+// second form); eight waves in two groups that take turns (1.01); eight waves on 256
+// rows with three buffers (1.07, but the seven prompts 161 against 144 us); a wave's
+// priority raised for its products, sums in chains (no change).
 constexpr int BM = 128, BK = 64;
 
 template <int DB>
@@ -423,7 +440,11 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
 
 // Few rows: one tile of 32 rows, the keys in tiles of 32 that four waves (two,
 // where LDS holds no more) take in turn, each with two buffers of its own, so that
-// none waits for another; their sums meet at the end.
+// none waits for another; their sums meet at the end.  Bound by reading keys and
+// values: 64 sequences of 6001 keys, 64 heads over 8: 265 us, 5.9 TB/s; of 4096 to
+// 8192, 302 us, 5.3 TB/s (a large copy reaches 5.1).  One token over 4096 keys: 10.7 us in 20 splits, of which 2.6 are
+// the launch of the join and 1 each the sequence's search, the first tile's way from
+// memory and each of two tiles.
 constexpr int FM = 32, FK = 32;
 constexpr int few_waves(int DB) { return DB <= 4 ? 4 : 2; }
 
@@ -601,9 +622,14 @@ struct Plan {
 // at up to 35 GB/s, all together at 5.4 TB/s, and takes 4 us besides: 16 sequences
 // of 8192 keys, 8 key heads: 135 us in one piece, 105 in two, 112 in four; 24: 157
 // in one, 162 in four; one sequence of 4096: 44 us in one piece, 11.9 in 16.
-// More rows: two workgroups on every CU where the keys allow pieces of 256 (the
-// queries' own keys count half): 256 queries over 4096 keys: 95 us in one piece, 40
-// in eight; a prompt of 512: 17 us in one, 23 in two.
+// More rows: the same, of a tile's 64 keys at a time.  A workgroup that has a CU to
+// itself takes 0.87 us for them with heads of 64, 1.09 of 128, 3.2 of 256; two on a CU
+// take 1.7 times as long each (past some 128 workgroups some CUs have two; with heads
+// past 128 none); starting and ending takes 6 us (and more than eight rounds of
+// workgroups gain nothing); the parts go to memory and back at 6 TB/s, behind a launch
+// of 4 us.  The queries' own keys count half.  256 queries of 32 heads over 4096 keys
+// of 8: 77 us in one piece, 36 in eight, 48 in 16; a prompt of 512: 15 us in one, 22 in
+// two; 305 queries of two heads of 256 over 857 keys: 49 us in one, 22 in six.
 Plan plan_for(int64_t tq, int64_t batch, int hq, int hk, int hd, int64_t max_kv_len) {
   Plan p;
   const int group = hq / hk;
@@ -624,8 +650,20 @@ Plan plan_for(int64_t tq, int64_t batch, int hq, int hk, int hd, int64_t max_kv_
       if (least == 0.0 || us < least) least = us, p.g.splits = s;
     }
   } else {
-    const int64_t keys = max_kv_len - std::min(max_kv_len, tq / batch) / 2;
-    p.g.splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(512 / tiles, keys / 256), 32));
+    const int db = hd <= 128 ? std::max((int)ceil_div(hd, 32), 2) : hd <= 192 ? 6 : 8;
+    const double step = db <= 4 ? 0.65 + 0.11 * db : 0.4 * db;  // us for 64 keys
+    const int64_t there = db <= 4 ? 512 : 256;                  // workgroups at a time
+    const double mean = (double)(max_kv_len - std::min(max_kv_len, tq / batch) / 2) / 64.0;
+    double least = 0.0;
+    for (int s = 1; s <= 32 && (s == 1 || (s * 128 <= max_kv_len && tiles * s <= 4096)); ++s) {
+      const int64_t n = tiles * s;
+      const double two = db <= 4 ? 1.0 + 0.7 * std::min(std::max((double)(n - 128) / 256.0, 0.0), 1.0) : 1.0;
+      const double longest = (double)ceil_div(ceil_div(max_kv_len, 64), s) * step * two;
+      const double all = (double)tiles * mean * step * (db <= 4 ? 1.7 : 1.0) / (double)there;
+      double us = std::max(longest, all) + 6.0 * (double)ceil_div(n, there);
+      if (s > 1) us += 4.0 + 2.0 * (double)s * (double)(tq * hq) * (4 * hd + 8) / 6e6;
+      if (least == 0.0 || us < least) least = us, p.g.splits = s;
+    }
   }
   p.bytes = p.g.splits > 1 ? (size_t)p.g.splits * tq * hq * (hd * 4 + 8) : 0;
   return p;

@@ -3,7 +3,25 @@
 //   (linear_epi.h), W_hat[n][k] = s[n][k/g] (q[n][k] - z[n][k/g]).
 //
 // q - z is exact in bf16, so products with X are exact in float32; a group's sum
-// stands by itself and is scaled into the total with one operation per sum.
+// stands by itself and is scaled into the total with one operation per sum
+// (v_mfma_f32_32x32x16_bf16: for every product of 32 x 32 x 16 as many vector
+// operations as a group has sixteens of k go into 16, so 8 at groups of 32, 4 at 64, 2
+// at 128; four cost nothing beside a product, eight take as long as it).
+//
+// Two forms of the weights.  Four bits: each wave takes its own 32 weight rows apart,
+// once, for up to 256 rows of X; chunks of 64 k of X and of the words come to LDS by
+// direct loads, up to three ahead.  Eight bits first (`Wide`) for many rows: a wave has
+// 64 weight rows, and two codes become bf16 with one operation.
+//
+// 8192 tokens through 57344 x 8192, groups of 128, gated, SiLU: 6.9 ms, 1.12 PF/s, of
+// which 0.15 ms make the weights wide; a library bf16 product of 8192^3 reaches 1.29.
+// The clock falls to some 1.65 GHz there (power), at which the matrix cores are busy
+// 61% of the cycles.  515 tokens through 4099 x 11008, groups of 32: 91 to 99 us by
+// card, of which the join of five splits takes 11: 14 vector operations to a product
+// (eight scale its sums, the rest are the codes' and addresses) are busy 45% of the
+// cycles, the matrix cores 25%, and waves wait 24% of theirs, at a workgroup's start
+// and end above all.  96 tokens through 4096 x
+// 4096: 24 us, of which launches, a workgroup's start and end take two thirds.
 #include "common.h"
 #include "kernels.h"
 #include "w4_dot.h"
