@@ -213,10 +213,24 @@ __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const cha
   }
 }
 
-// A row by the definition, key by key: for rows whose sums met an infinity or a
-// NaN, which may be a key's that the row does not see (a tile multiplies such a
-// key's value by a weight of 0).  A whole wave takes the row; lane l has columns
-// 4 l .. 4 l + 3.
+// Whether a value of keys from .. to is an infinity or a NaN, by a whole wave.
+__device__ __forceinline__ bool odd_values(const uint16_t* v, int64_t ldv, int hd, int from, int to) {
+  const int d = 4 * (threadIdx.x & 63);
+  bool odd = false;
+  for (int j = from; j <= to; ++j) {
+    if (d < hd) {
+      const uint2 u = *(const uint2*)(v + (int64_t)j * ldv + d);
+      odd = odd || (u.x & 0x7f80u) == 0x7f80u || (u.x & 0x7f800000u) == 0x7f800000u ||
+            (u.y & 0x7f80u) == 0x7f80u || (u.y & 0x7f800000u) == 0x7f800000u;
+    }
+  }
+  return __any(odd);
+}
+
+// A row by the definition, key by key: for rows whose sums met an infinity or a NaN
+// where a key that they do not see has such a value (a tile multiplies it by a weight
+// of 0; hidden keys' scores are replaced).  A whole wave takes the row; lane l has
+// columns 4 l .. 4 l + 3.
 struct Slow {
   float o[4], mc, l;
 };
@@ -289,12 +303,13 @@ __device__ __forceinline__ bool finite4(const f32x16& v) {
 }
 
 // The wave's 32 rows leave: lane l's is `row` of the sequence (query, head), with
-// l the whole row's sum and o its columns; lim: the last key that it sees.
+// l the whole row's sum and o its columns; lim: the last key that it sees; reach: the
+// end of the tiles that the wave took.
 template <int DB>
 __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Place& p, int group,
                                       int kvh, bool live, int query, int head, int lim, int split,
-                                      int begin, int end, float c, const f32x16 (&o)[DB], float mc,
-                                      float l, char* room) {
+                                      int begin, int end, int reach, float c, const f32x16 (&o)[DB],
+                                      float mc, float l, char* room) {
   constexpr int RB = 64 * DB;
   const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
   const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays)
@@ -336,6 +351,9 @@ __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Pl
   if (!a.causal) return;
   uint64_t bad = __ballot(live && !ok && lim < p.lk - 1);
   uint32_t rest = (uint32_t)bad | (uint32_t)(bad >> 32);
+  if (!rest || !odd_values(a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd,
+                           max(__builtin_amdgcn_readlane(lim, 0) + 1, begin), min(reach, p.lk) - 1))
+    return;
   while (rest) {
     const int r = __builtin_ctz(rest);
     rest &= rest - 1;
@@ -434,8 +452,9 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
   }
   const float l = w.l + other_half(w.l);
   __syncthreads();  // the tiles are read
-  leave<DB>(a, g, p, group, kvh, row0 + l32 < p.rows, query, head, lim, split, begin, end, c, w.o, w.mc, l,
-            lds + wave * 32 * RB);
+  const int reach = begin + (max(min(end, lim_last + 1) - begin, 0) + BK - 1) / BK * BK;
+  leave<DB>(a, g, p, group, kvh, row0 + l32 < p.rows, query, head, lim, split, begin, end, reach, c, w.o, w.mc,
+            l, lds + wave * 32 * RB);
 }
 
 // Few rows: one tile of 32 rows, the keys in tiles of 32 that four waves (two,
@@ -553,10 +572,14 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
   }
   if (!a.causal) return;
   __syncthreads();
+  const int reach = begin + (max(end - begin, 0) + FK - 1) / FK * FK;  // the end of the tiles
   for (int r = wave; r < live; r += FW) {
     const int at_row = p.row0 + r, at_query = (int)((uint32_t)at_row / (uint32_t)group);
     const int last = min(at_query + back, p.lk - 1);
-    if (!bad[r] || last >= p.lk - 1) continue;
+    if (!bad[r] || last >= p.lk - 1 ||
+        !odd_values(a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd, max(last + 1, begin),
+                    min(reach, p.lk) - 1))
+      continue;
     const int64_t qi = p.q0 + at_query;
     const int hr = kvh * group + at_row - at_query * group;
     const Slow t = slow_row(a.q + qi * a.ldq + hr * a.hsq, a.k + p.start * a.ldk + kvh * a.hsk, a.ldk,

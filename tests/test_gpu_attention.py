@@ -153,6 +153,31 @@ def test_what_is_not_seen_does_not_matter(lq, lk, bad):
             assert not bool(torch.isfinite(got[b - 3:b]).any())
 
 
+@pytest.mark.parametrize("lq,lk", [([300, 40], None), ([3], [500]), ([140], [2000])])
+@pytest.mark.parametrize("seen_too", [False, True])
+def test_a_value_that_spoils_some_rows(lq, lk, seen_too):
+    """A NaN in a value reaches the queries that see it, in its column and its heads alone, also
+    where a value that they do not see is infinite."""
+    c = Case(lq, lk, 4, 2, 96, seed=12)
+    good = c.call()
+    v = c.v.clone()
+    n0, a0 = int(c.lens[0]), int(c.starts[0])
+    first = n0 - lq[0] + 1                      # the second query sees it, the first does not
+    v[a0 + first, 1, 7] = float("nan")
+    if seen_too:
+        v[a0 + n0 - 1, 1, 9] = float("inf")     # only the last query sees it
+    got = c.call(v=v)
+    a, b = int(c.cu[0]), int(c.cu[1])
+    assert bool(torch.isnan(got[a + 1:b, 2:, 7]).all())
+    y, e = c.reference()
+    keep = [h for h in range(96) if h != 7]
+    for rows, heads, cols in ((slice(a, a + 1), slice(0, 4), list(range(96))),
+                              (slice(a + 1, b), slice(0, 2), list(range(96))),
+                              (slice(a + 1, b - 1), slice(2, 4), keep)):
+        within(got[rows, heads][:, :, cols], y[rows, heads][:, :, cols], e[rows, heads][:, :, cols])
+    assert torch.equal(got[b:int(c.cu[-1])], good[b:int(c.cu[-1])])
+
+
 @pytest.mark.parametrize("longest", [0, 1, 100, 100000])
 def test_max_kv_len_is_only_a_hint(longest):
     for lq, lk in (([1, 1], [1500, 40]), ([150], [800])):
