@@ -521,11 +521,12 @@ int gptq_qk_norm_rope(const void* Q, int64_t ldq, int64_t hsq, const void* K, in
  * ws          gptq_attention_workspace(...) bytes (0 where keys are not split);
  *             its contents on entry do not matter; calls in flight together need
  *             one each.
- * Scores, maxima and sums are float32; the weights p are rounded to bf16, relative
- * to a maximum that the row's own exceeds by less than a factor of 2^8, and their
- * sum is that of the rounded values (values V past some 2^120 / lk overflow the
- * sums).  The order of every sum is fixed.  Keys and values that a query does not see
- * do not reach it, whatever they hold.
+ * Scores, maxima and sums are float32; the weights p are rounded to bf16 (with few
+ * rows to a sequence to two bf16 parts, 2^-17), relative to a maximum that the row's
+ * own exceeds by less than a factor of 2^8, and their sum is that of the rounded
+ * values (values V past some 2^120 / lk overflow the sums).  The order of every sum is
+ * fixed.  Keys and values that a query does not see do not reach it, whatever they
+ * hold.
  * total_q * hq / 32 + batch * hk is bounded by 2^23 (GPTQ_EUNSUPPORTED past it).
  * ------------------------------------------------------------------------- */
 int gptq_attention(const void* Q, int64_t ldq, int64_t hsq, const void* K, int64_t ldk, int64_t hsk,

@@ -12,7 +12,8 @@
 // the contraction takes keys in any order: V^T's fragments are read in that order
 // by the LDS transpose read.)  Scores, maxima, sums and O stay in float32; P is
 // rounded to bf16 for the matrix cores and its sum is taken over the rounded
-// values, so that a row's weights add up to one.
+// values, so that a row's weights add up to one; where rows are few and the matrix
+// cores idle, P goes in two bf16 parts.
 #include "common.h"
 #include "kernels.h"
 
@@ -147,8 +148,11 @@ __device__ __forceinline__ void start_rows(Rows<DB>& w, const uint16_t* qrow, in
 }
 
 // One tile of 32 KB keys, in LDS at lk and lv.  rel: the last key that the lane's
-// row sees, less the tile's first; masked: some row does not see all of them.
-template <int DB, int KB>
+// row sees, less the tile's first; masked: some row does not see all of them.  FINE:
+// the weights in two bf16 parts, a rounding of 2^-17 in place of 2^-9 (one token's
+// error against 64 bits 0.0018 -> 0.0016, the output's own rounding; 10.7 -> 11.1 us,
+// nothing where memory is the bound; with many rows half as many products more).
+template <int DB, int KB, bool FINE>
 __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const char* lv, float c,
                                           int rel, bool masked) {
   constexpr int RB = 64 * DB;
@@ -191,13 +195,19 @@ __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const cha
   const int i16 = lane & 15, trow = 4 * h + (i16 >> 2), tu = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
 #pragma unroll
   for (int kc = 0; kc < 2 * KB; ++kc) {  // 16 keys
-    bf16x8 p;
+    bf16x8 p, rest;
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
-      const bf16x2 two = {(__bf16)exp2_of(fmaf(s[kc >> 1][8 * (kc & 1) + j], c, -w.mc)),
-                          (__bf16)exp2_of(fmaf(s[kc >> 1][8 * (kc & 1) + j + 1], c, -w.mc))};
+      const float e0 = exp2_of(fmaf(s[kc >> 1][8 * (kc & 1) + j], c, -w.mc));
+      const float e1 = exp2_of(fmaf(s[kc >> 1][8 * (kc & 1) + j + 1], c, -w.mc));
+      const bf16x2 two = {(__bf16)e0, (__bf16)e1};
       w.l = __builtin_amdgcn_fdot2_f32_bf16(two, ones, w.l, false);
       p[j] = two[0], p[j + 1] = two[1];
+      if constexpr (FINE) {
+        const bf16x2 left = {(__bf16)(e0 - (float)two[0]), (__bf16)(e1 - (float)two[1])};
+        w.l = __builtin_amdgcn_fdot2_f32_bf16(left, ones, w.l, false);
+        rest[j] = left[0], rest[j + 1] = left[1];
+      }
     }
 #pragma unroll
     for (int b = 0; b < DB; ++b) {
@@ -209,6 +219,7 @@ __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const cha
         __builtin_memcpy((char*)&v + 8 * e, &t, 8);
       }
       w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, w.o[b], 0, 0, 0);
+      if constexpr (FINE) w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, rest, w.o[b], 0, 0, 0);
     }
   }
 }
@@ -448,7 +459,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
     if (key0 + BK < end) issue(key0 + BK, buf ^ 1);
     if (key0 > lim_last) continue;
     const char* const t = lds + buf * 2 * TILE;
-    tile_step<DB, BK / 32>(w, t, t + TILE, c, lim - key0, lim_first < key0 + BK - 1);
+    tile_step<DB, BK / 32, false>(w, t, t + TILE, c, lim - key0, lim_first < key0 + BK - 1);
   }
   const float l = w.l + other_half(w.l);
   __syncthreads();  // the tiles are read
@@ -461,7 +472,7 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
 // where LDS holds no more) take in turn, each with two buffers of its own, so that
 // none waits for another; their sums meet at the end.  Bound by reading keys and
 // values: 64 sequences of 6001 keys, 64 heads over 8: 265 us, 5.9 TB/s; of 4096 to
-// 8192, 302 us, 5.3 TB/s (a large copy reaches 5.1).  One token over 4096 keys: 10.7 us in 20 splits, of which 2.6 are
+// 8192, 302 us, 5.3 TB/s (a large copy reaches 5.1).  One token over 4096 keys: 11.1 us in 20 splits, of which 2.6 are
 // the launch of the join and 1 each the sequence's search, the first tile's way from
 // memory and each of two tiles.
 constexpr int FM = 32, FK = 32;
@@ -526,7 +537,7 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
       __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     const char* const t = mine + buf * 2 * TILE;
-    tile_step<DB, FK / 32>(w, t, t + TILE, c, lim - key0, lim_first < key0 + FK - 1);
+    tile_step<DB, FK / 32, true>(w, t, t + TILE, c, lim - key0, lim_first < key0 + FK - 1);
   }
   const float l = w.l + other_half(w.l);
   // The waves' sums meet in LDS, where a thread takes four columns of a row: rows
