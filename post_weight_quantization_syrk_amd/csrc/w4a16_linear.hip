@@ -529,8 +529,18 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(Args a) {
   tile_product<1, G, GATED, WIDE>(a, lds, m0, c0, split);
 }
 
-// Few tokens: the kernels that read the weights once for all of them.
-bool few_tokens(int64_t m) { return m <= 64; }
+// Few tokens: the kernels that read the weights once for all of them, up to 16, and up
+// to 64 where the weights are not large.  Their vector work grows with every 16 tokens,
+// most with groups of 32, and past one round of workgroups nothing hides it (32 tokens,
+// groups of 32: 16384 x 8192 43 us, by tiles 37, but 8192 x 8192 22.5 and 26; 48: 11008
+// x 4096 27.5 and 27, 4096 x 4096 14 and 18; 64 tokens, groups of 64: 4096 x 11008 32
+// and 28, 4096 x 4096 20 and 20; groups of 128: 16384 x 8192 46 and 42; 48 tokens 39
+// and 40, 32 tokens 26 and 32).
+bool few_tokens(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
+  if (m > 64) return false;
+  const int64_t sixteens = ceil_div(m, 16), codes = d_out * d_in;
+  return group_size == 32 ? codes * (sixteens - 1) < 80000000 : sixteens < 4 || codes < 45000000;
+}
 
 struct Plan {
   bool wide;  // weights in eight bits first
@@ -607,7 +617,8 @@ hipError_t tiles_launch(const Args& a, int G, hipStream_t stream) {
 }  // namespace
 
 size_t linear_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_size, bool gated) {
-  if (few_tokens(m)) return linear_vec_workspace(m, d_out, d_in, group_size, gated);
+  if (few_tokens(m, d_out, d_in, group_size))
+    return linear_vec_workspace(m, d_out, d_in, group_size, gated);
   return plan_for(m, d_out, d_in, group_size, gated).bytes;
 }
 
@@ -615,7 +626,7 @@ hipError_t linear_launch(const void* X, int64_t m, int64_t ldx, const uint32_t* 
                          const uint16_t* scales_f16, const uint16_t* zeros_f16, int64_t d_out,
                          int64_t d_in, int group_size, bool gated, const Epilogue& e, void* ws,
                          hipStream_t stream) {
-  if (few_tokens(m))
+  if (few_tokens(m, d_out, d_in, group_size))
     return linear_vec_launch(X, m, ldx, qweight, scales_f16, zeros_f16, d_out, d_in, group_size,
                              gated, e, ws, stream);
   const Plan p = plan_for(m, d_out, d_in, group_size, gated);

@@ -69,6 +69,9 @@ CASES = [
     dict(m=49, d_in=4160, d_out=12290, g=64, sym=False, gated=True, act="gelu", bias="bf16"),
     dict(m=64, d_in=6176, d_out=8190, g=-1, sym=False, act="relu", res="f32", out="f32"),
     dict(m=64, d_in=5152, d_out=2102, g=-1, sym=False, gated=True, act="silu", bias="f32"),
+    # few tokens through large weights
+    dict(m=50, d_in=1056, d_out=25801, g=32, sym=False, act="silu", bias="bf16", res="f32"),
+    dict(m=57, d_in=4160, d_out=10880, g=64, sym=True, gated=True, act="gelu", out="f32"),
     # tiles: ragged rows, columns and k, splits, every group size
     dict(m=65, d_in=32, d_out=1, g=32, sym=False, act="relu", bias="f32", res="bf16"),
     dict(m=65, d_in=96, d_out=2, g=32, sym=True, gated=True, act="silu"),
