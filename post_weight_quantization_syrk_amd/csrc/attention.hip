@@ -384,17 +384,21 @@ __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Pl
 // 16384 tokens, 64 heads of 128 over 8: 4.0 to 4.2 ms, 1.05 to 1.10 PF/s, where a
 // library bf16 product of 8192^3 reaches 1.29: under it the chip's clock falls to some
 // 1.6 GHz, at which the matrix cores are busy 56% of the cycles and the other vector
-// instructions (maxima, exponentials, rounding: 5 to a product) 36%.  Heads of 192: 0.74 PF/s, of 256: 0.67 (256 to 512 registers: one wave per
-// SIMD).  Seven prompts of 8197 tokens in all, 32 heads: 131 us, 0.66 PF/s: a fifth of
-// the products fall on tiles that are partly masked, and starting and ending take 8 us
-// of some 30 that a workgroup lives.
+// instructions (maxima, exponentials, rounding: 5 to a product) 36%.  Heads of 192:
+// 0.74 PF/s, of 256: 0.67 (256 to 512 registers: one wave per SIMD).  Seven prompts of
+// 8197 tokens in all, 32 heads: 128 to 142 us by card, 0.65 PF/s: a fifth of the
+// products fall on tiles that are partly masked, starting and ending take 8 us of the
+// 27 that a workgroup lives, and over the last 30 us, the first sequence's rows, half
+// of the workgroups' places stand empty (all sequences' long tiles first would fill
+// them, and the L2s would lose the keys that a sequence's tiles share).
 //
 // Tried and slower (16384 tokens, against 1.05 PF/s on the same card, unless said): the
 // next tile's scores formed between this one's weights, whole tiles (0.87, spills) or
 // halves (0.94; heads of 256 0.75 against 0.67, of 192 0.70 against 0.74: not worth the
 // second form); eight waves in two groups that take turns (1.01); eight waves on 256
-// rows with three buffers (1.07, but the seven prompts 161 against 144 us); a wave's
-// priority raised for its products, sums in chains (no change).
+// rows with three buffers (1.07, but the seven prompts 161 against 144 us).  No change:
+// no barrier before the rows leave, a wave's priority raised for its products, sums in
+// chains.
 constexpr int BM = 128, BK = 64;
 
 template <int DB>
