@@ -14,6 +14,7 @@
 // rounded to bf16 for the matrix cores and its sum is taken over the rounded
 // values, so that a row's weights add up to one; where rows are few and the matrix
 // cores idle, P goes in two bf16 parts.
+#include "attention_ranges.h"
 #include "common.h"
 #include "kernels.h"
 
@@ -299,13 +300,6 @@ __device__ __forceinline__ void store4(const AttnArgs& a, const Grid& g, int spl
   }
 }
 
-// A tile's keys as this workgroup has them: [begin, end), whole tiles of `step`.
-__device__ __forceinline__ void key_range(int kend, int step, int splits, int split, int& begin,
-                                          int& end) {
-  const int tiles = (kend + step - 1) / step, per = (tiles + splits - 1) / splits;
-  begin = min(split * per * step, kend), end = min((split + 1) * per * step, kend);
-}
-
 __device__ __forceinline__ bool finite4(const f32x16& v) {
   float t = 0.0f;
 #pragma unroll
@@ -319,7 +313,7 @@ __device__ __forceinline__ bool finite4(const f32x16& v) {
 template <int DB>
 __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Place& p, int group,
                                       int kvh, bool live, int query, int head, int lim, int split,
-                                      int begin, int end, int reach, float c, const f32x16 (&o)[DB],
+                                      int begin, int end, int64_t reach, float c, const f32x16 (&o)[DB],
                                       float mc, float l, char* room) {
   constexpr int RB = 64 * DB;
   const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
@@ -363,7 +357,7 @@ __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Pl
   uint64_t bad = __ballot(live && !ok && lim < p.lk - 1);
   uint32_t rest = (uint32_t)bad | (uint32_t)(bad >> 32);
   if (!rest || !odd_values(a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd,
-                           max(__builtin_amdgcn_readlane(lim, 0) + 1, begin), min(reach, p.lk) - 1))
+                           max(__builtin_amdgcn_readlane(lim, 0) + 1, begin), (int)min(reach, (int64_t)p.lk) - 1))
     return;
   while (rest) {
     const int r = __builtin_ctz(rest);
@@ -420,8 +414,8 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
   // the last key that any row of the tile sees
   const int back = p.lk - p.lq;
   const int tile_last = (int)((uint32_t)min(p.row0 + BM - 1, p.rows - 1) / (uint32_t)group);
-  int begin, end;
-  key_range(a.causal ? min(tile_last + back, p.lk - 1) + 1 : p.lk, BK, g.splits, split, begin, end);
+  const KeyRange keys = key_range(a.causal ? min(tile_last + back, p.lk - 1) + 1 : p.lk, BK, g.splits, split);
+  const int begin = keys.begin, end = keys.end;
 
   // direct loads: this wave's DB KB of each tile, units past hd replaced
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
@@ -456,18 +450,20 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
   // the last key that a row sees: the lane's, the wave's first and last
   const int lim = a.causal ? min(query + back, p.lk - 1) : p.lk - 1;
   const int lim_first = __builtin_amdgcn_readlane(lim, 0), lim_last = __builtin_amdgcn_readlane(lim, 31);
-  for (int key0 = begin, buf = 0; key0 < end; key0 += BK, buf ^= 1) {
+  // (by the keys that are left: a key's number may be near 2^31)
+  for (int left = end - begin, buf = 0; left > 0; left -= BK, buf ^= 1) {
+    const int key0 = end - left;
     // this tile has landed, and the other buffer is read
     __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (key0 + BK < end) issue(key0 + BK, buf ^ 1);
+    if (left > BK) issue(key0 + BK, buf ^ 1);
     if (key0 > lim_last) continue;
     const char* const t = lds + buf * 2 * TILE;
-    tile_step<DB, BK / 32, false>(w, t, t + TILE, c, lim - key0, lim_first < key0 + BK - 1);
+    tile_step<DB, BK / 32, false>(w, t, t + TILE, c, lim - key0, lim_first - key0 < BK - 1);
   }
   const float l = w.l + other_half(w.l);
   __syncthreads();  // the tiles are read
-  const int reach = begin + (max(min(end, lim_last + 1) - begin, 0) + BK - 1) / BK * BK;
+  const int64_t reach = begin + ((int64_t)max(min(end - 1, lim_last) - begin + 1, 0) + BK - 1) / BK * BK;
   leave<DB>(a, g, p, group, kvh, row0 + l32 < p.rows, query, head, lim, split, begin, end, reach, c, w.o, w.mc,
             l, lds + wave * 32 * RB);
 }
@@ -496,8 +492,8 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
   const float c = a.scale * 1.4426950408889634f;
   const int back = p.lk - p.lq;
   const int tile_last = (int)((uint32_t)min(p.row0 + FM - 1, p.rows - 1) / (uint32_t)group);
-  int begin, end;
-  key_range(a.causal ? min(tile_last + back, p.lk - 1) + 1 : p.lk, FK * FW, g.splits, split, begin, end);
+  const KeyRange keys = key_range(a.causal ? min(tile_last + back, p.lk - 1) + 1 : p.lk, FK * FW, g.splits, split);
+  const int begin = keys.begin, end = keys.end;
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds + wave * 4 * TILE;
   const char* const mine = lds + wave * 4 * TILE;
@@ -522,8 +518,8 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
     for (int j = 0; j < PIECES; ++j)
       dma16(vs, (uint32_t)min(trow[j], most) * (uint32_t)(2 * a.ldv) + tcol[j], dst + TILE + 1024 * j);
   };
-  const int first = begin + FK * wave;
-  if (first < end) issue(first, 0);
+  const int mine_left = end - begin - FK * wave;  // keys from this wave's first on
+  if (mine_left > 0) issue(end - mine_left, 0);
 
   const int row = min(p.row0 + l32, p.rows - 1);
   const int query = (int)((uint32_t)row / (uint32_t)group), head = kvh * group + row - query * group;
@@ -531,17 +527,18 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
   start_rows<DB>(w, a.q + (p.q0 + query) * a.ldq + head * a.hsq, a.hd, h);
   const int lim = a.causal ? min(query + back, p.lk - 1) : p.lk - 1;
   const int lim_first = __builtin_amdgcn_readlane(lim, 0);
-  for (int key0 = first, buf = 0; key0 < end; key0 += FK * FW, buf ^= 1) {
+  for (int left = mine_left, buf = 0; left > 0; left -= FK * FW, buf ^= 1) {
+    const int key0 = end - left;
     // every read of the other buffer has returned before it is written again
     __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (key0 + FK * FW < end) {
+    if (left > FK * FW) {
       issue(key0 + FK * FW, buf ^ 1);
       __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PIECES) : "memory");
     } else {
       __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
     const char* const t = mine + buf * 2 * TILE;
-    tile_step<DB, FK / 32, true>(w, t, t + TILE, c, lim - key0, lim_first < key0 + FK - 1);
+    tile_step<DB, FK / 32, true>(w, t, t + TILE, c, lim - key0, lim_first - key0 < FK - 1);
   }
   const float l = w.l + other_half(w.l);
   // The waves' sums meet in LDS, where a thread takes four columns of a row: rows
@@ -587,13 +584,13 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
   }
   if (!a.causal) return;
   __syncthreads();
-  const int reach = begin + (max(end - begin, 0) + FK - 1) / FK * FK;  // the end of the tiles
+  const int64_t reach = begin + ((int64_t)(end - begin) + FK - 1) / FK * FK;  // the end of the tiles
   for (int r = wave; r < live; r += FW) {
     const int at_row = p.row0 + r, at_query = (int)((uint32_t)at_row / (uint32_t)group);
     const int last = min(at_query + back, p.lk - 1);
     if (!bad[r] || last >= p.lk - 1 ||
         !odd_values(a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd, max(last + 1, begin),
-                    min(reach, p.lk) - 1))
+                    (int)min(reach, (int64_t)p.lk) - 1))
       continue;
     const int64_t qi = p.q0 + at_query;
     const int hr = kvh * group + at_row - at_query * group;
