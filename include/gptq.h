@@ -526,7 +526,10 @@ int gptq_qk_norm_rope(const void* Q, int64_t ldq, int64_t hsq, const void* K, in
  * own exceeds by less than a factor of 2^8, and their sum is that of the rounded
  * values (values V past some 2^120 / lk overflow the sums).  The order of every sum is
  * fixed.  Keys and values that a query does not see do not reach it, whatever they
- * hold.
+ * hold; of an infinity or a NaN that it sees it gets what the formula gives, in a
+ * value's column alone (rows with one are gone over twice: some four times the time).
+ * A query whose scores are all -inf is 0 / 0, NaN.  Finite scores have magnitudes
+ * below 2^30 (scaled): past that one step of float32 is a factor of exp(64).
  * total_q * hq / 32 + batch * hk is bounded by 2^23 (GPTQ_EUNSUPPORTED past it).
  * ------------------------------------------------------------------------- */
 int gptq_attention(const void* Q, int64_t ldq, int64_t hsq, const void* K, int64_t ldk, int64_t hsk,

@@ -19,6 +19,7 @@
 #include "kernels.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace gptq {
 
@@ -28,7 +29,7 @@ typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
 typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 
-constexpr float NO_MAX = -3.0e38f;  // of a row that has seen no key yet
+constexpr float NO_MAX = -3.4028235e38f;  // of a row that has seen no key yet
 // O is scaled again only when a row's maximum has grown by more than 2^GROWTH
 // since the last time: p is then at most 2^GROWTH, with the same relative
 // rounding, and sums stay far inside float32.
@@ -131,6 +132,13 @@ struct Rows {
 };
 
 template <int DB>
+__device__ __forceinline__ void no_keys(Rows<DB>& w) {
+#pragma unroll
+  for (int b = 0; b < DB; ++b) w.o[b] = f32x16{};
+  w.mc = NO_MAX, w.l = 0.0f;
+}
+
+template <int DB>
 __device__ __forceinline__ void start_rows(Rows<DB>& w, const uint16_t* qrow, int hd, int h) {
 #pragma unroll
   for (int i = 0; i < 2 * DB; ++i) {
@@ -143,19 +151,51 @@ __device__ __forceinline__ void start_rows(Rows<DB>& w, const uint16_t* qrow, in
   // loads in flight, in every step
 #pragma unroll
   for (int i = 0; i < 2 * DB; ++i) asm volatile("" : "+v"(w.q[i]));
+  no_keys(w);
+}
+
+// A value's part in the products, and what is set aside where it is an infinity or a NaN:
+// 1 for +inf, 128 for -inf, 16384 for a NaN, so that their sum over 16 keys, weighted by
+// 1 for a key that is seen, tells which of them there were.  Whether there are any.
+__device__ __forceinline__ bool set_aside(bf16x8& v, bf16x8& odd) {
+  uint32_t u[4], o[4];
+  __builtin_memcpy(u, &v, 16);
 #pragma unroll
-  for (int b = 0; b < DB; ++b) w.o[b] = f32x16{};
-  w.mc = NO_MAX, w.l = 0.0f;
+  for (int i = 0; i < 4; ++i) {
+    o[i] = 0;
+#pragma unroll
+    for (int sh = 0; sh < 32; sh += 16) {
+      const uint32_t e = (u[i] >> sh) & 0xffffu, is = (e & 0x7f80u) == 0x7f80u ? 0xffffu : 0u;
+      const uint32_t inf = 0x3f80u + (e >> 15) * (0x4300u - 0x3f80u), code = (e & 0x7fu) ? 0x4680u : inf;
+      u[i] &= ~(is << sh);
+      o[i] |= (code & is) << sh;
+    }
+  }
+  __builtin_memcpy(&v, u, 16);
+  __builtin_memcpy(&odd, o, 16);
+  return (o[0] | o[1] | o[2] | o[3]) != 0;
+}
+
+__device__ __forceinline__ float of_odd(float sum) {
+  const float minus = floorf(sum * 0.0078125f), plus = sum - 128.0f * minus;
+  const float both = (plus > 0.0f ? INFINITY : 0.0f) + (minus > 0.0f ? -INFINITY : 0.0f);
+  return sum >= 16384.0f ? NAN : both;
 }
 
 // One tile of 32 KB keys, in LDS at lk and lv.  rel: the last key that the lane's
 // row sees, less the tile's first; masked: some row does not see all of them.  FINE:
-// the weights in two bf16 parts, a rounding of 2^-17 in place of 2^-9 (one token's
-// error against 64 bits 0.0018 -> 0.0016, the output's own rounding; 10.7 -> 11.1 us,
-// nothing where memory is the bound; with many rows half as many products more).
-template <int DB, int KB, bool FINE>
+// the weights in two bf16 parts, a rounding of 2^-17 in place of 2^-8 (one token's
+// error against 64 bits 0.0018 -> 0.0016; 10.7 -> 11.1 us, nothing where memory is the
+// bound; with many rows half as many products more).
+//
+// CAREFUL: for rows whose sums came out infinite or NaN.  A product with 0 is NaN where
+// the other side is odd: a value that the row does not see (its weight is 0), a value
+// that it sees (the second part of its weight may be 0, or of the other sign), a key's
+// last unit in place of columns past hd (the query's are 0 there).  So those columns are
+// taken as 0, and odd values apart from the others, by what the row sees of them.
+template <int DB, int KB, bool FINE, bool CAREFUL>
 __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const char* lv, float c,
-                                          int rel, bool masked) {
+                                          int rel, bool masked, int hd) {
   constexpr int RB = 64 * DB;
   const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
   f32x16 s[KB];
@@ -165,7 +205,10 @@ __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const cha
     s[kb] = f32x16{};
 #pragma unroll
     for (int i = 0; i < 2 * DB; ++i) {
-      const bf16x8 k = *(const bf16x8*)(lk + (32 * kb + l32) * RB + 16 * ((2 * i + h) ^ ksw));
+      bf16x8 k = *(const bf16x8*)(lk + (32 * kb + l32) * RB + 16 * ((2 * i + h) ^ ksw));
+      if constexpr (CAREFUL) {
+        if (16 * i + 8 * h >= hd) k = bf16x8{};
+      }
       s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, w.q[i], s[kb], 0, 0, 0);
     }
   }
@@ -193,10 +236,8 @@ __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const cha
       for (int i = 0; i < 16; ++i) w.o[b][i] *= f;
   }
   const bf16x2 ones = {(__bf16)1.0f, (__bf16)1.0f};
-  const int i16 = lane & 15, trow = 4 * h + (i16 >> 2), tu = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
-#pragma unroll
-  for (int kc = 0; kc < 2 * KB; ++kc) {  // 16 keys
-    bf16x8 p, rest;
+  // the weights of 16 keys
+  auto weights = [&](int kc, bf16x8& p, bf16x8& rest) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       const float e0 = exp2_of(fmaf(s[kc >> 1][8 * (kc & 1) + j], c, -w.mc));
@@ -210,72 +251,67 @@ __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const cha
         rest[j] = left[0], rest[j + 1] = left[1];
       }
     }
+  };
+  const int i16 = lane & 15, trow = 4 * h + (i16 >> 2), tu = 2 * ((lane >> 4) & 1) + ((i16 & 3) >> 1);
+  auto values = [&](int kc, int b) __attribute__((always_inline)) {
+    bf16x8 v;
 #pragma unroll
-    for (int b = 0; b < DB; ++b) {
-      bf16x8 v;
+    for (int e = 0; e < 2; ++e) {
+      const int row = 16 * kc + 8 * e + trow;
+      const s16x4 t = lds_read_tr16(lv + row * RB + 16 * ((4 * b + tu) ^ swizzle<DB>(row)) + 8 * (i16 & 1));
+      __builtin_memcpy((char*)&v + 8 * e, &t, 8);
+    }
+    return v;
+  };
+  if constexpr (!CAREFUL) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = 16 * kc + 8 * e + trow;
-        const s16x4 t = lds_read_tr16(lv + row * RB + 16 * ((4 * b + tu) ^ swizzle<DB>(row)) + 8 * (i16 & 1));
-        __builtin_memcpy((char*)&v + 8 * e, &t, 8);
+    for (int kc = 0; kc < 2 * KB; ++kc) {
+      bf16x8 p, rest;
+      weights(kc, p, rest);
+#pragma unroll
+      for (int b = 0; b < DB; ++b) {
+        const bf16x8 v = values(kc, b);
+        w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, w.o[b], 0, 0, 0);
+        if constexpr (FINE) w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, rest, w.o[b], 0, 0, 0);
       }
-      w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, w.o[b], 0, 0, 0);
-      if constexpr (FINE) w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, rest, w.o[b], 0, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int kc = 0; kc < 2 * KB; ++kc) {
+      bf16x8 p, rest, seen;
+      weights(kc, p, rest);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = 8 * (kc & 1) + j, key = 32 * (kc >> 1) + 8 * (i >> 2) + 4 * h + (i & 3);
+        // (a weight of exp(-inf) times an infinity is a NaN)
+        const float one = s[kc >> 1][i] * c == -INFINITY ? 16384.0f : 1.0f;
+        seen[j] = (__bf16)(key <= rel ? one : 0.0f);
+      }
+#pragma unroll
+      for (int b = 0; b < DB; ++b) {
+        __builtin_amdgcn_sched_barrier(0);
+        bf16x8 v = values(kc, b), odd;
+        const bool any = set_aside(v, odd);
+        w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, p, w.o[b], 0, 0, 0);
+        if constexpr (FINE) w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, rest, w.o[b], 0, 0, 0);
+        if (__any(any)) {
+          const f32x16 sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(odd, seen, f32x16{}, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w.o[b][i] += of_odd(sum[i]);
+        }
+      }
     }
   }
 }
 
-// Whether a value of keys from .. to is an infinity or a NaN, by a whole wave.
-__device__ __forceinline__ bool odd_values(const uint16_t* v, int64_t ldv, int hd, int from, int to) {
-  const int d = 4 * (threadIdx.x & 63);
-  bool odd = false;
-  for (int j = from; j <= to; ++j) {
-    if (d < hd) {
-      const uint2 u = *(const uint2*)(v + (int64_t)j * ldv + d);
-      odd = odd || (u.x & 0x7f80u) == 0x7f80u || (u.x & 0x7f800000u) == 0x7f800000u ||
-            (u.y & 0x7f80u) == 0x7f80u || (u.y & 0x7f800000u) == 0x7f800000u;
-    }
-  }
-  return __any(odd);
-}
-
-// A row by the definition, key by key: for rows whose sums met an infinity or a NaN
-// where a key that they do not see has such a value (a tile multiplies it by a weight
-// of 0; hidden keys' scores are replaced).  A whole wave takes the row; lane l has
-// columns 4 l .. 4 l + 3.
-struct Slow {
-  float o[4], mc, l;
-};
-__device__ __forceinline__ Slow slow_row(const uint16_t* q, const uint16_t* k, int64_t ldk,
-                                         const uint16_t* v, int64_t ldv, int hd, int begin, int end,
-                                         float c) {
-  const int lane = threadIdx.x & 63, d = 4 * lane;
-  const bool in = d < hd;
-  Slow r = {{0.0f, 0.0f, 0.0f, 0.0f}, NO_MAX, 0.0f};
-  float qv[4] = {};
-  if (in) {
-    for (int i = 0; i < 4; ++i) qv[i] = bf16_bits_to_float(q[d + i]);
-  }
-  for (int j = begin; j < end; ++j) {
-    float s = 0.0f, x[4] = {};
-    if (in) {
-      for (int i = 0; i < 4; ++i) {
-        s = fmaf(qv[i], bf16_bits_to_float(k[(int64_t)j * ldk + d + i]), s);
-        x[i] = bf16_bits_to_float(v[(int64_t)j * ldv + d + i]);
-      }
-    }
-    for (int o = 1; o < 64; o *= 2) s += __shfl_xor(s, o);
-    s *= c;
-    if (s > r.mc) {
-      const float f = exp2_of(r.mc - s);
-      r.mc = s, r.l *= f;
-      for (int i = 0; i < 4; ++i) r.o[i] *= f;
-    }
-    const float p = exp2_of(s - r.mc);
-    r.l += p;
-    for (int i = 0; i < 4; ++i) r.o[i] = fmaf(p, x[i], r.o[i]);
-  }
-  return r;
+template <int DB>
+__device__ __forceinline__ bool finite(const Rows<DB>& w) {
+  float t = w.l * 0.0f;
+#pragma unroll
+  for (int b = 0; b < DB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t = fmaf(w.o[b][i], 0.0f, t);
+  return t == 0.0f;
 }
 
 struct Grid {
@@ -285,42 +321,37 @@ struct Grid {
   float2* stat;  // maximum and sum [tq][hq][splits]
 };
 
+// What a row's columns are multiplied with: nothing for a row that sees no key, NaN for
+// one whose sum is NaN, or 0 with keys that it sees.
+__device__ __forceinline__ float inverse(float l, bool sees) {
+  return l > 0.0f ? 1.0f / l : sees ? NAN : l;
+}
+
 // Four columns of a row (query, head), finished or as a part.
 __device__ __forceinline__ void store4(const AttnArgs& a, const Grid& g, int split, int64_t query,
-                                       int head, int d, const float o[4], float mc, float l,
-                                       float inv) {
+                                       int head, int d, const float o[4], float mc, float l, bool sees) {
   if (d >= a.hd) return;
   if (g.splits == 1) {
+    const float inv = inverse(l, sees);
     *(bf16x4*)(a.out + query * a.ldo + head * a.hso + d) =
         bf16x4{(__bf16)(o[0] * inv), (__bf16)(o[1] * inv), (__bf16)(o[2] * inv), (__bf16)(o[3] * inv)};
   } else {
     const int64_t row = query * a.hq + head;
     *(float4*)(g.part + (split * a.tq * a.hq + row) * a.hd + d) = make_float4(o[0], o[1], o[2], o[3]);
-    if (d == 0) g.stat[row * g.splits + split] = make_float2(mc, l);
+    // (a maximum of -inf: it sees keys, and weighs none)
+    if (d == 0) g.stat[row * g.splits + split] = make_float2(sees && l == 0.0f ? -INFINITY : mc, l);
   }
 }
 
-__device__ __forceinline__ bool finite4(const f32x16& v) {
-  float t = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) t = fmaf(v[i], 0.0f, t);
-  return t == 0.0f;
-}
-
-// The wave's 32 rows leave: lane l's is `row` of the sequence (query, head), with
-// l the whole row's sum and o its columns; lim: the last key that it sees; reach: the
-// end of the tiles that the wave took.
+// The wave's 32 rows leave: lane l's is `row` of the sequence (query, head), with l the
+// whole row's sum and o its columns; sees: whether it sees a key of the wave's (the
+// scores of those that it sees may all be -inf: its weights are then 0 / 0).
 template <int DB>
-__device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Place& p, int group,
-                                      int kvh, bool live, int query, int head, int lim, int split,
-                                      int begin, int end, int64_t reach, float c, const f32x16 (&o)[DB],
-                                      float mc, float l, char* room) {
+__device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Place& p, bool live, int query,
+                                      int head, int split, bool sees, const f32x16 (&o)[DB], float mc, float l,
+                                      char* room) {
   constexpr int RB = 64 * DB;
   const int lane = threadIdx.x & 63, h = lane >> 5, l32 = lane & 31;
-  const float inv = l > 0.0f ? 1.0f / l : l;  // (a NaN stays)
-  bool ok = l - l == 0.0f;
-#pragma unroll
-  for (int b = 0; b < DB; ++b) ok = ok && finite4(o[b]);
   if (g.splits > 1) {
     if (live) {
 #pragma unroll
@@ -328,46 +359,31 @@ __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Pl
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float t[4] = {o[b][i], o[b][i + 1], o[b][i + 2], o[b][i + 3]};
-          store4(a, g, split, p.q0 + query, head, 32 * b + 2 * i + 4 * h, t, mc, l, inv);
+          store4(a, g, split, p.q0 + query, head, 32 * b + 2 * i + 4 * h, t, mc, l, sees);
         }
     }
-  } else {
-    // by way of LDS (the wave's own 32 RB bytes), so that whole rows are stored: in
-    // pieces of 8 bytes a row apart the stores took 4 us of a workgroup's time
-    constexpr int SW = DB % 2 == 0 ? 7 : 3;  // units change places inside their eight, or four
-    __asm__ volatile("" ::: "memory");
-#pragma unroll
-    for (int b = 0; b < DB; ++b)
-#pragma unroll
-      for (int i = 0; i < 16; i += 4)
-        *(bf16x4*)(room + l32 * RB + 16 * ((4 * b + (i >> 2)) ^ (l32 & SW)) + 8 * h) =
-            bf16x4{(__bf16)(o[b][i] * inv), (__bf16)(o[b][i + 1] * inv), (__bf16)(o[b][i + 2] * inv),
-                   (__bf16)(o[b][i + 3] * inv)};
-    const int64_t at = live ? (p.q0 + query) * a.ldo + head * a.hso : -1;
-    __asm__ volatile("" ::: "memory");  // the wave's LDS accesses keep their order
-#pragma unroll
-    for (int j = 0; j < 2 * DB; ++j) {
-      const int i = 64 * j + lane, r = i / (4 * DB), u = (i - r * 4 * DB) ^ (r & SW);
-      const uint4 v = *(const uint4*)(room + 16 * i);
-      const int64_t to = __shfl(at, r);
-      if (to >= 0 && 8 * u < a.hd) *(uint4*)(a.out + to + 8 * u) = v;
-    }
-  }
-  if (!a.causal) return;
-  uint64_t bad = __ballot(live && !ok && lim < p.lk - 1);
-  uint32_t rest = (uint32_t)bad | (uint32_t)(bad >> 32);
-  if (!rest || !odd_values(a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd,
-                           max(__builtin_amdgcn_readlane(lim, 0) + 1, begin), (int)min(reach, (int64_t)p.lk) - 1))
     return;
-  while (rest) {
-    const int r = __builtin_ctz(rest);
-    rest &= rest - 1;
-    const int64_t qi = p.q0 + __builtin_amdgcn_readlane(query, r);
-    const int hr = __builtin_amdgcn_readlane(head, r), last = __builtin_amdgcn_readlane(lim, r) + 1;
-    const Slow s = slow_row(a.q + qi * a.ldq + hr * a.hsq,
-                            a.k + p.start * a.ldk + kvh * a.hsk, a.ldk,
-                            a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd, begin, min(end, last), c);
-    store4(a, g, split, qi, hr, 4 * lane, s.o, s.mc, s.l, s.l > 0.0f ? 1.0f / s.l : s.l);
+  }
+  // by way of LDS (the wave's own 32 RB bytes), so that whole rows are stored: in
+  // pieces of 8 bytes a row apart the stores took 4 us of a workgroup's time
+  const float inv = inverse(l, sees);
+  constexpr int SW = DB % 2 == 0 ? 7 : 3;  // units change places inside their eight, or four
+  __asm__ volatile("" ::: "memory");
+#pragma unroll
+  for (int b = 0; b < DB; ++b)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *(bf16x4*)(room + l32 * RB + 16 * ((4 * b + (i >> 2)) ^ (l32 & SW)) + 8 * h) =
+          bf16x4{(__bf16)(o[b][i] * inv), (__bf16)(o[b][i + 1] * inv), (__bf16)(o[b][i + 2] * inv),
+                 (__bf16)(o[b][i + 3] * inv)};
+  const int64_t at = live ? (p.q0 + query) * a.ldo + head * a.hso : -1;
+  __asm__ volatile("" ::: "memory");  // the wave's LDS accesses keep their order
+#pragma unroll
+  for (int j = 0; j < 2 * DB; ++j) {
+    const int i = 64 * j + lane, r = i / (4 * DB), u = (i - r * 4 * DB) ^ (r & SW);
+    const uint4 v = *(const uint4*)(room + 16 * i);
+    const int64_t to = __shfl(at, r);
+    if (to >= 0 && 8 * u < a.hd) *(uint4*)(a.out + to + 8 * u) = v;
   }
 }
 
@@ -396,7 +412,7 @@ __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Pl
 constexpr int BM = 128, BK = 64;
 
 template <int DB>
-__global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Grid g) {
+__global__ __launch_bounds__(256, DB == 2 ? 4 : DB <= 4 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Grid g) {
   constexpr int RB = 64 * DB, TILE = BK * RB;  // bytes of a row and of a tile
   extern __shared__ __attribute__((aligned(1024))) char lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -450,22 +466,35 @@ __global__ __launch_bounds__(256, DB <= 4 ? 2 : 1) void attention_rows_kernel(At
   // the last key that a row sees: the lane's, the wave's first and last
   const int lim = a.causal ? min(query + back, p.lk - 1) : p.lk - 1;
   const int lim_first = __builtin_amdgcn_readlane(lim, 0), lim_last = __builtin_amdgcn_readlane(lim, 31);
-  // (by the keys that are left: a key's number may be near 2^31)
-  for (int left = end - begin, buf = 0; left > 0; left -= BK, buf ^= 1) {
-    const int key0 = end - left;
-    // this tile has landed, and the other buffer is read
-    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (left > BK) issue(key0 + BK, buf ^ 1);
-    if (key0 > lim_last) continue;
-    const char* const t = lds + buf * 2 * TILE;
-    tile_step<DB, BK / 32, false>(w, t, t + TILE, c, lim - key0, lim_first - key0 < BK - 1);
-  }
-  const float l = w.l + other_half(w.l);
+  auto over_keys = [&](auto careful) __attribute__((always_inline)) {
+    // (by the keys that are left: a key's number may be near 2^31)
+    for (int left = end - begin, buf = 0; left > 0; left -= BK, buf ^= 1) {
+      const int key0 = end - left;
+      // this tile has landed, and the other buffer is read
+      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();
+      if (left > BK) issue(key0 + BK, buf ^ 1);
+      if (key0 > lim_last) continue;
+      const char* const t = lds + buf * 2 * TILE;
+      tile_step<DB, BK / 32, false, decltype(careful)::value>(w, t, t + TILE, c, lim - key0,
+                                                              lim_first - key0 < BK - 1, a.hd);
+    }
+  };
+  over_keys(std::false_type());
+  float l = w.l + other_half(w.l);
+  int* const odd = (int*)(lds + 4 * TILE);
+  const bool mine = __any(!finite(w));
+  if (lane == 0) odd[wave] = mine;
   __syncthreads();  // the tiles are read
-  const int64_t reach = begin + ((int64_t)max(min(end - 1, lim_last) - begin + 1, 0) + BK - 1) / BK * BK;
-  leave<DB>(a, g, p, group, kvh, row0 + l32 < p.rows, query, head, lim, split, begin, end, reach, c, w.o, w.mc,
-            l, lds + wave * 32 * RB);
+  if (__builtin_expect(odd[0] | odd[1] | odd[2] | odd[3], 0)) {
+    no_keys(w);
+    if (begin < end) issue(begin, 0);
+    over_keys(std::true_type());
+    l = w.l + other_half(w.l);
+    __syncthreads();
+  }
+  leave<DB>(a, g, p, row0 + l32 < p.rows, query, head, split, min(lim, end - 1) >= begin, w.o, w.mc, l,
+            lds + wave * 32 * RB);
 }
 
 // Few rows: one tile of 32 rows, the keys in tiles of 32 that four waves (two,
@@ -527,27 +556,36 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
   start_rows<DB>(w, a.q + (p.q0 + query) * a.ldq + head * a.hsq, a.hd, h);
   const int lim = a.causal ? min(query + back, p.lk - 1) : p.lk - 1;
   const int lim_first = __builtin_amdgcn_readlane(lim, 0);
-  for (int left = mine_left, buf = 0; left > 0; left -= FK * FW, buf ^= 1) {
-    const int key0 = end - left;
-    // every read of the other buffer has returned before it is written again
-    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (left > FK * FW) {
-      issue(key0 + FK * FW, buf ^ 1);
-      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PIECES) : "memory");
-    } else {
-      __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  auto over_keys = [&](auto careful) __attribute__((always_inline)) {
+    for (int left = mine_left, buf = 0; left > 0; left -= FK * FW, buf ^= 1) {
+      const int key0 = end - left;
+      // every read of the other buffer has returned before it is written again
+      __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (left > FK * FW) {
+        issue(key0 + FK * FW, buf ^ 1);
+        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * PIECES) : "memory");
+      } else {
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      }
+      const char* const t = mine + buf * 2 * TILE;
+      tile_step<DB, FK / 32, true, decltype(careful)::value>(w, t, t + TILE, c, lim - key0,
+                                                             lim_first - key0 < FK - 1, a.hd);
     }
-    const char* const t = mine + buf * 2 * TILE;
-    tile_step<DB, FK / 32, true>(w, t, t + TILE, c, lim - key0, lim_first - key0 < FK - 1);
+  };
+  over_keys(std::false_type());
+  if (__builtin_expect(__any(!finite(w)), 0)) {
+    no_keys(w);
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // (the tiles are read)
+    issue(end - mine_left, 0);
+    over_keys(std::true_type());
   }
   const float l = w.l + other_half(w.l);
   // The waves' sums meet in LDS, where a thread takes four columns of a row: rows
   // that are not there (28 of 32 for a token of four heads) cost nothing.
   constexpr int PITCH = 32 * DB + 4;
-  static_assert(FW * 256 + 128 + FW * FM * PITCH * 4 <= FW * 4 * TILE, "in the tiles' place");
+  static_assert(FW * 256 + FW * FM * PITCH * 4 <= FW * 4 * TILE, "in the tiles' place");
   float2* const stat = (float2*)lds;                             // [FW][32]
-  int* const bad = (int*)(lds + FW * 256);                       // [32]
-  float* const parts = (float*)(lds + FW * 256 + 128);           // [FW][32][PITCH]
+  float* const parts = (float*)(lds + FW * 256);                 // [FW][32][PITCH]
   const int live = min(FM, p.rows - p.row0);
   __syncthreads();  // the tiles are read
   if (l32 < live) {
@@ -559,7 +597,6 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
       for (int i = 0; i < 16; i += 4)
         *(float4*)(mine + 32 * b + 2 * i) = make_float4(w.o[b][i], w.o[b][i + 1], w.o[b][i + 2], w.o[b][i + 3]);
   }
-  if (threadIdx.x < FM) bad[threadIdx.x] = 0;
   __syncthreads();
   const int per = a.hd / 4;
   for (int at = threadIdx.x; at < live * per; at += 64 * FW) {
@@ -576,27 +613,10 @@ __global__ __launch_bounds__(64 * few_waves(DB), 1) void attention_keys_kernel(A
       o[0] = fmaf(v.x, f, o[0]), o[1] = fmaf(v.y, f, o[1]);
       o[2] = fmaf(v.z, f, o[2]), o[3] = fmaf(v.w, f, o[3]);
     }
-    const float odd = fmaf(o[0], 0.0f, fmaf(o[1], 0.0f, fmaf(o[2], 0.0f, fmaf(o[3], 0.0f, sum * 0.0f))));
-    if (odd != 0.0f) bad[r] = 1;
     const int at_row = p.row0 + r, at_query = (int)((uint32_t)at_row / (uint32_t)group);
+    const int last = a.causal ? min(at_query + back, p.lk - 1) : p.lk - 1;
     store4(a, g, split, p.q0 + at_query, kvh * group + at_row - at_query * group, d, o, mc, sum,
-           sum > 0.0f ? 1.0f / sum : sum);
-  }
-  if (!a.causal) return;
-  __syncthreads();
-  const int64_t reach = begin + ((int64_t)(end - begin) + FK - 1) / FK * FK;  // the end of the tiles
-  for (int r = wave; r < live; r += FW) {
-    const int at_row = p.row0 + r, at_query = (int)((uint32_t)at_row / (uint32_t)group);
-    const int last = min(at_query + back, p.lk - 1);
-    if (!bad[r] || last >= p.lk - 1 ||
-        !odd_values(a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd, max(last + 1, begin),
-                    (int)min(reach, (int64_t)p.lk) - 1))
-      continue;
-    const int64_t qi = p.q0 + at_query;
-    const int hr = kvh * group + at_row - at_query * group;
-    const Slow t = slow_row(a.q + qi * a.ldq + hr * a.hsq, a.k + p.start * a.ldk + kvh * a.hsk, a.ldk,
-                            a.v + p.start * a.ldv + kvh * a.hsv, a.ldv, a.hd, begin, min(end, last + 1), c);
-    store4(a, g, split, qi, hr, 4 * lane, t.o, t.mc, t.l, t.l > 0.0f ? 1.0f / t.l : t.l);
+           min(last, end - 1) >= begin);
   }
 }
 
@@ -614,6 +634,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, Grid g)
   const int first = a.cu_q[0], last = a.cu_q[a.batch];
   float o[4] = {};
   float mc = lane < g.splits ? st.x : NO_MAX;
+  const bool blind = __any(mc == -INFINITY);  // sees keys, whose scores are -inf
 #pragma unroll
   for (int i = 1; i < 64; i *= 2) mc = fmaxf(mc, __shfl_xor(mc, i));
   const float f = lane < g.splits ? exp2_of(st.x - mc) : 0.0f;
@@ -641,7 +662,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a, Grid g)
 #pragma unroll
     for (int k = 0; k < 4; ++k) sum[k] += __shfl(o[k], (lane + i * per) & 63);
   if (sub != 0 || query < first || query >= last) return;
-  const float inv = l > 0.0f ? 1.0f / l : l;
+  const float inv = inverse(l, l != 0.0f || blind);
   *(bf16x4*)(a.out + query * a.ldo + head * a.hso + d) =
       bf16x4{(__bf16)(sum[0] * inv), (__bf16)(sum[1] * inv), (__bf16)(sum[2] * inv), (__bf16)(sum[3] * inv)};
 }
@@ -712,7 +733,7 @@ hipError_t launch(const AttnArgs& a, const Plan& p, hipStream_t stream) {
     hipLaunchKernelGGL((attention_keys_kernel<DB>), grid, dim3(64 * FW), (size_t)FW * 4 * FK * 64 * DB,
                        stream, a, p.g);
   } else {
-    hipLaunchKernelGGL((attention_rows_kernel<DB>), grid, dim3(256), (size_t)4 * BK * 64 * DB, stream,
+    hipLaunchKernelGGL((attention_rows_kernel<DB>), grid, dim3(256), (size_t)4 * BK * 64 * DB + 64, stream,
                        a, p.g);
   }
   return hipGetLastError();
