@@ -431,7 +431,8 @@ size_t gptq_w4a8_workspace(int64_t m, int64_t d_out, int64_t d_in, int group_siz
  * Products are exact; sums, the group scaling and everything behind them are
  * float32, rounded once to Y's type.  The order of every sum is fixed: the same
  * inputs give the same bits.  An infinity or a NaN in a row of X does not reach
- * other rows.
+ * other rows; its own gets what the formula gives (an infinity times a weight of 0
+ * is a NaN).
  * ------------------------------------------------------------------------- */
 typedef enum {
   GPTQ_ACT_NONE = 0,

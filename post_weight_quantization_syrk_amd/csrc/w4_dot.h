@@ -167,22 +167,31 @@ __global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, 
     for (int s = 0; s < ks; ++s) v += red[row * ks + s];
     return v;
   };
+  // (whole waves go round, as right_odd_sums wants them)
+  const int first = threadIdx.x & ~63;
   if constexpr (E::gated) {
-    for (int p = threadIdx.x; p < rows / 2; p += blockDim.x) {
+    for (int p0 = first; p0 < rows / 2; p0 += blockDim.x) {
+      const int p = p0 + lane;
       const int64_t u = (int64_t)blockIdx.x * (rows / 2) + p;
-      if (u < epi.e.F) finish<true>(epi.e, 0, u, summed(2 * p), summed(2 * p + 1));
+      const bool in = p < rows / 2 && u < epi.e.F;
+      float v0 = in ? summed(2 * p) : 0.0f, v1 = in ? summed(2 * p + 1) : 0.0f;
+      right_odd_sums(terms_of(a), in, 0, u, v0);
+      right_odd_sums(terms_of(a), in, 0, epi.e.F + u, v1);
+      if (in) finish<true>(epi.e, 0, u, v0, v1);
     }
     return;
   }
-  for (int row = threadIdx.x; row < rows; row += blockDim.x) {
+  for (int row0 = first; row0 < rows; row0 += blockDim.x) {
+    const int row = row0 + lane;
     const int64_t n = (int64_t)blockIdx.x * rows + row;
-    float v = summed(row);
+    const bool in = row < rows && n < a.n;
+    float v = in ? summed(row) : 0.0f;
     if constexpr (I8) v *= a.sx[0];
-    if (n < a.n) {
-      if constexpr (E::linear)
-        finish<false>(epi.e, 0, n, v, 0.0f);
-      else
-        a.y[n] = v;
+    if constexpr (E::linear) {
+      right_odd_sums(terms_of(a), in, 0, n, v);
+      if (in) finish<false>(epi.e, 0, n, v, 0.0f);
+    } else if (in) {
+      a.y[n] = v;
     }
   }
 }

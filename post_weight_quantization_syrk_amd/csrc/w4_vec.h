@@ -63,6 +63,8 @@ struct VecArgs {
   int slots;              // k slots of a workgroup, at most
 };
 
+__host__ __device__ inline Terms terms_of(const VecArgs& a) { return {a.x, a.ldx, a.q, a.s16, a.z16, a.k, a.ng}; }
+
 // How the sums leave: as they are (times sx), or finished by an epilogue.  Gated,
 // weight rows u and F + u belong together: a workgroup's row tiles are pairs of
 // tiles, first of gate rows, then of the up rows that go with them.
@@ -555,8 +557,11 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
       for (int q = wave; q < PER / 2; q += waves) {
         const int i = q & 3, t = (q >> 2) % NT, r = (q >> 2) / NT * 2;
         const int token = 16 * t + 4 * h + i, u = row_at(16 * r + l16);
-        const float v0 = summed((r * NT + t) * 4 + i), v1 = summed(((r + 1) * NT + t) * 4 + i);
-        if (token < a.m && u < epi.e.F) finish<true>(epi.e, token, u, v0, v1);
+        const bool in = token < a.m && u < epi.e.F;
+        float v0 = summed((r * NT + t) * 4 + i), v1 = summed(((r + 1) * NT + t) * 4 + i);
+        right_odd_sums(terms_of(a), in, token, u, v0);
+        right_odd_sums(terms_of(a), in, token, epi.e.F + u, v1);
+        if (in) finish<true>(epi.e, token, u, v0, v1);
       }
       return;
     }
@@ -567,6 +572,9 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
     const int token = 16 * t + 4 * h + i, n = row_at(16 * r + l16);
     bool in = token < a.m && n < a.n;
     if constexpr (E::gated) in = in && n - (r & 1) * epi.e.F < epi.e.F;
+    if constexpr (E::linear && !E::gated) {
+      if (a.splits == 1) right_odd_sums(terms_of(a), in, token, n, v);
+    }
     if (in) {
       if (I8 && a.splits == 1) v *= a.sx[token];
       if constexpr (E::linear && !E::gated) {
@@ -731,7 +739,7 @@ hipError_t vec_finish_launch(const VecArgs& a, int G, void* ws, const Epilogue& 
   const VecPlan p = vec_plan(I8, a.m, a.n, a.k, G, true, GATED);
   const hipError_t e = vec_launch_parts<I8>(a, p, G, ws, Finished<GATED>{epi}, stream);
   if (e != hipSuccess || p.splits == 1) return e;
-  return join_finish_launch<GATED>((const float*)ws, a.m, a.n, p.splits, epi, stream);
+  return join_finish_launch<GATED>((const float*)ws, a.m, a.n, p.splits, epi, terms_of(a), stream);
 }
 
 }  // namespace w4vec

@@ -182,6 +182,8 @@ __device__ __forceinline__ void lds_barrier() {
   __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+__device__ const uint4 zeros = {};  // a unit of X past the rows' end
+
 // Four waves side by side, each all 32 MI rows of X by 32 weight rows: a wave
 // takes the codes of its own weight rows apart, and none twice.  G: group size,
 // 0 for one group per row.
@@ -235,11 +237,14 @@ __device__ __forceinline__ void tile_product(const Args& a, char* lds, int64_t m
       for (int j = 0; j < MI; ++j) w4vec::dma16_from(xb, xoff[j], dst + (MI * wave + j) * 1024);
       if constexpr (!WIDE) w4vec::dma16_from(qb, qrow + qu, dst + ABYTES + wave * 1024);
     } else {
-      // a last chunk that is not whole: units past the row's end are copies
+      // a last chunk that is not whole: past the rows' end X is zeros (a copy might be
+      // infinite, and a weight of 0 times that is a NaN), words are copies
       const int xmost = 2 * a.K - 16 - c * 2 * KCH, qmost = a.K / 2 - 16 - c * (KCH / 2);
 #pragma unroll
-      for (int j = 0; j < MI; ++j)
-        w4vec::dma16_from(xb, xoff[j] - (uint32_t)max(xu(j) - xmost, 0), dst + (MI * wave + j) * 1024);
+      for (int j = 0; j < MI; ++j) {
+        const char* const from = xb + xoff[j];
+        w4vec::dma16_at(xu(j) <= xmost ? from : (const char*)&zeros, dst + (MI * wave + j) * 1024);
+      }
       if constexpr (!WIDE) w4vec::dma16_from(qb, qrow + min(qu, qmost), dst + ABYTES + wave * 1024);
     }
   };
@@ -611,7 +616,7 @@ hipError_t tiles_launch(const Args& a, int G, hipStream_t stream) {
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  return join_finish_launch<GATED>(a.part, a.M, a.N, a.splits, a.e, stream);
+  return join_finish_launch<GATED>(a.part, a.M, a.N, a.splits, a.e, Terms{}, stream);
 }
 
 }  // namespace
