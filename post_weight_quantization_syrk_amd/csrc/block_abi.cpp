@@ -154,7 +154,7 @@ int gptq_qk_norm_rope(const void* Q, int64_t ldq, int64_t hsq, const void* K, in
   a.m = m, a.hq = hq, a.hk = hk, a.hd = hd, a.rot = rot_dim;
   a.positions = positions, a.inv_freq = inv_freq;
   a.q_weight = q_weight, a.k_weight = k_weight;
-  a.w_f32 = w_dtype == GPTQ_F32, a.interleaved = interleaved != 0, a.eps = (float)eps;
+  a.w_f32 = w_dtype == GPTQ_F32, a.interleaved = interleaved != 0, a.eps = eps;
   a.slots = slots, a.kv_rows = kv_rows;
   a.q_out = (uint16_t*)Q_out, a.k_out = (uint16_t*)K_out, a.v_out = (uint16_t*)V_out;
   a.ldqo = ldqo, a.hsqo = hsqo, a.ldko = ldko, a.hsko = hsko, a.ldvo = ldvo, a.hsvo = hsvo;

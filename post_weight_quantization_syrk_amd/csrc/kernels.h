@@ -134,7 +134,7 @@ struct RopeArgs {
   const double* inv_freq;
   const void *q_weight, *k_weight;  // null: no norm
   bool w_f32, interleaved;
-  float eps;
+  double eps;
   const int64_t* slots;  // null: row t
   int64_t kv_rows;       // rows of k_out and v_out
   uint16_t *q_out, *k_out, *v_out;

@@ -147,8 +147,23 @@ __global__ __launch_bounds__(64 * WAVES, F32 ? 5 : 6) void qk_norm_rope_kernel(R
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(x0[i], x0[i], fmaf(x1[i], x1[i], ss));
     ss = head_sum<LPH>(ss);
+    float eps = (float)a.eps;
+    // squares past float32's end, or below its normal numbers where eps does not hide
+    // that: the head times a power of two, eps times its square (an infinity stays one)
+    const float up = ss / (float)a.hd + eps < 0x1p-90f ? 0x1p100f : ss > 3.4028235e38f ? 0x1p-70f : 1.0f;
+    if (__builtin_expect(__any(norm && up != 1.0f), 0)) {
+      const float k = norm ? up : 1.0f;
+      ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x0[i] *= k, x1[i] *= k;
+        ss = fmaf(x0[i], x0[i], fmaf(x1[i], x1[i], ss));
+      }
+      ss = head_sum<LPH>(ss);
+      eps = (float)(a.eps * k * k);
+    }
     if (norm) {
-      const float r = 1.0f / sqrtf(ss / (float)a.hd + a.eps);
+      const float r = 1.0f / sqrtf(ss / (float)a.hd + eps);
       const float* w = weights[is_q ? 0 : 1];
       // (units that are not there: their values are 0)
       const float* const w0 = w + 8 * min(u0, U - 1);
