@@ -22,8 +22,6 @@
 namespace gptq {
 namespace w4vec {
 
-constexpr int RUN = 2048;       // k per wave
-
 __device__ __forceinline__ float dot2(bf16x2 a, bf16x2 b, float c) {
   return __builtin_amdgcn_fdot2_f32_bf16(a, b, c, false);
 }
@@ -195,10 +193,6 @@ __global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, 
     }
   }
 }
-
-// One token, and a row of X that 16 waves hold.  (For two to four tokens the
-// registers of X leave too few waves: the kernel for a few tokens is faster.)
-inline bool dot_takes(int64_t m, int64_t k) { return m == 1 && k <= 16 * RUN; }
 
 // Rows per wave: few enough that the launch has some 8192 waves' rows at once.
 template <bool I8, class E = Plain>

@@ -24,15 +24,14 @@
 // 4096: 24 us, of which launches, a workgroup's start and end take two thirds.
 #include "common.h"
 #include "kernels.h"
+#include "linear_plan.h"
 #include "w4_dot.h"
-
-#include <algorithm>
 
 namespace gptq {
 
-namespace {
+using namespace linear;
 
-constexpr int KCH = 64;  // k per chunk: 128 bytes of a row of X, 32 of a weight row
+namespace {
 
 // Columns of a tile in the order in which it takes weight rows: gated, 32 gate
 // rows, then the 32 up rows that go with them.
@@ -43,29 +42,6 @@ __device__ __forceinline__ int64_t weight_row(int64_t c, int F) {
 template <bool GATED>
 __device__ __forceinline__ bool weight_row_in(int64_t c, int F) {
   return GATED ? (c >> 6) * 32 + (c & 31) < F : c < F;
-}
-
-// The weights in eight bits, for calls with many rows of X: q - z as e4m3, which
-// has every whole number up to 16 in magnitude, so that two leave for bf16 with one
-// operation and no zero is taken off again.  Panels of 32 columns x 64 k (2 KB),
-// chunk after chunk, 16-byte unit u of row r at u ^ (r / 4 mod 4), as the tiles
-// have them in LDS; columns past the last and k past the row's end are zeros.
-// Scales follow as float32 [ng][cols].  (57344 x 8192: 0.15 ms.)
-struct Wide {
-  int64_t cols;  // padded to whole tiles
-  int nch, ng;
-  size_t scales;  // byte offset
-  size_t bytes;
-};
-
-Wide wide_of(int64_t d_out, int64_t d_in, int group_size, bool gated) {
-  Wide w;
-  w.cols = ceil_div(gated ? ceil_div(d_out / 2, 32) * 64 : d_out, 256) * 256;
-  w.nch = (int)ceil_div(d_in, KCH);
-  w.ng = group_size == -1 ? 1 : (int)(d_in / group_size);
-  w.scales = (size_t)w.cols * w.nch * KCH;
-  w.bytes = w.scales + (size_t)w.cols * w.ng * 4;
-  return w;
 }
 
 template <bool GATED>
@@ -155,11 +131,6 @@ struct Args {
   int splits, per_split;  // of the chunks
 };
 
-// A wave's tile: up to 256 rows of X by 32 weight rows, or, of the wide weights,
-// 128 by 64.
-constexpr int blocks_n(bool wide) { return wide ? 2 : 1; }
-constexpr int most_m(bool wide) { return wide ? 4 : 8; }
-constexpr int tile_n(bool wide) { return 128 * blocks_n(wide); }
 constexpr int BLOCK = 8;  // groups whose scales a wave has in LDS
 constexpr int SCALES = 4 * BLOCK * 32 * 4;
 constexpr int LDS_BYTES = 80 * 1024;  // two workgroups on a CU
@@ -532,77 +503,6 @@ __global__ __launch_bounds__(256, 2) void linear_kernel(Args a) {
   if (n == 3) return tile_product<3, G, GATED, WIDE>(a, lds, m0, c0, split);
   if (n == 2) return tile_product<2, G, GATED, WIDE>(a, lds, m0, c0, split);
   tile_product<1, G, GATED, WIDE>(a, lds, m0, c0, split);
-}
-
-// Few tokens: the kernels that read the weights once for all of them, up to 16, and up
-// to 64 where the weights are not large.  Their vector work grows with every 16 tokens,
-// most with groups of 32, and past one round of workgroups nothing hides it (32 tokens,
-// groups of 32: 16384 x 8192 43 us, by tiles 37, but 8192 x 8192 22.5 and 26; 48: 11008
-// x 4096 27.5 and 27, 4096 x 4096 14 and 18; 64 tokens, groups of 64: 4096 x 11008 32
-// and 28, 4096 x 4096 20 and 20; groups of 128: 16384 x 8192 46 and 42; 48 tokens 39
-// and 40, 32 tokens 26 and 32).
-bool few_tokens(int64_t m, int64_t d_out, int64_t d_in, int group_size) {
-  if (m > 64) return false;
-  const int64_t sixteens = ceil_div(m, 16), codes = d_out * d_in;
-  return group_size == 32 ? codes * (sixteens - 1) < 80000000 : sixteens < 4 || codes < 45000000;
-}
-
-struct Plan {
-  bool wide;  // weights in eight bits first
-  int tiles_m, tiles_n;
-  int splits, per_split;
-  size_t part_off, bytes;
-};
-
-// Tiles, splits of k and the form of the weights by the least of a time in us,
-// fitted to some 300 launches of 128 to 4096 tokens through seven layers.  A chunk
-// takes a tile of b blocks of 32 rows `alone` where it has a CU to itself (up to
-// 256 workgroups) and `shared` where the CU has two (past 256 some have, with more
-// to wait for than the mean); where the chip is full its power is the bound, and
-// taking four bits apart in every tile costs a tenth more.  Making the weights wide
-// costs a launch and their bytes, splits their sums' bytes.
-// 515 tokens through 4099 x 11008, groups of 32: 92 us with three tiles of rows and
-// k in five (98 with five and three; 106 wide); 2048 tokens through 8192 x 8192: 333
-// us wide, 349 from four bits; 8192 tokens through 57344 x 8192: 7.0 and 7.6 ms.
-Plan plan_for(int64_t m, int64_t d_out, int64_t d_in, int group_size, bool gated) {
-  const int nch = (int)ceil_div(d_in, KCH);
-  const int64_t blocks = ceil_div(m, 32), cols = gated ? ceil_div(d_out / 2, 32) * 64 : d_out;
-  const bool g32 = group_size == 32;
-  Plan p = {};
-  double best = 0.0;
-  // (a launch's threads are below 2^32)
-  const bool may_widen = ceil_div(cols, 256) * 256 * (4 * nch) < (int64_t)1 << 31;
-  for (int wide = 0; wide < 1 + may_widen; ++wide) {
-    const int64_t tiles_n = ceil_div(cols, tile_n(wide));
-    int64_t before = 0;
-    for (int b = most_m(wide); b >= 1; --b) {
-      const int64_t tiles_m = ceil_div(blocks, b);
-      if (tiles_m == before) continue;  // the larger b gave the same tiles
-      before = tiles_m;
-      const int most = (int)ceil_div(blocks, tiles_m);
-      const double alone = wide ? 0.26 + 0.276 * most : 0.32 + (g32 ? 0.173 : 0.146) * most;
-      const double two = wide ? 0.31 + 0.511 * most : g32 ? 0.57 + 0.233 * most : 0.47 + 0.224 * most;
-      for (int splits = 1; splits <= 8 && (splits == 1 || splits * 4 <= nch); ++splits) {
-        const int64_t groups = tiles_m * tiles_n * splits, last = groups % 512;
-        const double shared = std::max(alone, !wide && groups >= 512 ? 1.1 * two : two);
-        const double end = last == 0 ? 0.0
-                           : last <= 256 ? alone
-                                         : alone + (shared - alone) * (0.55 + 0.45 * (double)(last - 256) / 256);
-        double us = (double)ceil_div(nch, splits) * ((double)(groups / 512) * shared + end);
-        if (splits > 1) us += 4.0e-6 * (double)(m * d_out) * (splits + 1) / 3.0;
-        if (wide) us += 4.0 + 1.5e-6 * (double)(cols * d_in) / 5.0;
-        if (best == 0.0 || us < best) {
-          best = us;
-          p.wide = wide, p.tiles_m = (int)tiles_m, p.tiles_n = (int)tiles_n, p.splits = splits;
-        }
-      }
-    }
-  }
-  p.per_split = (int)ceil_div(nch, p.splits);
-  p.splits = (int)ceil_div(nch, p.per_split);
-  p.part_off = p.wide ? ceil_div(wide_of(d_out, d_in, group_size, gated).bytes, 256) * 256 : 0;
-  p.bytes = p.part_off + (p.splits > 1 ? (size_t)p.splits * m * d_out * 4 : 0);
-  return p;
 }
 
 template <bool GATED, bool WIDE>
