@@ -165,32 +165,50 @@ __global__ __launch_bounds__(1024) void w4_dot_kernel(VecArgs a, int G, int ks, 
     for (int s = 0; s < ks; ++s) v += red[row * ks + s];
     return v;
   };
-  // (whole waves go round, as right_odd_sums wants them)
+  // whole waves go round; sums that are not finite in a second one
   const int first = threadIdx.x & ~63;
-  if constexpr (E::gated) {
-    for (int p0 = first; p0 < rows / 2; p0 += blockDim.x) {
-      const int p = p0 + lane;
-      const int64_t u = (int64_t)blockIdx.x * (rows / 2) + p;
-      const bool in = p < rows / 2 && u < epi.e.F;
-      float v0 = in ? summed(2 * p) : 0.0f, v1 = in ? summed(2 * p + 1) : 0.0f;
-      right_odd_sums(terms_of(a), in, 0, u, v0);
-      right_odd_sums(terms_of(a), in, 0, epi.e.F + u, v1);
-      if (in) finish<true>(epi.e, 0, u, v0, v1);
+  auto finished = [&](auto second) __attribute__((always_inline)) {
+    constexpr bool SECOND = decltype(second)::value;
+    bool odd = false;
+    if constexpr (E::gated) {
+      for (int p0 = first; p0 < rows / 2; p0 += blockDim.x) {
+        const int p = p0 + lane;
+        const int64_t u = (int64_t)blockIdx.x * (rows / 2) + p;
+        bool now = p < rows / 2 && u < epi.e.F;
+        float v0 = now ? summed(2 * p) : 0.0f, v1 = now ? summed(2 * p + 1) : 0.0f;
+        const bool fin = is_finite(v0) && is_finite(v1);
+        odd = odd || !fin;
+        now = now && fin != SECOND;
+        if constexpr (SECOND) {
+          right_odd_sums(terms_of(a), now, 0, u, v0);
+          right_odd_sums(terms_of(a), now, 0, epi.e.F + u, v1);
+        }
+        if (now) finish<true>(epi.e, 0, u, v0, v1);
+      }
+    } else if constexpr (E::linear) {
+      for (int row0 = first; row0 < rows; row0 += blockDim.x) {
+        const int row = row0 + lane;
+        const int64_t n = (int64_t)blockIdx.x * rows + row;
+        bool now = row < rows && n < a.n;
+        float v = now ? summed(row) : 0.0f;
+        const bool fin = is_finite(v);
+        odd = odd || !fin;
+        now = now && fin != SECOND;
+        if constexpr (SECOND) right_odd_sums(terms_of(a), now, 0, n, v);
+        if (now) finish<false>(epi.e, 0, n, v, 0.0f);
+      }
     }
+    return __any(odd);
+  };
+  if constexpr (E::linear) {
+    if (__builtin_expect(finished(std::false_type()), 0)) finished(std::true_type());
     return;
   }
-  for (int row0 = first; row0 < rows; row0 += blockDim.x) {
-    const int row = row0 + lane;
+  for (int row = threadIdx.x; row < rows; row += blockDim.x) {
     const int64_t n = (int64_t)blockIdx.x * rows + row;
-    const bool in = row < rows && n < a.n;
-    float v = in ? summed(row) : 0.0f;
+    float v = summed(row);
     if constexpr (I8) v *= a.sx[0];
-    if constexpr (E::linear) {
-      right_odd_sums(terms_of(a), in, 0, n, v);
-      if (in) finish<false>(epi.e, 0, n, v, 0.0f);
-    } else if (in) {
-      a.y[n] = v;
-    }
+    if (n < a.n) a.y[n] = v;
   }
 }
 
