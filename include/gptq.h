@@ -528,9 +528,9 @@ int gptq_qk_norm_rope(const void* Q, int64_t ldq, int64_t hsq, const void* K, in
  * values (values V past some 2^120 / lk overflow the sums).  The order of every sum is
  * fixed.  Keys and values that a query does not see do not reach it, whatever they
  * hold; of an infinity or a NaN that it sees it gets what the formula gives, in a
- * value's column alone (rows with one are gone over twice: some four times the time).
- * A query whose scores are all -inf is 0 / 0, NaN.  Finite scores have magnitudes
- * below 2^30 (scaled): past that one step of float32 is a factor of exp(64).
+ * value's column alone (rows with one are gone over twice: up to eight times the
+ * time).  A query whose scores are all -inf is 0 / 0, NaN.  Scaled scores are below
+ * 2^30 in magnitude: past that a step of float32 is more than the weights span.
  * total_q * hq / 32 + batch * hk is bounded by 2^23 (GPTQ_EUNSUPPORTED past it).
  * ------------------------------------------------------------------------- */
 int gptq_attention(const void* Q, int64_t ldq, int64_t hsq, const void* K, int64_t ldk, int64_t hsk,

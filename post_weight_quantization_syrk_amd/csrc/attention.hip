@@ -184,15 +184,19 @@ __device__ __forceinline__ float of_odd(float sum) {
 
 // One tile of 32 KB keys, in LDS at lk and lv.  rel: the last key that the lane's
 // row sees, less the tile's first; masked: some row does not see all of them.  FINE:
-// the weights in two bf16 parts, a rounding of 2^-17 in place of 2^-8 (one token's
-// error against 64 bits 0.0018 -> 0.0016; 10.7 -> 11.1 us, nothing where memory is the
-// bound; with many rows half as many products more).
+// the weights in two bf16 parts, a rounding of 2^-17 in place of 2^-8.  Few rows have
+// it: one token's error against 64 bits 0.0018 -> 0.0016, in 11.1 us for 10.7, nothing
+// where memory is the bound.  Many rows do not: with it 16384 tokens are 0.0014 off in
+// place of 0.0017 (0.0014 is the rounding of the output alone) and take 6.03 ms in place
+// of 4.26, seven prompts 0.00116 for 0.00133 and 176 us for 133.
 //
 // CAREFUL: for rows whose sums came out infinite or NaN.  A product with 0 is NaN where
 // the other side is odd: a value that the row does not see (its weight is 0), a value
 // that it sees (the second part of its weight may be 0, or of the other sign), a key's
 // last unit in place of columns past hd (the query's are 0 there).  So those columns are
-// taken as 0, and odd values apart from the others, by what the row sees of them.
+// taken as 0, and odd values apart from the others, by what the row sees of them.  (A
+// prompt of 2048 tokens whose values are all NaN, 32 heads over 8: 0.50 ms, clean 0.064;
+// rows gone over again key by key took 25.)
 template <int DB, int KB, bool FINE, bool CAREFUL>
 __device__ __forceinline__ void tile_step(Rows<DB>& w, const char* lk, const char* lv, float c,
                                           int rel, bool masked, int hd) {
@@ -391,11 +395,12 @@ __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Pl
 // of them; two workgroups on a CU (heads up to 128), so that one's products run while
 // the other forms its weights.
 //
-// 16384 tokens, 64 heads of 128 over 8: 4.0 to 4.2 ms, 1.05 to 1.10 PF/s, where a
-// library bf16 product of 8192^3 reaches 1.29: under it the chip's clock falls to some
+// 16384 tokens, 64 heads of 128 over 8: 4.0 to 4.5 ms by card, 0.98 to 1.10 PF/s, where a
+// library bf16 product of 8192^3 reaches 1.26 to 1.31: under it the chip's clock falls to some
 // 1.6 GHz, at which the matrix cores are busy 56% of the cycles and the other vector
-// instructions (maxima, exponentials, rounding: 5 to a product) 36%.  Heads of 192:
-// 0.74 PF/s, of 256: 0.67 (256 to 512 registers: one wave per SIMD).  Seven prompts of
+// instructions (maxima, exponentials, rounding: 5 to a product) 36%.  Heads of 192 7.7
+// ms, 0.86 PF/s, of 256 11.9 ms, 0.74 (256 to 512 registers: one wave per SIMD), of 96
+// 3.3 to 3.5 ms, 0.95, of 64 2.4 to 2.5 ms, 0.92.  Seven prompts of
 // 8197 tokens in all, 32 heads: 128 to 142 us by card, 0.65 PF/s: a fifth of the
 // products fall on tiles that are partly masked, starting and ending take 8 us of the
 // 27 that a workgroup lives, and over the last 30 us, the first sequence's rows, half
@@ -404,13 +409,16 @@ __device__ __forceinline__ void leave(const AttnArgs& a, const Grid& g, const Pl
 //
 // Tried and slower (16384 tokens, against 1.05 PF/s on the same card, unless said): the
 // next tile's scores formed between this one's weights, whole tiles (0.87, spills) or
-// halves (0.94; heads of 256 0.75 against 0.67, of 192 0.70 against 0.74: not worth the
-// second form); eight waves in two groups that take turns (1.01); eight waves on 256
+// halves (0.94; heads of 192 0.70 against 0.74 then; of 256 0.75 against 0.67, a second
+// form of the loop for that width alone); eight waves in two groups that take turns
+// (1.01); eight waves on 256
 // rows with three buffers (1.07, but the seven prompts 161 against 144 us).  No change:
 // no barrier before the rows leave, a wave's priority raised for its products, sums in
 // chains.
 constexpr int BM = 128, BK = 64;
 
+// (Heads up to 64: four waves per SIMD; the careful pass alone keeps registers in memory
+// for it.)
 template <int DB>
 __global__ __launch_bounds__(256, DB == 2 ? 4 : DB <= 4 ? 2 : 1) void attention_rows_kernel(AttnArgs a, Grid g) {
   constexpr int RB = 64 * DB, TILE = BK * RB;  // bytes of a row and of a tile
@@ -501,9 +509,9 @@ __global__ __launch_bounds__(256, DB == 2 ? 4 : DB <= 4 ? 2 : 1) void attention_
 // where LDS holds no more) take in turn, each with two buffers of its own, so that
 // none waits for another; their sums meet at the end.  Bound by reading keys and
 // values: 64 sequences of 6001 keys, 64 heads over 8: 265 us, 5.9 TB/s; of 4096 to
-// 8192, 302 us, 5.3 TB/s (a large copy reaches 5.1).  One token over 4096 keys: 11.1 us in 20 splits, of which 2.6 are
-// the launch of the join and 1 each the sequence's search, the first tile's way from
-// memory and each of two tiles.
+// 8192, 302 us, 5.3 TB/s (a large copy reaches 5.1).  One token over 4096 keys: 11.0 us
+// in 20 splits, of which 2.6 are the launch of the join and 1 each the sequence's search,
+// the first tile's way from memory and each of two tiles.
 constexpr int FM = 32, FK = 32;
 constexpr int few_waves(int DB) { return DB <= 4 ? 4 : 2; }
 
@@ -674,10 +682,14 @@ struct Plan {
 };
 
 // Few rows (up to 32 to a sequence): the kernel whose waves share the keys; its
-// splits by the least of a time in us.  One workgroup to a CU reads keys and values
-// at up to 35 GB/s, all together at 5.4 TB/s, and takes 4 us besides: 16 sequences
+// splits by the least of a time in us.  A workgroup is priced at 35 GB/s of keys and
+// values (alone on a CU it reads 39 with heads of 64, 55 of 128, 34 of 256), all
+// together at 5.4 TB/s, and 4 us besides: 16 sequences
 // of 8192 keys, 8 key heads: 135 us in one piece, 105 in two, 112 in four; 24: 157
-// in one, 162 in four; one sequence of 4096: 44 us in one piece, 11.9 in 16.
+// in one, 162 in four; one sequence of 4096, one key head: 43 us in one piece, 11.2 in
+// 16.  Over 221 calls of 1 to 128 sequences, 1 or 8 key heads and 256 to 16384 keys what
+// it chooses takes 6% longer than the best number of splits on average (with heads of
+// 128 2.5%); prices fitted to each width gave 4%.
 // More rows: the same, of a tile's 64 keys at a time.  A workgroup that has a CU to
 // itself takes 0.87 us for them with heads of 64, 1.09 of 128, 3.2 of 256; two on a CU
 // take 1.7 times as long each (past some 128 workgroups some CUs have two; with heads

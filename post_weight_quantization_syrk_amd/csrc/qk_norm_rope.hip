@@ -7,7 +7,8 @@
 //
 // Bound by memory: each value is read once and written once.  16384 tokens of 64 + 8
 // + 8 heads of 128, bf16, take 128 us, 5.2 TB/s (a large copy reaches 5.1); 4096
-// tokens of 48 heads 19.7 us, 5.1 TB/s; one token 4.3 us, a launch and its loads.
+// tokens of 48 heads 23.7 us, 4.3 TB/s (19.7 where the last-level cache has the inputs);
+// one token 3.9 us, a launch and its loads.
 // A head's columns are taken as units of 8, two units per lane, such that both
 // columns of every pair are in one lane: no value crosses lanes but the sum of
 // squares.  A wave takes a token, or a part of its heads, with the next heads' loads

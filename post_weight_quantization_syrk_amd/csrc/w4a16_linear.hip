@@ -13,7 +13,7 @@
 // direct loads, up to three ahead.  Eight bits first (`Wide`) for many rows: a wave has
 // 64 weight rows, and two codes become bf16 with one operation.
 //
-// 8192 tokens through 57344 x 8192, groups of 128, gated, SiLU: 6.9 ms, 1.12 PF/s, of
+// 8192 tokens through 57344 x 8192, groups of 128, gated, SiLU: 6.8 to 7.3 ms by card, 1.06 to 1.13 PF/s, of
 // which 0.15 ms make the weights wide; a library bf16 product of 8192^3 reaches 1.29.
 // The clock falls to some 1.65 GHz there (power), at which the matrix cores are busy
 // 61% of the cycles.  515 tokens through 4099 x 11008, groups of 32: 91 to 99 us by
