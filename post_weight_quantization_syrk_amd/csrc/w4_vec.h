@@ -299,20 +299,26 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
       }
     }
   };
-  // Aligned where the rows are; else at any address (31 tokens through 25020 x 5216,
-  // groups of 32, gated, 58 us, with 2 bytes a load 85; 16 through 8192 x 11040 20.8
-  // and 26.5), one by one where the matrix has fewer than a piece.
+  // Aligned where the rows are; else, for bf16 tokens, at any address with groups of 32
+  // (31 tokens through 25020 x 5216, gated, 58 us, with 2 bytes a load 85; 16 through 8192
+  // x 11040 20.8 and 26.5) or many weight rows (15 tokens, groups of 64: 9700 x 5440 16%
+  // less than 2 bytes a load, 5500 x 5440 4%, 4100 x 2752 7% more; of 128: 9700 x 5504 10%
+  // less, 4100 x 2432 2% more).  One by one otherwise, and for int8 tokens (15 tokens, groups
+  // of 64, 11436 x 5440: 11.1 us, at any address 11.8; 2684 x 5440 6.9 and 8.3).
   auto scales = [&](int b) __attribute__((always_inline)) {
     constexpr std::false_type aligned{};
     if constexpr (G != 0) {
-      if (S::GPB >= 8 && a.vec >= 8)
+      if (S::GPB >= 8 && a.vec >= 8) {
         scales_by(b, std::integral_constant<int, S::GPB >= 8 ? 8 : 1>(), aligned);
-      else if (a.vec >= 4)
+      } else if (a.vec >= 4) {
         scales_by(b, std::integral_constant<int, 4>(), aligned);
-      else if ((int64_t)a.n * a.ng >= 8)
-        scales_by(b, std::integral_constant<int, S::GPB >= 8 ? 8 : 4>(), std::true_type());
-      else
+      } else {
+        if constexpr (!I8) {
+          if ((G == 32 || a.n >= 5000) && (int64_t)a.n * a.ng >= 8)
+            return scales_by(b, std::integral_constant<int, S::GPB >= 8 ? 8 : 4>(), std::true_type());
+        }
         scales_by(b, std::integral_constant<int, 1>(), aligned);
+      }
     }
   };
 
