@@ -304,7 +304,7 @@ __global__ __launch_bounds__((64 * RS * Shape<I8, NT, R, G, RS>::SLOTS)) void w4
   // x 11040 20.8 and 26.5) or many weight rows (15 tokens, groups of 64: 9700 x 5440 16%
   // less than 2 bytes a load, 5500 x 5440 4%, 4100 x 2752 7% more; of 128: 9700 x 5504 10%
   // less, 4100 x 2432 2% more).  One by one otherwise, and for int8 tokens (15 tokens, groups
-  // of 64, 11436 x 5440: 11.1 us, at any address 11.8; 2684 x 5440 6.9 and 8.3).
+  // of 64, 11436 x 5440: 11.1 us, at any address 11.8; 2684 x 5440 7.4 and 8.3).
   auto scales = [&](int b) __attribute__((always_inline)) {
     constexpr std::false_type aligned{};
     if constexpr (G != 0) {
